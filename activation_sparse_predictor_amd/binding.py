@@ -38,12 +38,33 @@ PI_DETERMINISTIC = 0x4
 PI_CHECK_IDX = 0x8
 PI_NOALLOC_SCRATCH_BYTES = 4 << 20   # the static scratch of pi_ffn_decode_noalloc, per GPU
 
+PI_KV_INT8 = 0
+PI_KV_FP8 = 1
+PI_KV_MAX_SEQ = 1024
+
+KV_FMTS = {"int8": PI_KV_INT8, "fp8": PI_KV_FP8}
 KINDS = {"relu": PI_FFN_RELU, "reglu": PI_FFN_REGLU, "swiglu": PI_FFN_SWIGLU}
 ACTS = {"relu": PI_ACT_RELU, "none": PI_ACT_NONE}
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+
+
+class KvCache(ctypes.Structure):
+    """pi_kv_cache: the pointers are device addresses."""
+    _fields_ = [("fmt", _I), ("n_pages", _I), ("n_kv", _I), ("page", _I), ("d", _I),
+                ("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P)]
+
+
+class KvBatch(ctypes.Structure):
+    """pi_kv_batch: the pointers are device addresses."""
+    _fields_ = [("n_seq", _I), ("n_tok", _I), ("max_q", _I), ("table_stride", _I),
+                ("q_start", _P), ("ctx", _P), ("table", _P)]
+
+
+_KC = ctypes.POINTER(KvCache)
+_KB = ctypes.POINTER(KvBatch)
 
 _SIGNATURES = {
     "pi_ffn_predict": (_I, [_P, _I, _I, _P, _P, _I, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
@@ -64,6 +85,10 @@ _SIGNATURES = {
     "pi_quantize_rows": (_I, [_P, _I, _I, _P, _P, _P]),
     "pi_ffn_sparse_q4": (_I, [_I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_uint32,
                               _P, _SZ, _P]),
+    "pi_kv_append": (_I, [_KC, _KB, _P, ctypes.c_int64, _P, ctypes.c_int64, _P]),
+    "pi_kv_read": (_I, [_KC, _KB, _P, _P, _P]),
+    "pi_kv_attend": (_I, [_KC, _KB, _P, ctypes.c_int64, _I, ctypes.c_float, _I, _P, _P, _P, _SZ, _P]),
+    "pi_kv_workspace_size": (_I, [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "pi_profile": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
     "pi_reorder": (_I, [_P, _I, ctypes.c_double, _P, _P]),
     "pi_permute_rows": (_I, [_P, _P, _I, _I, _P, _P]),
@@ -205,6 +230,27 @@ def pi_ffn_decode_noalloc(kind, x, B, d, ffn, P1, b1, act, P2, b2, r, tau, W_up,
     return load().pi_ffn_decode_noalloc(kind, _ptr(x), B, d, ffn, _ptr(P1), _ptr(b1), act, _ptr(P2), _ptr(b2), r,
                                         tau, _ptr(W_up), _ptr(b_up), _ptr(W_gate), _ptr(b_gate), _ptr(W_down),
                                         _ptr(idx), _ptr(count), _ptr(y), flags, _stream(stream))
+
+
+def pi_kv_append(cache, batch, k, k_stride, v, v_stride, stream=None) -> int:
+    """cache: KvCache, batch: KvBatch (or None, which the library rejects)."""
+    return load().pi_kv_append(cache, batch, _ptr(k), k_stride, _ptr(v), v_stride, _stream(stream))
+
+
+def pi_kv_read(cache, batch, k, v, stream=None) -> int:
+    return load().pi_kv_read(cache, batch, _ptr(k), _ptr(v), _stream(stream))
+
+
+def pi_kv_attend(cache, batch, q, q_stride, n_head, scale, window, y, lse, ws, ws_bytes, stream=None) -> int:
+    return load().pi_kv_attend(cache, batch, _ptr(q), q_stride, n_head, scale, window, _ptr(y), _ptr(lse), _ptr(ws),
+                               ws_bytes, _stream(stream))
+
+
+def pi_kv_workspace_size(n_seq, n_tok, max_q, n_head, n_kv, d) -> int:
+    out = _SZ(0)
+    check(load().pi_kv_workspace_size(n_seq, n_tok, max_q, n_head, n_kv, d, ctypes.byref(out)),
+          "pi_kv_workspace_size")
+    return out.value
 
 
 def pi_profile(X, n, d, ffn, W_fire, b_fire, counts, ws=None, ws_bytes=0, stream=None) -> int:

@@ -210,6 +210,70 @@ pi_status check_sparse_args(int kind, const pi_half* x, int B, int d, int ffn, c
 }
 
 
+// ---- the 8-bit paged cache
+constexpr int kOpKvAttend = 100;   // workspace layouts beside pi_op's
+
+size_t kv_ws_bytes(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d) {
+    return pi::kSyncBytes + pi::kv_attend_bytes(n_seq, n_tok, max_q, n_head, n_kv, d);
+}
+
+pi_status check_heads(int n_head, int n_kv) {
+    PI_REQUIRE(n_head >= 1 && n_head <= PI_KV_MAX_HEADS, PI_ERR_INVALID_ARG, "n_head=%d outside [1, %d]", n_head,
+               PI_KV_MAX_HEADS);
+    PI_REQUIRE(n_head % n_kv == 0, PI_ERR_INVALID_ARG, "n_head=%d is not a multiple of n_kv=%d", n_head, n_kv);
+    return PI_OK;
+}
+
+pi_status check_kv_counts(int n_seq, int n_tok, int max_q) {
+    PI_REQUIRE(n_seq >= 1 && n_seq <= PI_KV_MAX_SEQ, PI_ERR_INVALID_ARG, "n_seq=%d outside [1, %d]", n_seq,
+               PI_KV_MAX_SEQ);
+    PI_REQUIRE(n_tok >= 1 && n_tok <= PI_KV_MAX_TOKENS, PI_ERR_INVALID_ARG, "n_tok=%d outside [1, %d]", n_tok,
+               PI_KV_MAX_TOKENS);
+    PI_REQUIRE(max_q >= 1 && max_q <= n_tok, PI_ERR_INVALID_ARG, "max_q=%d outside [1, n_tok=%d]", max_q, n_tok);
+    return PI_OK;
+}
+
+pi_status check_kv_d(int d) {
+    PI_REQUIRE(d >= 1, PI_ERR_INVALID_ARG, "d=%d must be positive", d);
+    PI_REQUIRE(d % 16 == 0 && d <= PI_KV_MAX_D, PI_ERR_UNSUPPORTED, "d=%d is not a multiple of 16 up to %d", d,
+               PI_KV_MAX_D);
+    return PI_OK;
+}
+
+pi_status check_stride(int64_t stride, int64_t row, const char* name) {
+    PI_REQUIRE(stride >= row, PI_ERR_INVALID_ARG, "%s=%lld is below a row's %lld elements", name, (long long)stride,
+               (long long)row);
+    PI_REQUIRE(stride % 8 == 0, PI_ERR_UNSUPPORTED, "%s=%lld is not a multiple of 8", name, (long long)stride);
+    PI_REQUIRE(stride <= (int64_t)1 << 40, PI_ERR_INVALID_ARG, "%s=%lld out of range", name, (long long)stride);
+    return PI_OK;
+}
+
+// The descriptors, checked and turned into the kernels' own.
+pi_status check_kv(const pi_kv_cache* c, const pi_kv_batch* b, pi::KvCache* kc, pi::KvBatch* kb) {
+    PI_REQUIRE(c != nullptr && b != nullptr, PI_ERR_INVALID_ARG, "cache or batch is NULL");
+    PI_REQUIRE(c->fmt == PI_KV_INT8 || c->fmt == PI_KV_FP8, PI_ERR_INVALID_ARG, "fmt=%d unknown", c->fmt);
+    PI_REQUIRE(c->n_pages >= 1, PI_ERR_INVALID_ARG, "n_pages=%d must be positive", c->n_pages);
+    PI_REQUIRE(c->n_kv >= 1 && c->n_kv <= PI_KV_MAX_HEADS, PI_ERR_INVALID_ARG, "n_kv=%d outside [1, %d]", c->n_kv,
+               PI_KV_MAX_HEADS);
+    PI_REQUIRE(c->page >= 1, PI_ERR_INVALID_ARG, "page=%d must be positive", c->page);
+    PI_REQUIRE(c->page >= 16 && c->page <= PI_KV_MAX_PAGE && (c->page & (c->page - 1)) == 0, PI_ERR_UNSUPPORTED,
+               "page=%d is not 16, 32, 64, 128 or 256", c->page);
+    PI_TRY(check_kv_d(c->d));
+    PI_TRY(check_half(reinterpret_cast<const pi_half*>(c->k), "cache k", true));
+    PI_TRY(check_half(reinterpret_cast<const pi_half*>(c->v), "cache v", true));
+    PI_TRY(check_word(c->k_scale, "k_scale", true));
+    PI_TRY(check_word(c->v_scale, "v_scale", true));
+    PI_TRY(check_kv_counts(b->n_seq, b->n_tok, b->max_q));
+    PI_REQUIRE(b->table_stride >= 1 && (int64_t)b->table_stride * c->page <= INT32_MAX / 2, PI_ERR_INVALID_ARG,
+               "table_stride=%d out of range", b->table_stride);
+    PI_TRY(check_word(b->q_start, "q_start", true));
+    PI_TRY(check_word(b->ctx, "ctx", true));
+    PI_TRY(check_word(b->table, "table", true));
+    *kc = pi::KvCache{c->fmt, c->n_pages, c->n_kv, c->page, c->d, c->k, c->v, c->k_scale, c->v_scale};
+    *kb = pi::KvBatch{b->n_seq, b->n_tok, b->max_q, b->table_stride, c->page, b->q_start, b->ctx, b->table};
+    return PI_OK;
+}
+
 // The calls proper, on a checked workspace: hdr is its synchronisation header,
 // data the call's data area; clear: zero the tagged words first (single-token
 // paths only).
@@ -696,6 +760,72 @@ pi_status pi_ffn_sparse_q4(int kind, const pi_half* x, int B, int d, int ffn, co
                                      reinterpret_cast<const pi::h16*>(s_gate), b_gate, q_down,
                                      reinterpret_cast<const pi::h16*>(s_down), idx, count, y, L, data, st);
     if (e != hipSuccess) return hip_fail(e, "pi_ffn_sparse_q4");
+    return ok();
+}
+
+pi_status pi_kv_append(const pi_kv_cache* cache, const pi_kv_batch* batch, const pi_half* k, int64_t k_stride,
+                       const pi_half* v, int64_t v_stride, void* stream) {
+    pi::KvCache c;
+    pi::KvBatch b;
+    PI_TRY(check_kv(cache, batch, &c, &b));
+    PI_TRY(check_half(k, "k", true));
+    PI_TRY(check_half(v, "v", true));
+    PI_TRY(check_stride(k_stride, (int64_t)c.n_kv * c.d, "k_stride"));
+    PI_TRY(check_stride(v_stride, (int64_t)c.n_kv * c.d, "v_stride"));
+    hipError_t e = pi::launch_kv_append(c, b, reinterpret_cast<const pi::h16*>(k), k_stride,
+                                        reinterpret_cast<const pi::h16*>(v), v_stride, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "pi_kv_append");
+    return ok();
+}
+
+pi_status pi_kv_read(const pi_kv_cache* cache, const pi_kv_batch* batch, pi_half* k, pi_half* v, void* stream) {
+    pi::KvCache c;
+    pi::KvBatch b;
+    PI_TRY(check_kv(cache, batch, &c, &b));
+    PI_TRY(check_half(k, "k", true));
+    PI_TRY(check_half(v, "v", true));
+    hipError_t e = pi::launch_kv_read(c, b, reinterpret_cast<pi::h16*>(k), reinterpret_cast<pi::h16*>(v),
+                                      static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "pi_kv_read");
+    return ok();
+}
+
+pi_status pi_kv_attend(const pi_kv_cache* cache, const pi_kv_batch* batch, const pi_half* q, int64_t q_stride,
+                       int n_head, float scale, int window, pi_half* y, float* lse, void* ws, size_t ws_bytes,
+                       void* stream) {
+    pi::KvCache c;
+    pi::KvBatch b;
+    PI_TRY(check_kv(cache, batch, &c, &b));
+    PI_TRY(check_heads(n_head, c.n_kv));
+    PI_REQUIRE(std::isfinite(scale), PI_ERR_INVALID_ARG, "scale is not finite");
+    PI_REQUIRE(window >= 0, PI_ERR_INVALID_ARG, "window=%d is negative", window);
+    PI_TRY(check_half(q, "q", true));
+    PI_TRY(check_stride(q_stride, (int64_t)n_head * c.d, "q_stride"));
+    PI_TRY(check_half(y, "y", true));
+    PI_TRY(check_word(lse, "lse", false));
+    PI_TRY(check_ws(ws, ws_bytes, kv_ws_bytes(b.n_seq, b.n_tok, b.max_q, n_head, c.n_kv, c.d), "pi_kv_attend"));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char* data = static_cast<char*>(ws) + pi::kSyncBytes;
+    // one key for every shape: the counters have one place, and each call leaves them zero
+    const LayoutKey key{kOpKvAttend, 0, 0, 0, 0};
+    hipError_t e = hipSuccess;
+    if (ws_needs_clear(ws, key)) e = pi::launch_zero(data, pi::kv_attend_zero_bytes(), s);
+    if (e == hipSuccess)
+        e = pi::launch_kv_attend(c, b, reinterpret_cast<const pi::h16*>(q), q_stride, n_head, scale, window,
+                                 reinterpret_cast<pi::h16*>(y), lse, data, s);
+    if (e != hipSuccess) return hip_fail(e, "pi_kv_attend");
+    ws_record(ws, key);
+    return ok();
+}
+
+pi_status pi_kv_workspace_size(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d, size_t* bytes) {
+    PI_REQUIRE(bytes != nullptr, PI_ERR_INVALID_ARG, "bytes is NULL");
+    PI_REQUIRE(n_kv >= 1 && n_kv <= PI_KV_MAX_HEADS, PI_ERR_INVALID_ARG, "n_kv=%d outside [1, %d]", n_kv,
+               PI_KV_MAX_HEADS);
+    PI_TRY(check_heads(n_head, n_kv));
+    PI_TRY(check_kv_counts(n_seq, n_tok, max_q));
+    PI_TRY(check_kv_d(d));
+    *bytes = kv_ws_bytes(n_seq, n_tok, max_q, n_head, n_kv, d);
     return ok();
 }
 

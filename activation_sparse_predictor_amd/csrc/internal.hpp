@@ -292,6 +292,28 @@ hipError_t launch_ffn_q4(int kind, bool dense, const h16* x, int B, int d, int f
                          const uint8_t* qd, const h16* sd, const int32_t* idx, const int32_t* count, float* y,
                          const SparseLayout& L, char* data, hipStream_t s);
 
+// ---- the 8-bit paged cache: the C ABI's descriptors with device-side types
+struct KvCache {
+    int fmt, n_pages, n_kv, page, d;
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+};
+struct KvBatch {
+    int n_seq, n_tok, max_q, table_stride, page;   // page: the cache's
+    const int32_t *q_start, *ctx, *table;
+};
+
+// kv.hip
+hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const h16* k, long long k_stride, const h16* v,
+                            long long v_stride, hipStream_t s);
+hipError_t launch_kv_read(const KvCache& c, const KvBatch& b, h16* k, h16* v, hipStream_t s);
+
+// attend.hip
+size_t kv_attend_bytes(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d);
+size_t kv_attend_zero_bytes();   // at the data area's start: counters, all zero between calls
+hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
+                            float scale, int window, h16* y, float* lse, char* data, hipStream_t s);
+
 // profile.hip
 hipError_t launch_profile(const h16* X, int n, int d, int ffn, const h16* W, const float* b,
                           uint32_t* counts, hipStream_t s);

@@ -1,0 +1,126 @@
+// Device helpers of the 8-bit paged cache (kv.hip, attend.hip): code formats,
+// byte order, and where a call's tokens lie.
+#pragma once
+
+#include "common.hpp"
+#include "internal.hpp"
+
+namespace pi {
+
+// A page's bytes come in granules of 16 tokens, 16 d bytes for K and for V.
+constexpr int kGran = 16;
+
+// Byte of (token t, dimension i) inside a page and head.
+__device__ __forceinline__ int k_byte(int t, int i, int d) {
+    return (t >> 2) * 4 * d + (i >> 4) * 64 + (t & 3) * 16 + (i & 15);
+}
+__device__ __forceinline__ int v_byte(int t, int i, int d) { return (t >> 4) * 16 * d + i * 16 + (t & 15); }
+
+// First byte of a page and head; pages * heads * bytes pass 32 bits.
+__device__ __forceinline__ size_t page_base(const KvCache& c, int id, int h) {
+    return ((size_t)id * c.n_kv + h) * (size_t)(c.page * c.d);
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
+
+template <int FMT> struct Codes;
+
+// int8: byte = code + 128.
+template <> struct Codes<0> {
+    static constexpr float kMax = 127.f;
+    static constexpr uint32_t kZero4 = 0x80808080u;   // four zero codes
+    // Four codes as fp16, exactly: each byte beneath 0x64 is the fp16 number
+    // 1024 + byte, and 1024 + byte - 1152 = code.
+    static __device__ __forceinline__ void to_f16(uint32_t w, f16x2& a, f16x2& b) {
+        const f16x2 off = {(f16)1152.0f, (f16)1152.0f};
+        a = as_h2(__builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) - off;
+        b = as_h2(__builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) - off;
+    }
+    static __device__ __forceinline__ float value(uint32_t byte) { return (float)((int)(byte & 0xFFu) - 128); }
+    // round(clamp(x, -127, 127)) of two numbers as two bytes (rintf: ties to even)
+    static __device__ __forceinline__ uint32_t encode2(float x, float y) {
+        const int a = (int)rintf(fminf(fmaxf(x, -kMax), kMax)) + 128;
+        const int b = (int)rintf(fminf(fmaxf(y, -kMax), kMax)) + 128;
+        return (uint32_t)a | ((uint32_t)b << 8);
+    }
+};
+
+// fp8: the byte is the OCP e4m3 number; the conversions round to nearest even.
+template <> struct Codes<1> {
+    static constexpr float kMax = 448.f;
+    static constexpr uint32_t kZero4 = 0u;
+    static __device__ __forceinline__ void to_f16(uint32_t w, f16x2& a, f16x2& b) {
+        a = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+        b = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
+    }
+    static __device__ __forceinline__ float value(uint32_t byte) {
+        return (float)__builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(byte & 0xFFu, 1.0f, false)).x;
+    }
+    static __device__ __forceinline__ uint32_t encode2(float x, float y) {
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(fminf(fmaxf(x, -kMax), kMax), fminf(fmaxf(y, -kMax), kMax), 0,
+                                                         false) & 0xFFFFu;
+    }
+};
+
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    return Codes<FMT>::encode2(a, b) | (Codes<FMT>::encode2(c, d) << 16);
+}
+
+// A sequence of the batch, with everything read from the device clamped so
+// that no row and no table entry outside the arrays can follow from it.
+struct Seq {
+    int s, row0, n, ctx;   // its index, first row, rows and length
+};
+__device__ __forceinline__ Seq kv_seq(const KvBatch& b, int s) {
+    const int a = b.q_start[s], e = b.q_start[s + 1], c = b.ctx[s];
+    Seq q;
+    q.s = s;
+    q.row0 = a < 0 ? 0 : (a > b.n_tok ? b.n_tok : a);
+    const int end = e > b.n_tok ? b.n_tok : e;
+    q.n = end > q.row0 ? end - q.row0 : 0;
+    const int cap = b.table_stride * b.page;
+    q.ctx = c < 0 ? 0 : (c > cap ? cap : c);
+    return q;
+}
+
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int v) {
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+        const int o = __shfl_up(v, off, kWave);
+        if (lane_id() >= off) v += o;
+    }
+    return v;
+}
+
+// The sequence that item `item` of a list of count(seq) items per sequence
+// belongs to, and the item's number inside it (wave-uniform; s = -1 past the
+// list's end).  Every lane takes one sequence a round.
+template <class F>
+__device__ __forceinline__ Seq find_seq(const KvBatch& b, int item, int& inside, F count) {
+    Seq none{-1, 0, 0, 0};
+    int before = 0;
+    for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
+        const int s = s0 + lane_id();
+        const Seq q = s < b.n_seq ? kv_seq(b, s) : Seq{-1, 0, 0, 0};
+        const int n = s < b.n_seq ? count(q) : 0;
+        const int upto = before + wave_scan(n);
+        const uint64_t hit = __ballot(upto > item);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            Seq r;
+            r.s = s0 + l;
+            r.row0 = __builtin_amdgcn_readlane(q.row0, l);
+            r.n = __builtin_amdgcn_readlane(q.n, l);
+            r.ctx = __builtin_amdgcn_readlane(q.ctx, l);
+            inside = item - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
+            return r;
+        }
+        before = __builtin_amdgcn_readlane(upto, kWave - 1);
+    }
+    inside = 0;
+    return none;
+}
+
+}  // namespace pi

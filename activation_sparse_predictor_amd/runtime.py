@@ -264,6 +264,177 @@ def decode_hot_end(layer: dict, x: torch.Tensor, n_hot: int, idx: torch.Tensor, 
     return y
 
 
+# ---- the 8-bit paged cache.  A cache is a dict of device tensors named as in
+# the C ABI (k and v: n_pages x n_kv x page x d bytes in the library's order,
+# k_scale and v_scale: n_pages x n_kv floats) plus fmt ("int8" or "fp8"); a
+# batch is a dict of the device arrays q_start, ctx and table (int32) plus the
+# host's n_tok and max_q.
+
+
+def kv_cache(n_pages: int, n_kv: int, d: int, page: int = 16, fmt: str = "int8", device="cuda") -> dict:
+    """An empty cache.  Its memory is not initialised: no slot is read before it is written."""
+    def bytes_():
+        return torch.empty(n_pages, n_kv, page, d, dtype=torch.uint8, device=device)
+
+    def scales():
+        return torch.empty(n_pages, n_kv, dtype=torch.float32, device=device)
+
+    return {"fmt": fmt, "k": bytes_(), "v": bytes_(), "k_scale": scales(), "v_scale": scales()}
+
+
+def kv_batch(new, ctx, table, device="cuda") -> dict:
+    """A batch from host lists: new[s] rows of the call for sequence s, ctx[s]
+    its length with them, table[s] its page ids (rows may differ in length)."""
+    start = [0]
+    for n in new:
+        start.append(start[-1] + int(n))
+    width = max(1, max(len(r) for r in table))
+    rows = [list(r) + [-1] * (width - len(r)) for r in table]
+
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32, device=device)
+
+    return {"q_start": ints(start), "ctx": ints(list(ctx)), "table": ints(rows), "n_tok": start[-1],
+            "max_q": max(int(n) for n in new)}
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _kv_args(cache: dict, batch: dict, device):
+    """The C descriptors of a cache and a batch on `device`."""
+    k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
+    start, ctx, table = batch["q_start"], batch["ctx"], batch["table"]
+    _need(cache["fmt"] in B.KV_FMTS, "cache fmt must be 'int8' or 'fp8'")
+    _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype == torch.uint8,
+          "cache k and v must be n_pages x n_kv x page x d bytes")
+    _need(ks.shape == vs.shape == k.shape[:2] and ks.dtype == vs.dtype == torch.float32,
+          "cache scales must be n_pages x n_kv floats")
+    n_seq = ctx.shape[0]
+    _need(ctx.dim() == 1 and start.shape == (n_seq + 1,) and table.dim() == 2 and table.shape[0] == n_seq,
+          "batch arrays must be q_start (n_seq + 1), ctx (n_seq) and table (n_seq x pages)")
+    _need(start.dtype == ctx.dtype == table.dtype == torch.int32, "batch arrays must be int32")
+    for t in (k, v, ks, vs, start, ctx, table):
+        _need(t.is_contiguous() and t.device == device, "cache and batch tensors must be contiguous and on one device")
+    n_pages, n_kv, page, d = k.shape
+    return (B.KvCache(B.KV_FMTS[cache["fmt"]], n_pages, n_kv, page, d, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
+                      vs.data_ptr()),
+            B.KvBatch(n_seq, batch["n_tok"], batch["max_q"], table.shape[1], start.data_ptr(), ctx.data_ptr(),
+                      table.data_ptr()))
+
+
+def _kv_rows(t: torch.Tensor, n_tok: int, heads: Optional[int], d: int, name: str, stride: bool = True) -> int:
+    """Checks n_tok x heads x d fp16 rows; returns the elements between tokens."""
+    _need(t.dtype == torch.float16 and t.dim() == 3 and t.shape[0] == n_tok and t.shape[2] == d
+          and (heads is None or t.shape[1] == heads), f"{name} must be fp16, n_tok x heads x d")
+    heads = t.shape[1]
+    _need((t.stride(2) == 1 or d == 1) and (t.stride(1) == d or heads == 1) and (stride or t.is_contiguous()),
+          f"{name}: the heads of a token must be contiguous" if stride else f"{name} must be contiguous")
+    return t.stride(0) if n_tok > 1 else heads * d
+
+
+def _elsewhere(stream, device, tensors, call):
+    """call() on another stream or device than the current ones: what it
+    allocates belongs to that stream, and the caller's tensors are not reused
+    by the allocator before that stream is done with them."""
+    with torch.cuda.device(device):
+        if stream is None:
+            st = torch.cuda.current_stream(device)
+        elif isinstance(stream, int):
+            st = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+        else:
+            st = stream
+        with torch.cuda.stream(st):
+            out = call()
+        for t in tensors:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(st)
+        return out
+
+
+def _is_elsewhere(stream, device) -> bool:
+    _need(device.type == "cuda", "tensors must be on the GPU")
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, batch: dict, stream=None) -> None:
+    """pi_kv_append: quantises k and v (n_tok x n_kv x d fp16, tokens any
+    multiple of 8 elements apart) into the batch's places of the cache."""
+    if _is_elsewhere(stream, k.device):
+        return _elsewhere(stream, k.device, (k, v, *cache.values(), *batch.values()),
+                          lambda: kv_append(cache, k, v, batch))
+    c, b = _kv_args(cache, batch, k.device)
+    ks = _kv_rows(k, b.n_tok, c.n_kv, c.d, "k")
+    vs = _kv_rows(v, b.n_tok, c.n_kv, c.d, "v")
+    _need(v.device == k.device, "k and v must be on one device")
+    B.check(B.pi_kv_append(c, b, k, ks, v, vs), "pi_kv_append")
+
+
+def kv_read(cache: dict, batch: dict, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """pi_kv_read: the stored keys and values of the batch's tokens (n_tok x n_kv x d fp16)."""
+    dev = cache["k"].device
+    if _is_elsewhere(stream, dev):
+        return _elsewhere(stream, dev, (k, v, *cache.values(), *batch.values()), lambda: kv_read(cache, batch, k, v))
+    c, b = _kv_args(cache, batch, dev)
+    if k is None:
+        k = torch.empty(b.n_tok, c.n_kv, c.d, dtype=torch.float16, device=dev)
+    if v is None:
+        v = torch.empty(b.n_tok, c.n_kv, c.d, dtype=torch.float16, device=dev)
+    for t, name in ((k, "k"), (v, "v")):
+        _kv_rows(t, b.n_tok, c.n_kv, c.d, name, stride=False)
+        _need(t.device == dev, "k and v must be on the cache's device")
+    B.check(B.pi_kv_read(c, b, k, v), "pi_kv_read")
+    return k, v
+
+
+_KV_WS: Dict[Tuple[int, int], Workspace] = {}
+
+
+def kv_workspace(n_seq: int, n_tok: int, max_q: int, n_head: int, n_kv: int, d: int, device="cuda") -> torch.Tensor:
+    """A fresh zero-filled workspace for kv_attend, for callers that keep their own."""
+    nbytes = B.pi_kv_workspace_size(n_seq, n_tok, max_q, n_head, n_kv, d)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def kv_attend(cache: dict, q: torch.Tensor, batch: dict, y: Optional[torch.Tensor] = None,
+              scale: Optional[float] = None, window: int = 0, lse: Optional[torch.Tensor] = None,
+              ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pi_kv_attend: attention of q (n_tok x n_head x d fp16, tokens any multiple
+    of 8 elements apart) over the cache; scale defaults to 1 / sqrt(d), window 0
+    is none, lse (n_tok x n_head floats) is filled if given.  Without ws, each
+    stream has a workspace of its own."""
+    if _is_elsewhere(stream, q.device):
+        return _elsewhere(stream, q.device, (q, y, lse, ws, *cache.values(), *batch.values()),
+                          lambda: kv_attend(cache, q, batch, y, scale, window, lse, ws))
+    dev = q.device
+    c, b = _kv_args(cache, batch, dev)
+    qs = _kv_rows(q, b.n_tok, None, c.d, "q")
+    heads = q.shape[1]
+    if y is None:
+        y = torch.empty(b.n_tok, heads, c.d, dtype=torch.float16, device=dev)
+    else:
+        _kv_rows(y, b.n_tok, heads, c.d, "y", stride=False)
+        _need(y.device == dev, "y must be on q's device")
+    if lse is not None:
+        _need(lse.shape == (b.n_tok, heads) and lse.dtype == torch.float32 and lse.is_contiguous()
+              and lse.device == dev, "lse must be n_tok x n_head floats")
+    st = torch.cuda.current_stream().cuda_stream
+    if ws is None:
+        key = (dev.index, st)
+        if key not in _KV_WS:
+            _KV_WS[key] = Workspace(dev)
+        ws, wsb = _KV_WS[key].get(B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, c.d))
+    else:
+        _need(ws.device == dev and ws.is_contiguous(), "ws must be contiguous and on q's device")
+        wsb = ws.numel() * ws.element_size()
+    B.check(B.pi_kv_attend(c, b, q, qs, heads, c.d ** -0.5 if scale is None else float(scale), int(window), y, lse, ws,
+                           wsb, st), "pi_kv_attend")
+    return y
+
+
 def profile(X: torch.Tensor, W_fire: torch.Tensor, b_fire: Optional[torch.Tensor],
             counts: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     n, d = X.shape

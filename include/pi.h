@@ -442,6 +442,143 @@ pi_status pi_reorder(const uint32_t* counts, int ffn, double hot_share,
 pi_status pi_permute_rows(const void* src, void* dst, int rows, int row_bytes,
                           const int32_t* perm, void* stream);
 
+/*
+ * ---- Attention over an 8-bit paged cache ------------------------------------
+ *
+ * The attention half of a decoder layer, beside the sparse FFN: keys and
+ * values of the tokens so far are quantised to 8 bits as they are written
+ * (pi_kv_append), attention reads the codes directly (pi_kv_attend), and
+ * pi_kv_read gives the stored values back as fp16.
+ *
+ * The cache.  A page is a block of `page` tokens of all n_kv heads, with one
+ * fp32 scale per page and head for K and one for V.  A stored value is
+ * code * scale:
+ *   PI_KV_INT8  byte = code + 128, code in [-127, 127]         QMAX = 127
+ *   PI_KV_FP8   byte = the OCP e4m3 number (no infinities)     QMAX = 448
+ * k and v hold n_pages * n_kv * page * d bytes each, k_scale and v_scale
+ * n_pages * n_kv floats.  Inside a page and head, the byte of token t and
+ * dimension i is at
+ *   K: (t / 4) * 4 d + (i / 16) * 64 + (t % 4) * 16 + i % 16
+ *   V: (t / 16) * 16 d + i * 16 + t % 16
+ * so that one wave's loads are contiguous and become matrix operands without
+ * a shuffle.  Nothing has to be initialised: a page's old contents are never
+ * read before its first token is written.
+ *
+ * The batch.  n_seq sequences; sequence s holds ctx[s] tokens, its own new
+ * ones included, and its call's tokens are rows q_start[s] .. q_start[s + 1] - 1
+ * of the call's tensors (q_start[0] = 0, ascending, q_start[n_seq] = n_tok).
+ * They are its newest: with n = q_start[s + 1] - q_start[s], its token i is at
+ * position ctx[s] - n + i; a token whose position is negative has no place in
+ * the cache (an unused slot of a batch: nothing is written for it, it reads as
+ * zeros, and its attention output is 0).  Position p of sequence s is in page
+ * table[s * table_stride + p / page]; entries past the last position are not
+ * read.  max_q is an upper bound of every n: n above it is unspecified.
+ * Lengths stay on the device, so a captured graph can be replayed as they
+ * grow.  Broken contents never make a kernel touch memory outside the arrays:
+ * q_start is clamped to [0, n_tok], ctx to [0, table_stride * page], and a page
+ * id outside [0, n_pages) is not written, reads as NaN, and makes the rows
+ * that attend to it NaN.
+ */
+typedef enum pi_kv_fmt {
+    PI_KV_INT8 = 0,
+    PI_KV_FP8 = 1
+} pi_kv_fmt;
+
+#define PI_KV_MAX_SEQ 1024
+#define PI_KV_MAX_HEADS 1024
+#define PI_KV_MAX_D 256
+#define PI_KV_MAX_PAGE 256
+#define PI_KV_MAX_TOKENS (1 << 20)
+
+typedef struct pi_kv_cache {   /* read by the host during the call; k .. v_scale are device pointers */
+    int fmt;                   /* pi_kv_fmt */
+    int n_pages, n_kv;         /* pages in the pool; kv heads, 1 .. PI_KV_MAX_HEADS */
+    int page;                  /* tokens of a page: 16, 32, 64, 128 or 256 */
+    int d;                     /* size of a head: a multiple of 16 up to PI_KV_MAX_D */
+    uint8_t* k;                /* 16-byte aligned */
+    uint8_t* v;                /* 16-byte aligned */
+    float* k_scale;
+    float* v_scale;
+} pi_kv_cache;
+
+typedef struct pi_kv_batch {   /* read by the host during the call; the arrays are on the device */
+    int n_seq;                 /* 1 .. PI_KV_MAX_SEQ */
+    int n_tok;                 /* rows of the call's tensors, 1 .. PI_KV_MAX_TOKENS */
+    int max_q;                 /* 1 .. n_tok */
+    int table_stride;          /* entries of a sequence's row of the table, >= 1 */
+    const int32_t* q_start;    /* n_seq + 1 */
+    const int32_t* ctx;        /* n_seq */
+    const int32_t* table;      /* n_seq x table_stride */
+} pi_kv_batch;
+
+/*
+ * pi_kv_append -- quantise the call's keys and values into the cache.
+ *
+ * k and v: n_tok x n_kv x d, the heads of a token contiguous, tokens k_stride
+ * and v_stride elements apart (so slices of one projection's output can be
+ * passed).  For every block (page) that gets new tokens, per head, K and V
+ * apart, with N the new tokens and O the block's older ones:
+ *   m = max |x| over N;  s0 = the block's scale, 0 if O is empty
+ *   s = max(s0, m / QMAX)
+ *   if s > s0, the codes of O become round(code * (s0 / s))
+ *   the codes of N are round(clamp(x / s, -QMAX, QMAX)), 0 if s = 0
+ * in fp32, round = to nearest, ties to even (to an integer, or to e4m3).  So a
+ * block's scale only grows while it fills, older codes are rounded again when
+ * it does, and what a block holds depends on how its tokens were grouped into
+ * calls.  An x that is not finite cannot be held: it makes the block's scale
+ * NaN (the new codes 0) until a call writes the block from its first token
+ * again, so that such a block reads as NaN and cannot pass as a result.
+ * One page must not be in use by two sequences that append to it.
+ *
+ * Errors (all three calls): INVALID_ARG for NULL pointers, an unknown fmt,
+ * counts out of range, n_head not a multiple of n_kv, a negative window, a
+ * stride below a row; UNSUPPORTED for a page size or d not listed, a stride
+ * not a multiple of 8, or misalignment (fp16 tensors, k and v 16 bytes, the
+ * others 4).
+ */
+pi_status pi_kv_append(const pi_kv_cache* cache, const pi_kv_batch* batch,
+                       const pi_half* k, int64_t k_stride, const pi_half* v, int64_t v_stride,
+                       void* stream);
+
+/*
+ * pi_kv_read -- the stored values of the batch's tokens, as fp16.
+ *
+ * k and v: n_tok x n_kv x d, contiguous, fully written for rows that belong to
+ * a sequence: fp16(code * scale), rounded once (a scale above what fp16 holds
+ * gives infinities), 0 for a negative position.  q_start is any range of
+ * newest tokens: with n = ctx[s] it is the whole sequence.
+ */
+pi_status pi_kv_read(const pi_kv_cache* cache, const pi_kv_batch* batch,
+                     pi_half* k, pi_half* v, void* stream);
+
+/*
+ * pi_kv_attend -- attention of the call's tokens over the cache.
+ *
+ * q: n_tok x n_head x d (heads contiguous, tokens q_stride elements apart);
+ * query head a reads kv head a / (n_head / n_kv).  Per token at position p and
+ * head, over the positions A = { j : max(0, p - window + 1) <= j <= p }
+ * (window = 0: all j <= p):
+ *   x_j = scale * q . K_j;  m = max x_j;  l = sum e^(x_j - m)
+ *   y = sum e^(x_j - m) V_j / l;  lse = m + ln l
+ * over the values the cache holds.  The call's own tokens are part of the
+ * cache: append them first.  A token with nothing to attend to (negative
+ * position) gets y = 0, lse = -infinity.  y: n_tok x n_head x d fp16; lse:
+ * n_tok x n_head floats, or NULL.  Codes become fp16 exactly, products are
+ * fp16 x fp16 with fp32 sums, the softmax's statistics are fp32.  Slots outside
+ * A may hold anything, NaN included.
+ *
+ * Work is split over the sequences' actual lengths, which the kernels read on
+ * the device; the split, and with it the order of the sums, is a function of
+ * those lengths and the sizes alone.  ws: pi_kv_workspace_size() bytes, under
+ * the workspace rules above.
+ */
+pi_status pi_kv_attend(const pi_kv_cache* cache, const pi_kv_batch* batch,
+                       const pi_half* q, int64_t q_stride, int n_head, float scale, int window,
+                       pi_half* y, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of pi_kv_attend for these sizes. */
+pi_status pi_kv_workspace_size(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d, size_t* bytes);
+
 /* Workspace bytes that `op` needs for these sizes (op is a pi_op). */
 pi_status pi_workspace_size(int op, int B, int d, int r, int ffn, size_t* bytes);
 
