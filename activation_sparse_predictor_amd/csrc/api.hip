@@ -224,6 +224,13 @@ pi_status check_heads(int n_head, int n_kv) {
     return PI_OK;
 }
 
+pi_status check_kv_rows(int n_tok, int n_head, int n_kv) {
+    PI_REQUIRE((int64_t)n_tok * (n_head / n_kv) <= PI_KV_MAX_ROWS, PI_ERR_UNSUPPORTED,
+               "n_tok=%d with %d query heads a kv head: above PI_KV_MAX_ROWS=%d rows", n_tok, n_head / n_kv,
+               PI_KV_MAX_ROWS);
+    return PI_OK;
+}
+
 pi_status check_kv_counts(int n_seq, int n_tok, int max_q) {
     PI_REQUIRE(n_seq >= 1 && n_seq <= PI_KV_MAX_SEQ, PI_ERR_INVALID_ARG, "n_seq=%d outside [1, %d]", n_seq,
                PI_KV_MAX_SEQ);
@@ -797,6 +804,7 @@ pi_status pi_kv_attend(const pi_kv_cache* cache, const pi_kv_batch* batch, const
     pi::KvBatch b;
     PI_TRY(check_kv(cache, batch, &c, &b));
     PI_TRY(check_heads(n_head, c.n_kv));
+    PI_TRY(check_kv_rows(b.n_tok, n_head, c.n_kv));
     PI_REQUIRE(std::isfinite(scale), PI_ERR_INVALID_ARG, "scale is not finite");
     PI_REQUIRE(window >= 0, PI_ERR_INVALID_ARG, "window=%d is negative", window);
     PI_TRY(check_half(q, "q", true));
@@ -824,6 +832,7 @@ pi_status pi_kv_workspace_size(int n_seq, int n_tok, int max_q, int n_head, int 
                PI_KV_MAX_HEADS);
     PI_TRY(check_heads(n_head, n_kv));
     PI_TRY(check_kv_counts(n_seq, n_tok, max_q));
+    PI_TRY(check_kv_rows(n_tok, n_head, n_kv));
     PI_TRY(check_kv_d(d));
     *bytes = kv_ws_bytes(n_seq, n_tok, max_q, n_head, n_kv, d);
     return ok();

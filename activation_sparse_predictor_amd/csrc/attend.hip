@@ -1,81 +1,535 @@
 // Attention over the 8-bit paged cache.
 //
-// One wave a (row, query head): 64 keys a step, a key a lane for the scores, a
-// running maximum and sum, and d / 64 dimensions a lane for the output.
+// For a row (query token, head) and its keys j: x_j = scale log2(e) q . K_j,
+// p_j = 2^(x_j - R), l = sum p_j, y = sum p_j V_j / l, in one pass over the
+// cache with running references in place of R.
+//
+// K_j = ks code and V_j = vs code, one ks and vs a page and head.  Codes are
+// exact in fp16, so q . code runs on the matrix cores without rounding the
+// cache a second time; ks multiplies the fp32 score and vs the weight.  A
+// weight p vs can lie anywhere between 2^-31 and 2^9 times p, so the weights
+// have a reference of their own: M follows max (x + log2 vs), the weights are
+// w = 2^(x + log2 vs - M + 14), and y = (sum w code) 2^(M - R - 14) / l.  Both
+// references move only when a new maximum is more than 1 above them, so w
+// stays within 2^15 and fp16 holds it, down to 2^-39 of the row's largest; M is
+// kept above R - 60, below which nothing of the row can reach fp16.
+//
+// Operands.  A wave takes 64 keys (four granules of 16) a step, as the rows of
+// S^T = K Q^T and the inner axis of O^T = V^T P^T, with 16x16x32 products.
+// Row i of score tile t is token 4 t + i % 4 of granule i / 4.  Then lane
+// (n, g) = (lane % 16, lane / 16) ends up with the 16 scores of query n against
+// the tokens of granule g, in order: they are, as they stand, the second
+// operand of the output's products, all share one page, and the V operand is
+// 16 contiguous bytes (a dimension's 16 tokens).  So nothing is shuffled or
+// staged between the two products, and a lane has one ks and one vs a step.
 #include "kv.hpp"
 
 namespace pi {
 
-template <int FMT>
-__global__ __launch_bounds__(256) void k_attend(KvCache c, KvBatch b, const h16* __restrict__ q, long long q_stride,
-                                                int n_head, float scale, int window, h16* __restrict__ y,
-                                                float* __restrict__ lse) {
-    const int lane = lane_id();
-    const long long unit = (long long)blockIdx.x * 4 + threadIdx.x / kWave;
-    const int row = (int)(unit / n_head), head = (int)(unit % n_head);
-    if (row >= b.n_tok) return;
-    int inside;
-    const Seq sq = find_seq(b, row, inside, [](const Seq& x) { return x.n; });
-    if (sq.s < 0) return;
-    const int h = head / (n_head / c.n_kv), d = c.d;
-    const int pos = sq.ctx - sq.n + inside;
-    const int lo = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
-    const h16* qr = q + (size_t)row * q_stride + (size_t)head * d;
-    float m = -__builtin_inff(), l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = lo & ~63; j0 <= pos; j0 += kWave) {
-        const int j = j0 + lane;
-        const bool in = j >= lo && j <= pos;
-        float x = -__builtin_inff(), vs = 0.f;
-        size_t at = 0;
-        if (in) {
-            int id = b.table[(size_t)sq.s * b.table_stride + j / c.page];
-            const bool known = id >= 0 && id < c.n_pages;
-            id = known ? id : 0;
-            const size_t si = (size_t)id * c.n_kv + h;
-            const float ks = known ? c.k_scale[si] : __builtin_nanf("");
-            vs = known ? c.v_scale[si] : __builtin_nanf("");
-            at = page_base(c, id, h);
-            const int t = j & (c.page - 1);
-            float dot = 0.f;
-            for (int i = 0; i < d; ++i) dot = fmaf((float)qr[i], Codes<FMT>::value(c.k[at + k_byte(t, i, d)]), dot);
-            x = dot * ks * scale;
-        }
-        float mx = x;
-        for (int off = 1; off < kWave; off <<= 1) mx = fmaxf(mx, __shfl_xor(mx, off, kWave));
-        const float mn = fmaxf(m, mx);
-        const float f = m == mn ? 1.f : expf(m - mn);
-        const float p = in ? expf(x - mn) : 0.f;
-        l = fmaf(l, f, group_sum<64>(p));
-        m = mn;
-        for (int i = 0; i < 4; ++i) acc[i] *= f;
-        const float w = in ? p * vs : 0.f;
-        for (int k = 0; k < kWave; ++k) {
-            if (j0 + k < lo || j0 + k > pos) continue;
-            const float wk = __shfl(w, k, kWave);
-            const size_t ak = ((size_t)(uint32_t)__shfl((int)(at >> 32), k, kWave) << 32) | (uint32_t)__shfl((int)at, k, kWave);
-            const int t = (j0 + k) & (c.page - 1);
-            for (int i = 0; i < 4; ++i)
-                if (lane + 64 * i < d)
-                    acc[i] = fmaf(wk, Codes<FMT>::value(c.v[ak + v_byte(t, lane + 64 * i, d)]), acc[i]);
-        }
-    }
-    h16* yr = y + ((size_t)row * n_head + head) * d;
-    for (int i = 0; i < 4; ++i)
-        if (lane + 64 * i < d) yr[lane + 64 * i] = (h16)(pos < 0 ? 0.f : acc[i] / l);
-    if (lse && lane == 0) lse[(size_t)row * n_head + head] = pos < 0 ? -__builtin_inff() : m + logf(l);
+constexpr int kTile = 64;          // keys a wave takes at a time
+constexpr int kAttWaves = 8;
+constexpr int kAttThreads = kAttWaves * kWave;
+constexpr int kAttTarget = 512;    // workgroups the work is split into, two a CU
+constexpr int kAttMinTiles = 4;    // fewest tiles worth a workgroup of their own
+constexpr int kAttSlots = 2 * kAttTarget;   // units of split items: ceil(t / C) < 2 t / C where t > C
+constexpr int kAttCtrStride = 16;  // words between arrival counters
+
+constexpr float kLift = 14.f, kSlack = 1.f, kFloor = 60.f, kNone = -1e30f, kLn2 = 0.69314718055994531f;
+
+// max over the lanes that hold the same query (lane ^ 16, lane ^ 32)
+__device__ __forceinline__ float max_groups(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+    const uint32_t w = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_groups(float v) { return add_swap<32>(add_swap<16>(v)); }
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
+
+struct AttArgs {
+    KvCache c;
+    KvBatch b;
+    const h16* q;
+    long long q_stride;
+    int n_head, group, window;
+    float scale2;   // scale * log2(e)
+    h16* y;
+    float* lse;
+    uint32_t* ctr;
+    float* part;
+};
+
+// What a workgroup works on: `rows` query rows of a sequence from row0 on,
+// tiles [t0, t1), head h, piece `split` of `splits`.
+struct AttUnit {
+    Seq q;
+    int h, row_tile, t0, t1, split, splits, slot;
+};
+
+// First tile of a sequence that any of its rows attends to, and the tiles in all (at least one).
+__device__ __forceinline__ int att_first_tile(const Seq& q, int window) {
+    const int lo = q.ctx - q.n - window + 1;
+    return window > 0 && lo > 0 ? lo / kTile : 0;
+}
+__device__ __forceinline__ int att_tiles(const Seq& q, int window) {
+    const int n = (q.ctx + kTile - 1) / kTile - att_first_tile(q, window);
+    return n > 0 ? n : 1;
 }
 
-size_t kv_attend_bytes(int, int, int, int, int, int) { return 256; }
-size_t kv_attend_zero_bytes() { return 256; }
+// Splits the whole batch's tiles over about kAttTarget workgroups: C tiles a
+// workgroup, the same for every sequence, from the lengths as they are on the
+// device.  Each item (sequence, row tile) becomes ceil(tiles / C) pieces of
+// nearly equal size, for each head.  Every wave computes it for itself: a
+// round of 64 sequences is one round of loads.  Fills in unit `item`, if there is
+// one, and returns how many there are (of each head).  With at most 2^24 rows
+// and 2^10 sequences, whatever the lengths say, the sums stay below 2^31.
+template <int ROWS>
+__device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) {
+    const KvBatch& b = A.b;
+    long long all = 0;
+    for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
+        const int s = s0 + lane_id();
+        long long n = 0;
+        if (s < b.n_seq) {
+            const Seq q = kv_seq(b, s);
+            n = (long long)((q.n * A.group + ROWS - 1) / ROWS) * att_tiles(q, A.window);
+        }
+#pragma unroll
+        for (int off = 1; off < kWave; off <<= 1) n += __shfl_xor(n, off, kWave);
+        all += n;
+    }
+    const long long c64 = (all * A.c.n_kv + kAttTarget - 1) / kAttTarget;
+    const int C = c64 < kAttMinTiles ? kAttMinTiles : (int)c64;
+    int before = 0, slots = 0;
+    for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
+        const int s = s0 + lane_id();
+        Seq q{-1, 0, 0, 0};
+        int rt = 0, ns = 1, tiles = 1;
+        if (s < b.n_seq) {
+            q = kv_seq(b, s);
+            rt = (q.n * A.group + ROWS - 1) / ROWS;
+            tiles = att_tiles(q, A.window);
+            ns = (tiles + C - 1) / C;
+        }
+        const int upto = before + wave_scan(rt * ns), held = ns > 1 ? rt * ns : 0;
+        const int slots_upto = slots + wave_scan(held);
+        const uint64_t hit = __ballot(upto > item);
+        if (hit && before <= item) {
+            const int l = __builtin_ctzll(hit);
+            w.q.s = s0 + l;
+            w.q.row0 = __builtin_amdgcn_readlane(q.row0, l);
+            w.q.n = __builtin_amdgcn_readlane(q.n, l);
+            w.q.ctx = __builtin_amdgcn_readlane(q.ctx, l);
+            w.splits = __builtin_amdgcn_readlane(ns, l);
+            const int rts = __builtin_amdgcn_readlane(rt, l), T = __builtin_amdgcn_readlane(tiles, l);
+            const int inside = item - (__builtin_amdgcn_readlane(upto, l) - rts * w.splits);
+            w.row_tile = inside / w.splits;
+            w.split = inside % w.splits;
+            w.slot = __builtin_amdgcn_readlane(slots_upto, l) - __builtin_amdgcn_readlane(held, l) +
+                     w.row_tile * w.splits;   // the item's first slot
+            const int f = att_first_tile(w.q, A.window);
+            w.t0 = f + (int)((long long)T * w.split / w.splits);
+            w.t1 = f + (int)((long long)T * (w.split + 1) / w.splits);
+        }
+        before = __builtin_amdgcn_readlane(upto, kWave - 1);
+        slots = __builtin_amdgcn_readlane(slots_upto, kWave - 1);
+    }
+    return before;
+}
+
+// A granule's page: its place in the pool and whether it exists.
+struct Page {
+    int id;      // clamped into the pool
+    bool known;
+};
+
+// KJ: 64-dimension steps of a head, NT: 16-row tiles of queries a wave carries.
+template <int FMT, int KJ, int NT>
+__device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) {
+    constexpr int ROWS = 16 * NT, DP = 64 * KJ, LD = DP + 4;
+    extern __shared__ float lds[];   // [waves][ROWS][LD] outputs, [waves][3][ROWS] statistics
+    __shared__ int s_last;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int lane = lane_id(), n16 = lane & 15, g = lane >> 4;
+    const int d = A.c.d, dc = d / 16, page = A.c.page, group = A.group;
+    const int ctx = w.q.ctx, first = ctx - w.q.n, rows_all = w.q.n * group;
+    const int shift = __builtin_ctz(page), last_gran = ctx > 0 ? (ctx - 1) / kGran : 0;
+    const int32_t* table = A.b.table + (size_t)w.q.s * A.b.table_stride;
+
+    // this lane's queries: position, and the operand's fragments
+    int pos[NT], lo[NT];
+    f16x8 qf[NT][2 * KJ];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = w.row_tile * ROWS + nt * 16 + n16;
+        const int tok = r / group, head = w.h * group + r % group;
+        const bool live = r < rows_all;
+        pos[nt] = live ? first + tok : -1;
+        lo[nt] = A.window > 0 && pos[nt] - A.window + 1 > 0 ? pos[nt] - A.window + 1 : 0;
+        const h16* qr = A.q + (size_t)(w.q.row0 + (live ? tok : 0)) * A.q_stride + (size_t)head * d;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+            const int ch = j * 4 + g;
+            u32x4 a = {0u, 0u, 0u, 0u}, e = a;
+            if (live && ch < dc) {
+                a = ld16(qr + ch * 16);
+                e = ld16(qr + ch * 16 + 8);
+            }
+            qf[nt][2 * j] = __builtin_bit_cast(f16x8, a);
+            qf[nt][2 * j + 1] = __builtin_bit_cast(f16x8, e);
+        }
+    }
+    // positions that every row of this workgroup attends to need no mask
+    const int row_a = w.row_tile * ROWS / group;
+    int row_b = (w.row_tile * ROWS + ROWS - 1) / group;
+    if (row_b >= w.q.n) row_b = w.q.n - 1;
+    const int free_to = first + row_a;                                                   // up to this one
+    const int free_from = A.window > 0 ? first + row_b - A.window + 1 : 0;               // from this one on
+
+    // and outside these, none attends
+    const int any_to = first + row_b, any_from = A.window > 0 ? first + row_a - A.window + 1 : 0;
+
+    // byte offsets of this lane's pieces inside a granule
+    int ko[KJ];
+#pragma unroll
+    for (int j = 0; j < KJ; ++j) {
+        const int ch = j * 4 + g < dc ? j * 4 + g : dc - 1;   // beyond d: any finite code, its query is 0
+        ko[j] = ch * 64 + (n16 & 3) * 16;
+    }
+    const int gk = n16 >> 2;
+
+    auto lookup = [&](int tile, int gl) {
+        int gi = tile * (kTile / kGran) + gl;
+        gi = gi < last_gran ? gi : last_gran;   // past the end: some page of the sequence; masked
+        const int id = ctx > 0 ? table[gi * kGran >> shift] : -1;
+        return Page{id >= 0 && id < A.c.n_pages ? id : 0, id >= 0 && id < A.c.n_pages};
+    };
+    auto gran_base = [&](const Page& p, int tile, int gl) {
+        int gi = tile * (kTile / kGran) + gl;
+        gi = gi < last_gran ? gi : last_gran;
+        return ((size_t)p.id * A.c.n_kv + w.h) * (size_t)(page * d) + (size_t)((gi * kGran & (page - 1)) * d);
+    };
+
+    float R[NT], M[NT], l[NT];
+    f32x4 O[NT][4 * KJ];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        R[nt] = M[nt] = kNone;
+        l[nt] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4 * KJ; ++k) O[nt][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    u32x4 kc[4][KJ];
+    auto load_k = [&](const Page& p, int tile) {
+        const uint8_t* at = A.c.k + gran_base(p, tile, gk);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) kc[t][j] = ld16_stream(at + t * 4 * d + ko[j]);
+    };
+
+    int tile = w.t0 + wave;
+    Page pk{0, false}, pv{0, false};
+    float ks = 0.f, vs = 0.f;
+    if (tile < w.t1) {
+        pk = lookup(tile, gk);
+        pv = lookup(tile, g);
+        load_k(pk, tile);
+    }
+    for (; tile < w.t1; tile += kAttWaves) {
+        // this step's V and scales
+        u32x4 vc[4 * KJ];
+        {
+            const uint8_t* at = A.c.v + gran_base(pv, tile, g) + n16 * 16;
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k) vc[k] = ld16_stream(at + (k < dc ? k : dc - 1) * 256);
+        }
+        const size_t si = (size_t)pv.id * A.c.n_kv + w.h;
+        ks = A.c.k_scale[si];
+        vs = A.c.v_scale[si];
+        const bool known = pv.known;
+        const int next = tile + kAttWaves < w.t1 ? tile + kAttWaves : tile;
+        pk = lookup(next, gk);
+        pv = lookup(next, g);
+
+        f32x4 S[NT][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) S[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                f16x2 c[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) Codes<FMT>::to_f16(kc[t][j][i], c[2 * i], c[2 * i + 1]);
+                f16x8 a = {c[0].x, c[0].y, c[1].x, c[1].y, c[2].x, c[2].y, c[3].x, c[3].y};
+                f16x8 e = {c[4].x, c[4].y, c[5].x, c[5].y, c[6].x, c[6].y, c[7].x, c[7].y};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    S[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[nt][2 * j], S[nt][t], 0, 0, 0);
+                    S[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, qf[nt][2 * j + 1], S[nt][t], 0, 0, 0);
+                }
+            }
+        }
+        if (next != tile) load_k(pk, next);
+
+        ks = known ? ks : __builtin_nanf("");
+        vs = known ? vs : __builtin_nanf("");
+        const float kx = ks * A.scale2, lv = log2_fast(vs);
+        const int key0 = tile * kTile + g * kGran;   // position of this lane's first key
+        const bool edge = tile * kTile < free_from || tile * kTile + kTile - 1 > free_to;
+        f16x8 ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = S[nt][i / 4][i % 4] * kx;
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    x[i] = key0 + i >= lo[nt] && key0 + i <= pos[nt] ? x[i] : -__builtin_inff();
+            }
+            float mx = x[0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[i]);
+            const float mr = max_groups(mx), mw = max_groups(mx + lv);
+            if (__ballot(mr > R[nt] + kSlack || mw > M[nt] + kSlack)) {
+                const float r = fmaxf(R[nt], mr), m = fmaxf(fmaxf(M[nt], mw), r - kFloor);
+                l[nt] *= exp2_fast(R[nt] - r);
+                const float f = exp2_fast(M[nt] - m);
+#pragma unroll
+                for (int k = 0; k < 4 * KJ; ++k) O[nt][k] *= f;
+                R[nt] = r;
+                M[nt] = m;
+            }
+            const float up = vs * exp2_fast(R[nt] - M[nt] + kLift);
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float p = exp2_fast(x[i] - R[nt]);
+                sum += p;
+                float wt = p * up;
+                if (edge) wt = key0 + i >= lo[nt] && key0 + i <= pos[nt] ? wt : 0.f;
+                const f16 hi = (f16)wt;
+                ph[nt][i / 8][i % 8] = hi;
+                pl[nt][i / 8][i % 8] = (f16)(wt - (float)hi);
+            }
+            l[nt] += sum;
+        }
+        // fp8 slots that no row here attends to may hold NaN, which a zero weight would not silence
+        const bool tail = FMT == 1 && (tile * kTile < any_from || tile * kTile + kTile - 1 > any_to);
+#pragma unroll
+        for (int k = 0; k < 4 * KJ; ++k) {
+            u32x4 v = vc[k];
+            if (tail) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k0 = key0 + 4 * i;   // the word's tokens are k0 .. k0 + 3
+                    const int have = any_to + 1 - k0, skip = any_from - k0;
+                    v[i] = have >= 4 ? v[i] : have <= 0 ? 0u : v[i] & ((1u << (8 * have)) - 1u);
+                    v[i] = skip <= 0 ? v[i] : skip >= 4 ? 0u : v[i] & ~((1u << (8 * skip)) - 1u);
+                }
+            }
+            f16x2 c[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Codes<FMT>::to_f16(v[i], c[2 * i], c[2 * i + 1]);
+            f16x8 a = {c[0].x, c[0].y, c[1].x, c[1].y, c[2].x, c[2].y, c[3].x, c[3].y};
+            f16x8 e = {c[4].x, c[4].y, c[5].x, c[5].y, c[6].x, c[6].y, c[7].x, c[7].y};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[nt][0], O[nt][k], 0, 0, 0);
+                O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, ph[nt][1], O[nt][k], 0, 0, 0);
+                O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[nt][0], O[nt][k], 0, 0, 0);
+                O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, pl[nt][1], O[nt][k], 0, 0, 0);
+            }
+        }
+    }
+
+    // join the waves that had tiles
+    const int parts = w.t1 - w.t0 < kAttWaves ? w.t1 - w.t0 : kAttWaves;
+    float* outs = lds;                                   // [parts][ROWS][LD]
+    float* stat = lds + kAttWaves * ROWS * LD;           // [parts][3][ROWS]: R, M, l
+    if (wave < parts) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float sum = sum_groups(l[nt]);
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k)
+                *reinterpret_cast<f32x4*>(&outs[(wave * ROWS + nt * 16 + n16) * LD + k * 16 + g * 4]) = O[nt][k];
+            if (g == 0) {
+                stat[(wave * 3 + 0) * ROWS + nt * 16 + n16] = R[nt];
+                stat[(wave * 3 + 1) * ROWS + nt * 16 + n16] = M[nt];
+                stat[(wave * 3 + 2) * ROWS + nt * 16 + n16] = sum;
+            }
+        }
+    }
+    __syncthreads();
+    const int rows = rows_all - w.row_tile * ROWS < ROWS ? rows_all - w.row_tile * ROWS : ROWS;
+    auto emit = [&](int r, int i, float o, float sum, float Rr, float Mr) {
+        const int gr = w.row_tile * ROWS + r, tok = gr / group, head = w.h * group + gr % group;
+        const size_t at = (size_t)(w.q.row0 + tok) * A.n_head + head;
+        const bool empty = first + tok < 0;
+        // no weight at all although there are keys: every score was -infinity
+        const float val = empty ? 0.f : sum == 0.f ? __builtin_nanf("") : o * exp2_fast(Mr - Rr - kLift) / sum;
+        A.y[at * d + i] = (h16)val;
+        if (A.lse && i == 0) A.lse[at] = empty ? -__builtin_inff() : (Rr + log2_fast(sum)) * kLn2;
+    };
+    constexpr int kSlotWords = ROWS * (DP + 3);
+    float* mine = A.part + ((size_t)(w.slot + w.split) * A.c.n_kv + w.h) * kSlotWords;
+    for (int e = threadIdx.x; e < rows * d; e += kAttThreads) {
+        const int r = e / d, i = e % d;
+        float Rr = kNone, Mr = kNone;
+        for (int p = 0; p < parts; ++p) {
+            Rr = fmaxf(Rr, stat[(p * 3 + 0) * ROWS + r]);
+            Mr = fmaxf(Mr, stat[(p * 3 + 1) * ROWS + r]);
+        }
+        float o = 0.f, sum = 0.f;
+        for (int p = 0; p < parts; ++p) {
+            o = fmaf(outs[(p * ROWS + r) * LD + i], exp2_fast(stat[(p * 3 + 1) * ROWS + r] - Mr), o);
+            sum = fmaf(stat[(p * 3 + 2) * ROWS + r], exp2_fast(stat[(p * 3 + 0) * ROWS + r] - Rr), sum);
+        }
+        if (w.splits == 1) {
+            emit(r, i, o, sum, Rr, Mr);
+        } else {
+            st_coherent(&mine[r * DP + i], o);
+            if (i == 0) {
+                st_coherent(&mine[ROWS * DP + r], Rr);
+                st_coherent(&mine[ROWS * DP + ROWS + r], Mr);
+                st_coherent(&mine[ROWS * DP + 2 * ROWS + r], sum);
+            }
+        }
+    }
+    if (w.splits == 1) return;
+
+    // the last of the item's pieces to arrive joins them, in their order
+    uint32_t* ctr = A.ctr + ((size_t)w.slot * A.c.n_kv + w.h) * kAttCtrStride;
+    wait_own_memory();
+    __syncthreads();
+    if (threadIdx.x == 0) s_last = fetch_add_acq_rel(ctr, 1u) == (uint32_t)(w.splits - 1);
+    __syncthreads();
+    if (!s_last) return;
+    const float* p0 = A.part + ((size_t)w.slot * A.c.n_kv + w.h) * kSlotWords;
+    const size_t step = (size_t)A.c.n_kv * kSlotWords;
+    // each row's references and sum over the pieces: a row's lanes take a piece each
+    constexpr int kRowLanes = kAttThreads / ROWS;   // 32 or 16
+    {
+        const int r = threadIdx.x / kRowLanes, j = threadIdx.x % kRowLanes;
+        float Rr = kNone, Mr = kNone, sum = 0.f;
+        for (int p = j; p < w.splits; p += kRowLanes) {
+            const float* at = p0 + p * step + ROWS * DP + r;
+            const float pr = ld_coherent(at), pm = ld_coherent(at + ROWS), ps = ld_coherent(at + 2 * ROWS);
+            if (r >= rows) continue;   // rows that nobody wrote
+            const float nr = fmaxf(Rr, pr);
+            sum = sum * exp2_fast(Rr - nr) + ps * exp2_fast(pr - nr);
+            Rr = nr;
+            Mr = fmaxf(Mr, pm);
+        }
+#pragma unroll
+        for (int off = 1; off < kRowLanes; off <<= 1) {
+            const float pr = __shfl_xor(Rr, off, kWave), ps = __shfl_xor(sum, off, kWave);
+            const float nr = fmaxf(Rr, pr);
+            sum = sum * exp2_fast(Rr - nr) + ps * exp2_fast(pr - nr);
+            Rr = nr;
+            Mr = fmaxf(Mr, __shfl_xor(Mr, off, kWave));
+        }
+        if (j == 0) {
+            stat[r] = Rr;
+            stat[ROWS + r] = Mr;
+            stat[2 * ROWS + r] = sum;
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < rows * d; e += kAttThreads) {
+        const int r = e / d, i = e % d;
+        const float Mr = stat[ROWS + r];
+        float o = 0.f;
+        for (int p = 0; p < w.splits; p += 16) {   // sixteen pieces' loads at a time
+            float v[16], m[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float* at = p0 + (p + k < w.splits ? p + k : p) * step;
+                v[k] = ld_coherent(at + r * DP + i);
+                m[k] = ld_coherent(at + ROWS * DP + ROWS + r);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (p + k < w.splits) o = fmaf(v[k], exp2_fast(m[k] - Mr), o);
+        }
+        emit(r, i, o, stat[2 * ROWS + r], stat[r], Mr);
+    }
+    if (threadIdx.x == 0) st_flag(ctr, 0u);
+}
+
+// A workgroup takes units until there are none: whatever the lengths on the
+// device say, every piece of every item runs, and the counters end at zero.
+template <int FMT, int KJ, int NT>
+__global__ __launch_bounds__(kAttThreads, 2) void k_attend(AttArgs A) {
+    AttUnit w;
+    w.h = blockIdx.y;
+    const int units = att_plan<16 * NT>(A, blockIdx.x, w);
+    for (int u = blockIdx.x; u < units;) {
+        attend_unit<FMT, KJ, NT>(A, w);
+        u += gridDim.x;
+        if (u < units) {
+            __syncthreads();   // the next unit uses the same shared memory
+            att_plan<16 * NT>(A, u, w);
+        }
+    }
+}
+
+static int att_rows(int d, int max_rows) { return d > 128 || max_rows <= 16 ? 16 : 32; }
+static int att_dp(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+
+static long long att_row_tiles(int n_seq, int n_tok, int max_q, int group, int rows) {
+    const long long each = (long long)n_seq * (((long long)max_q * group + rows - 1) / rows);
+    const long long all = (long long)n_tok * group / rows + n_seq;
+    return each < all ? each : all;
+}
+
+size_t kv_attend_zero_bytes() { return (size_t)kAttSlots * kAttCtrStride * 4; }
+
+size_t kv_attend_bytes(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d) {
+    (void)n_seq;
+    (void)n_tok;
+    const int rows = att_rows(d, max_q * (n_head / n_kv));
+    return kv_attend_zero_bytes() + (size_t)kAttSlots * rows * (att_dp(d) + 3) * 4;
+}
 
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
-                            float scale, int window, h16* y, float* lse, char*, hipStream_t s) {
-    const long long units = (long long)b.n_tok * n_head;
-    const dim3 grid((unsigned)((units + 3) / 4));
-    if (c.fmt == 0)
-        hipLaunchKernelGGL(k_attend<0>, grid, dim3(256), 0, s, c, b, q, q_stride, n_head, scale, window, y, lse);
-    else
-        hipLaunchKernelGGL(k_attend<1>, grid, dim3(256), 0, s, c, b, q, q_stride, n_head, scale, window, y, lse);
+                            float scale, int window, h16* y, float* lse, char* data, hipStream_t s) {
+    const int group = n_head / c.n_kv;
+    const int rows = att_rows(c.d, b.max_q * group), dp = att_dp(c.d);
+    AttArgs A{c, b, q, q_stride, n_head, group, window, scale * 1.4426950408889634f, y, lse,
+              reinterpret_cast<uint32_t*>(data), reinterpret_cast<float*>(data + kv_attend_zero_bytes())};
+    const long long items = att_row_tiles(b.n_seq, b.n_tok, b.max_q, group, rows);
+    const long long cap = ((long long)b.table_stride * c.page + kTile - 1) / kTile;
+    const long long most = items * ((cap + kAttMinTiles - 1) / kAttMinTiles);
+    long long grid = items + (kAttTarget + c.n_kv - 1) / c.n_kv;
+    if (grid > most) grid = most;
+    if (grid > 65536) grid = 65536;
+    const size_t shm = (size_t)kAttWaves * rows * (dp + 4 + 3) * 4;
+    hipError_t e = hipSuccess;
+#define PI_ATT(F, K, N)                                                                                        \
+    do {                                                                                                       \
+        if (shm > 65536)                                                                                       \
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<F, K, N>),                         \
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);                     \
+        if (e == hipSuccess)                                                                                   \
+            hipLaunchKernelGGL((k_attend<F, K, N>), dim3((unsigned)grid, c.n_kv), dim3(kAttThreads), shm, s, A);       \
+    } while (0)
+#define PI_ATT_D(F)                                          \
+    if (dp == 64) { if (rows == 16) PI_ATT(F, 1, 1); else PI_ATT(F, 1, 2); }   \
+    else if (dp == 128) { if (rows == 16) PI_ATT(F, 2, 1); else PI_ATT(F, 2, 2); } \
+    else PI_ATT(F, 4, 1)
+    if (c.fmt == 0) { PI_ATT_D(0); } else { PI_ATT_D(1); }
+#undef PI_ATT_D
+#undef PI_ATT
+    if (e != hipSuccess) return e;
     return hipGetLastError();
 }
 

@@ -489,6 +489,7 @@ typedef enum pi_kv_fmt {
 #define PI_KV_MAX_D 256
 #define PI_KV_MAX_PAGE 256
 #define PI_KV_MAX_TOKENS (1 << 20)
+#define PI_KV_MAX_ROWS (1 << 24)    /* pi_kv_attend: n_tok * n_head / n_kv */
 
 typedef struct pi_kv_cache {   /* read by the host during the call; k .. v_scale are device pointers */
     int fmt;                   /* pi_kv_fmt */
@@ -532,7 +533,7 @@ typedef struct pi_kv_batch {   /* read by the host during the call; the arrays a
  *
  * Errors (all three calls): INVALID_ARG for NULL pointers, an unknown fmt,
  * counts out of range, n_head not a multiple of n_kv, a negative window, a
- * stride below a row; UNSUPPORTED for a page size or d not listed, a stride
+ * stride below a row; UNSUPPORTED for more than PI_KV_MAX_ROWS rows, a page size or d not listed, a stride
  * not a multiple of 8, or misalignment (fp16 tensors, k and v 16 bytes, the
  * others 4).
  */
