@@ -27,7 +27,7 @@
 namespace pi {
 
 constexpr int kTile = 64;          // keys a wave takes at a time
-constexpr int kAttWaves = 8;
+constexpr int kAttWaves = 4;
 constexpr int kAttThreads = kAttWaves * kWave;
 constexpr int kAttTarget = 512;    // workgroups the work is split into, two a CU
 constexpr int kAttMinTiles = 4;    // fewest tiles worth a workgroup of their own
@@ -84,37 +84,39 @@ __device__ __forceinline__ int att_tiles(const Seq& q, int window) {
 // workgroup, the same for every sequence, from the lengths as they are on the
 // device.  Each item (sequence, row tile) becomes ceil(tiles / C) pieces of
 // nearly equal size, for each head.  Every wave computes it for itself: a
-// round of 64 sequences is one round of loads.  Fills in unit `item`, if there is
-// one, and returns how many there are (of each head).  With at most 2^24 rows
-// and 2^10 sequences, whatever the lengths say, the sums stay below 2^31.
+// round of 64 sequences is one round of loads.  Fills in unit `item`, if there
+// is one, and returns how many there are (of each head).  With at most 2^24
+// rows and 2^10 sequences, whatever the lengths say, the sums stay below 2^31.
 template <int ROWS>
 __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) {
     const KvBatch& b = A.b;
-    long long all = 0;
+    float all = 0.f;   // C only has to be the same everywhere and a little above the quotient
+    Seq q{-1, 0, 0, 0};
+    int rt = 0, tiles = 1;
     for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
         const int s = s0 + lane_id();
-        long long n = 0;
-        if (s < b.n_seq) {
-            const Seq q = kv_seq(b, s);
-            n = (long long)((q.n * A.group + ROWS - 1) / ROWS) * att_tiles(q, A.window);
-        }
-#pragma unroll
-        for (int off = 1; off < kWave; off <<= 1) n += __shfl_xor(n, off, kWave);
-        all += n;
-    }
-    const long long c64 = (all * A.c.n_kv + kAttTarget - 1) / kAttTarget;
-    const int C = c64 < kAttMinTiles ? kAttMinTiles : (int)c64;
-    int before = 0, slots = 0;
-    for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
-        const int s = s0 + lane_id();
-        Seq q{-1, 0, 0, 0};
-        int rt = 0, ns = 1, tiles = 1;
+        rt = 0;
         if (s < b.n_seq) {
             q = kv_seq(b, s);
             rt = (q.n * A.group + ROWS - 1) / ROWS;
             tiles = att_tiles(q, A.window);
-            ns = (tiles + C - 1) / C;
         }
+        all += group_sum<64>((float)rt * (float)tiles);
+    }
+    const float want = all * (float)A.c.n_kv * (1.001f / kAttTarget);
+    const int C = want < kAttMinTiles ? kAttMinTiles : (int)want + 1;
+    int before = 0, slots = 0;
+    for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
+        const int s = s0 + lane_id();
+        if (b.n_seq > kWave) {   // otherwise the first loop's values are still there
+            rt = 0;
+            if (s < b.n_seq) {
+                q = kv_seq(b, s);
+                rt = (q.n * A.group + ROWS - 1) / ROWS;
+                tiles = att_tiles(q, A.window);
+            }
+        }
+        const int ns = (tiles + C - 1) / C;
         const int upto = before + wave_scan(rt * ns), held = ns > 1 ? rt * ns : 0;
         const int slots_upto = slots + wave_scan(held);
         const uint64_t hit = __ballot(upto > item);
@@ -125,15 +127,15 @@ __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) 
             w.q.n = __builtin_amdgcn_readlane(q.n, l);
             w.q.ctx = __builtin_amdgcn_readlane(q.ctx, l);
             w.splits = __builtin_amdgcn_readlane(ns, l);
-            const int rts = __builtin_amdgcn_readlane(rt, l), T = __builtin_amdgcn_readlane(tiles, l);
-            const int inside = item - (__builtin_amdgcn_readlane(upto, l) - rts * w.splits);
+            const int T = __builtin_amdgcn_readlane(tiles, l);
+            const int inside = item - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(rt, l) * w.splits);
             w.row_tile = inside / w.splits;
-            w.split = inside % w.splits;
+            w.split = inside - w.row_tile * w.splits;
             w.slot = __builtin_amdgcn_readlane(slots_upto, l) - __builtin_amdgcn_readlane(held, l) +
                      w.row_tile * w.splits;   // the item's first slot
-            const int f = att_first_tile(w.q, A.window);
-            w.t0 = f + (int)((long long)T * w.split / w.splits);
-            w.t1 = f + (int)((long long)T * (w.split + 1) / w.splits);
+            const int each = T / w.splits, more = T - each * w.splits;
+            w.t0 = att_first_tile(w.q, A.window) + w.split * each + (w.split < more ? w.split : more);
+            w.t1 = w.t0 + each + (w.split < more ? 1 : 0);
         }
         before = __builtin_amdgcn_readlane(upto, kWave - 1);
         slots = __builtin_amdgcn_readlane(slots_upto, kWave - 1);
@@ -141,11 +143,24 @@ __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) 
     return before;
 }
 
-// A granule's page: its place in the pool and whether it exists.
-struct Page {
-    int id;      // clamped into the pool
-    bool known;
-};
+// 16 bytes of a piece's results, written and read past the caches that other
+// XCDs do not see (as the agent-scope atomics do).
+__device__ __forceinline__ void st16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at, f32x4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, (int)at, 0, 16);
+}
+__device__ __forceinline__ f32x4 ld16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, 0, 16));
+}
+
+typedef const __attribute__((address_space(4))) int32_t* const_i32;
+typedef const __attribute__((address_space(4))) float* const_f32;
+
+// v[i] for a lane's i in 0 .. 3
+template <class T>
+__device__ __forceinline__ T pick(const T (&v)[4], int i) {
+    const T a = i & 1 ? v[1] : v[0], b = i & 1 ? v[3] : v[2];
+    return i & 2 ? b : a;
+}
 
 // KJ: 64-dimension steps of a head, NT: 16-row tiles of queries a wave carries.
 template <int FMT, int KJ, int NT>
@@ -158,7 +173,67 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     const int d = A.c.d, dc = d / 16, page = A.c.page, group = A.group;
     const int ctx = w.q.ctx, first = ctx - w.q.n, rows_all = w.q.n * group;
     const int shift = __builtin_ctz(page), last_gran = ctx > 0 ? (ctx - 1) / kGran : 0;
-    const int32_t* table = A.b.table + (size_t)w.q.s * A.b.table_stride;
+
+    // The pages of a tile's four granules and their scales, through the scalar
+    // cache: uniform over the wave, and off the counter that the K and V loads
+    // wait on.  Granules past the end: some page of the sequence, masked.
+    const const_i32 table = (const_i32)(A.b.table + (size_t)w.q.s * A.b.table_stride);
+    const const_f32 k_scale = (const_f32)A.c.k_scale, v_scale = (const_f32)A.c.v_scale;
+    auto gran = [&](int tile, int i) {
+        const int gi = tile * (kTile / kGran) + i;
+        return gi < last_gran ? gi : last_gran;
+    };
+    auto lookup = [&](int tile, int (&id)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) id[i] = ctx > 0 ? table[gran(tile, i) * kGran >> shift] : -1;
+    };
+    auto known = [&](int id) { return id >= 0 && id < A.c.n_pages; };
+    auto scales = [&](const int (&id)[4], float (&ks)[4], float (&vs)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t at = (size_t)(known(id[i]) ? id[i] : 0) * A.c.n_kv + w.h;
+            ks[i] = known(id[i]) ? k_scale[at] : __builtin_nanf("");
+            vs[i] = known(id[i]) ? v_scale[at] : __builtin_nanf("");
+        }
+    };
+    auto gran_base = [&](const int (&id)[4], int tile, int i) {   // i: per lane
+        int p = pick(id, i);
+        p = known(p) ? p : 0;
+        return ((size_t)p * A.c.n_kv + w.h) * (size_t)(page * d) + (size_t)((gran(tile, i) * kGran & (page - 1)) * d);
+    };
+
+    // byte offsets of this lane's pieces inside a granule
+    int ko[KJ];
+#pragma unroll
+    for (int j = 0; j < KJ; ++j) {
+        const int ch = j * 4 + g < dc ? j * 4 + g : dc - 1;   // beyond d: any finite code, its query is 0
+        ko[j] = ch * 64 + (n16 & 3) * 16;
+    }
+    const int gk = n16 >> 2;
+    u32x4 kc[4][KJ], vc[4 * KJ];
+    auto load_k = [&](const int (&id)[4], int tile) {
+        const uint8_t* at = A.c.k + gran_base(id, tile, gk);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) kc[t][j] = ld16_stream(at + t * 4 * d + ko[j]);
+    };
+    auto load_v = [&](const int (&id)[4], int tile) {
+        const uint8_t* at = A.c.v + gran_base(id, tile, g) + n16 * 16;
+#pragma unroll
+        for (int k = 0; k < 4 * KJ; ++k) vc[k] = ld16_stream(at + (k < dc ? k : dc - 1) * 256);
+    };
+
+    int tile = w.t0 + wave;
+    int id[4];
+    float ks[4], vs[4];
+    if (tile < w.t1) {
+        lookup(tile, id);
+        load_k(id, tile);
+        load_v(id, tile);
+        scales(id, ks, vs);
+        lookup(tile + kAttWaves, id);
+    }
 
     // this lane's queries: position, and the operand's fragments
     int pos[NT], lo[NT];
@@ -189,30 +264,8 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     if (row_b >= w.q.n) row_b = w.q.n - 1;
     const int free_to = first + row_a;                                                   // up to this one
     const int free_from = A.window > 0 ? first + row_b - A.window + 1 : 0;               // from this one on
-
     // and outside these, none attends
     const int any_to = first + row_b, any_from = A.window > 0 ? first + row_a - A.window + 1 : 0;
-
-    // byte offsets of this lane's pieces inside a granule
-    int ko[KJ];
-#pragma unroll
-    for (int j = 0; j < KJ; ++j) {
-        const int ch = j * 4 + g < dc ? j * 4 + g : dc - 1;   // beyond d: any finite code, its query is 0
-        ko[j] = ch * 64 + (n16 & 3) * 16;
-    }
-    const int gk = n16 >> 2;
-
-    auto lookup = [&](int tile, int gl) {
-        int gi = tile * (kTile / kGran) + gl;
-        gi = gi < last_gran ? gi : last_gran;   // past the end: some page of the sequence; masked
-        const int id = ctx > 0 ? table[gi * kGran >> shift] : -1;
-        return Page{id >= 0 && id < A.c.n_pages ? id : 0, id >= 0 && id < A.c.n_pages};
-    };
-    auto gran_base = [&](const Page& p, int tile, int gl) {
-        int gi = tile * (kTile / kGran) + gl;
-        gi = gi < last_gran ? gi : last_gran;
-        return ((size_t)p.id * A.c.n_kv + w.h) * (size_t)(page * d) + (size_t)((gi * kGran & (page - 1)) * d);
-    };
 
     float R[NT], M[NT], l[NT];
     f32x4 O[NT][4 * KJ];
@@ -224,39 +277,8 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
         for (int k = 0; k < 4 * KJ; ++k) O[nt][k] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    u32x4 kc[4][KJ];
-    auto load_k = [&](const Page& p, int tile) {
-        const uint8_t* at = A.c.k + gran_base(p, tile, gk);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < KJ; ++j) kc[t][j] = ld16_stream(at + t * 4 * d + ko[j]);
-    };
-
-    int tile = w.t0 + wave;
-    Page pk{0, false}, pv{0, false};
-    float ks = 0.f, vs = 0.f;
-    if (tile < w.t1) {
-        pk = lookup(tile, gk);
-        pv = lookup(tile, g);
-        load_k(pk, tile);
-    }
     for (; tile < w.t1; tile += kAttWaves) {
-        // this step's V and scales
-        u32x4 vc[4 * KJ];
-        {
-            const uint8_t* at = A.c.v + gran_base(pv, tile, g) + n16 * 16;
-#pragma unroll
-            for (int k = 0; k < 4 * KJ; ++k) vc[k] = ld16_stream(at + (k < dc ? k : dc - 1) * 256);
-        }
-        const size_t si = (size_t)pv.id * A.c.n_kv + w.h;
-        ks = A.c.k_scale[si];
-        vs = A.c.v_scale[si];
-        const bool known = pv.known;
-        const int next = tile + kAttWaves < w.t1 ? tile + kAttWaves : tile;
-        pk = lookup(next, gk);
-        pv = lookup(next, g);
-
+        const int next = tile + kAttWaves;
         f32x4 S[NT][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -276,11 +298,9 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
                 }
             }
         }
-        if (next != tile) load_k(pk, next);
+        if (next < w.t1) load_k(id, next);
 
-        ks = known ? ks : __builtin_nanf("");
-        vs = known ? vs : __builtin_nanf("");
-        const float kx = ks * A.scale2, lv = log2_fast(vs);
+        const float kx = pick(ks, g) * A.scale2, vl = pick(vs, g), lv = log2_fast(vl);
         const int key0 = tile * kTile + g * kGran;   // position of this lane's first key
         const bool edge = tile * kTile < free_from || tile * kTile + kTile - 1 > free_to;
         f16x8 ph[NT][2], pl[NT][2];
@@ -307,7 +327,7 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
                 R[nt] = r;
                 M[nt] = m;
             }
-            const float up = vs * exp2_fast(R[nt] - M[nt] + kLift);
+            const float up = vl * exp2_fast(R[nt] - M[nt] + kLift);
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -322,22 +342,24 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
             l[nt] += sum;
         }
         // fp8 slots that no row here attends to may hold NaN, which a zero weight would not silence
-        const bool tail = FMT == 1 && (tile * kTile < any_from || tile * kTile + kTile - 1 > any_to);
+        if (FMT == 1 && (tile * kTile < any_from || tile * kTile + kTile - 1 > any_to)) {
 #pragma unroll
-        for (int k = 0; k < 4 * KJ; ++k) {
-            u32x4 v = vc[k];
-            if (tail) {
+            for (int k = 0; k < 4 * KJ; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int k0 = key0 + 4 * i;   // the word's tokens are k0 .. k0 + 3
                     const int have = any_to + 1 - k0, skip = any_from - k0;
-                    v[i] = have >= 4 ? v[i] : have <= 0 ? 0u : v[i] & ((1u << (8 * have)) - 1u);
-                    v[i] = skip <= 0 ? v[i] : skip >= 4 ? 0u : v[i] & ~((1u << (8 * skip)) - 1u);
+                    uint32_t v = vc[k][i];
+                    v = have >= 4 ? v : have <= 0 ? 0u : v & ((1u << (8 * have)) - 1u);
+                    v = skip <= 0 ? v : skip >= 4 ? 0u : v & ~((1u << (8 * skip)) - 1u);
+                    vc[k][i] = v;
                 }
-            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4 * KJ; ++k) {
             f16x2 c[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) Codes<FMT>::to_f16(v[i], c[2 * i], c[2 * i + 1]);
+            for (int i = 0; i < 4; ++i) Codes<FMT>::to_f16(vc[k][i], c[2 * i], c[2 * i + 1]);
             f16x8 a = {c[0].x, c[0].y, c[1].x, c[1].y, c[2].x, c[2].y, c[3].x, c[3].y};
             f16x8 e = {c[4].x, c[4].y, c[5].x, c[5].y, c[6].x, c[6].y, c[7].x, c[7].y};
 #pragma unroll
@@ -348,63 +370,84 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
                 O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, pl[nt][1], O[nt][k], 0, 0, 0);
             }
         }
+        if (next < w.t1) {
+            load_v(id, next);
+            scales(id, ks, vs);
+            lookup(next + kAttWaves, id);
+        }
     }
 
-    // join the waves that had tiles
+    // Join the waves that had tiles: statistics first, then every wave brings
+    // its outputs to the common reference and the workgroup adds them up.
     const int parts = w.t1 - w.t0 < kAttWaves ? w.t1 - w.t0 : kAttWaves;
     float* outs = lds;                                   // [parts][ROWS][LD]
     float* stat = lds + kAttWaves * ROWS * LD;           // [parts][3][ROWS]: R, M, l
+    float* done = stat + kAttWaves * 3 * ROWS;           // [3][ROWS]: the workgroup's
+    const int rows = rows_all - w.row_tile * ROWS < ROWS ? rows_all - w.row_tile * ROWS : ROWS;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const float sum = sum_groups(l[nt]);
+        if (g == 0 && wave < parts) {
+            stat[(wave * 3 + 0) * ROWS + nt * 16 + n16] = R[nt];
+            stat[(wave * 3 + 1) * ROWS + nt * 16 + n16] = M[nt];
+            stat[(wave * 3 + 2) * ROWS + nt * 16 + n16] = sum;
+        }
+    }
+    __syncthreads();
     if (wave < parts) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float sum = sum_groups(l[nt]);
+            const int r = nt * 16 + n16;
+            float Rr = kNone, Mr = kNone, sum = 0.f;
+            for (int p = 0; p < parts; ++p) {
+                Rr = fmaxf(Rr, stat[(p * 3 + 0) * ROWS + r]);
+                Mr = fmaxf(Mr, stat[(p * 3 + 1) * ROWS + r]);
+            }
+            const float f = exp2_fast(M[nt] - Mr);
 #pragma unroll
             for (int k = 0; k < 4 * KJ; ++k)
-                *reinterpret_cast<f32x4*>(&outs[(wave * ROWS + nt * 16 + n16) * LD + k * 16 + g * 4]) = O[nt][k];
-            if (g == 0) {
-                stat[(wave * 3 + 0) * ROWS + nt * 16 + n16] = R[nt];
-                stat[(wave * 3 + 1) * ROWS + nt * 16 + n16] = M[nt];
-                stat[(wave * 3 + 2) * ROWS + nt * 16 + n16] = sum;
+                *reinterpret_cast<f32x4*>(&outs[(wave * ROWS + r) * LD + k * 16 + g * 4]) = O[nt][k] * f;
+            if (wave == 0 && g == 0) {
+                for (int p = 0; p < parts; ++p)
+                    sum = fmaf(stat[(p * 3 + 2) * ROWS + r], exp2_fast(stat[(p * 3 + 0) * ROWS + r] - Rr), sum);
+                done[r] = Rr;
+                done[ROWS + r] = Mr;
+                done[2 * ROWS + r] = sum;
             }
         }
     }
     __syncthreads();
-    const int rows = rows_all - w.row_tile * ROWS < ROWS ? rows_all - w.row_tile * ROWS : ROWS;
-    auto emit = [&](int r, int i, float o, float sum, float Rr, float Mr) {
-        const int gr = w.row_tile * ROWS + r, tok = gr / group, head = w.h * group + gr % group;
+
+    // four outputs of a row, from its sum of weights and references in `done`
+    auto emit = [&](int r, int i, f32x4 o) {
+        const int gr = w.row_tile * ROWS + r, tok = gr / group, head = w.h * group + gr - tok * group;
         const size_t at = (size_t)(w.q.row0 + tok) * A.n_head + head;
         const bool empty = first + tok < 0;
+        const float Rr = done[r], sum = done[2 * ROWS + r];
         // no weight at all although there are keys: every score was -infinity
-        const float val = empty ? 0.f : sum == 0.f ? __builtin_nanf("") : o * exp2_fast(Mr - Rr - kLift) / sum;
-        A.y[at * d + i] = (h16)val;
+        const float f = sum == 0.f ? __builtin_nanf("") : exp2_fast(done[ROWS + r] - Rr - kLift) / sum;
+        typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+        f16x4 v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = empty ? (f16)0.f : (f16)(o[k] * f);
+        *reinterpret_cast<f16x4*>(A.y + at * d + i) = v;
         if (A.lse && i == 0) A.lse[at] = empty ? -__builtin_inff() : (Rr + log2_fast(sum)) * kLn2;
     };
-    constexpr int kSlotWords = ROWS * (DP + 3);
-    float* mine = A.part + ((size_t)(w.slot + w.split) * A.c.n_kv + w.h) * kSlotWords;
-    for (int e = threadIdx.x; e < rows * d; e += kAttThreads) {
-        const int r = e / d, i = e % d;
-        float Rr = kNone, Mr = kNone;
-        for (int p = 0; p < parts; ++p) {
-            Rr = fmaxf(Rr, stat[(p * 3 + 0) * ROWS + r]);
-            Mr = fmaxf(Mr, stat[(p * 3 + 1) * ROWS + r]);
-        }
-        float o = 0.f, sum = 0.f;
-        for (int p = 0; p < parts; ++p) {
-            o = fmaf(outs[(p * ROWS + r) * LD + i], exp2_fast(stat[(p * 3 + 1) * ROWS + r] - Mr), o);
-            sum = fmaf(stat[(p * 3 + 2) * ROWS + r], exp2_fast(stat[(p * 3 + 0) * ROWS + r] - Rr), sum);
-        }
-        if (w.splits == 1) {
-            emit(r, i, o, sum, Rr, Mr);
-        } else {
-            st_coherent(&mine[r * DP + i], o);
-            if (i == 0) {
-                st_coherent(&mine[ROWS * DP + r], Rr);
-                st_coherent(&mine[ROWS * DP + ROWS + r], Mr);
-                st_coherent(&mine[ROWS * DP + 2 * ROWS + r], sum);
-            }
-        }
+    constexpr int kSlotBytes = ROWS * (DP + 4) * 4;   // outputs [ROWS][DP], then R, M, l and nothing [4][ROWS]
+    const size_t step = (size_t)A.c.n_kv * kSlotBytes;
+    char* item = reinterpret_cast<char*>(A.part) + ((size_t)w.slot * A.c.n_kv + w.h) * kSlotBytes;
+    const __amdgpu_buffer_rsrc_t mine = buf_rsrc(item + w.split * step, kSlotBytes);
+    for (int e = threadIdx.x; e < rows * (DP / 4); e += kAttThreads) {
+        const int r = e / (DP / 4), i = e % (DP / 4) * 4;
+        if (i >= d) continue;
+        f32x4 o = *reinterpret_cast<const f32x4*>(&outs[r * LD + i]);
+        for (int p = 1; p < parts; ++p) o += *reinterpret_cast<const f32x4*>(&outs[(p * ROWS + r) * LD + i]);
+        if (w.splits == 1) emit(r, i, o);
+        else st16_coherent(mine, (uint32_t)(r * DP + i) * 4, o);
     }
     if (w.splits == 1) return;
+    for (int e = threadIdx.x; e < 3 * ROWS / 4; e += kAttThreads)
+        st16_coherent(mine, (uint32_t)(ROWS * DP + e * 4) * 4, *reinterpret_cast<const f32x4*>(&done[e * 4]));
 
     // the last of the item's pieces to arrive joins them, in their order
     uint32_t* ctr = A.ctr + ((size_t)w.slot * A.c.n_kv + w.h) * kAttCtrStride;
@@ -413,17 +456,14 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     if (threadIdx.x == 0) s_last = fetch_add_acq_rel(ctr, 1u) == (uint32_t)(w.splits - 1);
     __syncthreads();
     if (!s_last) return;
-    const float* p0 = A.part + ((size_t)w.slot * A.c.n_kv + w.h) * kSlotWords;
-    const size_t step = (size_t)A.c.n_kv * kSlotWords;
     // each row's references and sum over the pieces: a row's lanes take a piece each
-    constexpr int kRowLanes = kAttThreads / ROWS;   // 32 or 16
+    constexpr int kRowLanes = kAttThreads / ROWS;
     {
         const int r = threadIdx.x / kRowLanes, j = threadIdx.x % kRowLanes;
         float Rr = kNone, Mr = kNone, sum = 0.f;
         for (int p = j; p < w.splits; p += kRowLanes) {
-            const float* at = p0 + p * step + ROWS * DP + r;
+            const float* at = reinterpret_cast<const float*>(item + p * step) + ROWS * DP + r;
             const float pr = ld_coherent(at), pm = ld_coherent(at + ROWS), ps = ld_coherent(at + 2 * ROWS);
-            if (r >= rows) continue;   // rows that nobody wrote
             const float nr = fmaxf(Rr, pr);
             sum = sum * exp2_fast(Rr - nr) + ps * exp2_fast(pr - nr);
             Rr = nr;
@@ -438,29 +478,33 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
             Mr = fmaxf(Mr, __shfl_xor(Mr, off, kWave));
         }
         if (j == 0) {
-            stat[r] = Rr;
-            stat[ROWS + r] = Mr;
-            stat[2 * ROWS + r] = sum;
+            done[r] = Rr;
+            done[ROWS + r] = Mr;
+            done[2 * ROWS + r] = sum;
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < rows * d; e += kAttThreads) {
-        const int r = e / d, i = e % d;
-        const float Mr = stat[ROWS + r];
-        float o = 0.f;
+    for (int e = threadIdx.x; e < rows * (DP / 4); e += kAttThreads) {
+        const int r = e / (DP / 4), i = e % (DP / 4) * 4;
+        if (i >= d) continue;
+        const float Mr = done[ROWS + r];
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
         for (int p = 0; p < w.splits; p += 16) {   // sixteen pieces' loads at a time
-            float v[16], m[16];
+            f32x4 v[16];
+            float m[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-                const float* at = p0 + (p + k < w.splits ? p + k : p) * step;
-                v[k] = ld_coherent(at + r * DP + i);
-                m[k] = ld_coherent(at + ROWS * DP + ROWS + r);
+                const char* at = item + (p + k < w.splits ? p + k : p) * step;
+                v[k] = ld16_coherent(buf_rsrc(at, kSlotBytes), (uint32_t)(r * DP + i) * 4);
+                m[k] = ld_coherent(reinterpret_cast<const float*>(at) + ROWS * DP + ROWS + r);
             }
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-                if (p + k < w.splits) o = fmaf(v[k], exp2_fast(m[k] - Mr), o);
+            for (int k = 0; k < 16; ++k) {
+                const float f = p + k < w.splits ? exp2_fast(m[k] - Mr) : 0.f;
+                if (p + k < w.splits) o += v[k] * f;
+            }
         }
-        emit(r, i, o, stat[2 * ROWS + r], stat[r], Mr);
+        emit(r, i, o);
     }
     if (threadIdx.x == 0) st_flag(ctr, 0u);
 }
@@ -468,7 +512,7 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
 // A workgroup takes units until there are none: whatever the lengths on the
 // device say, every piece of every item runs, and the counters end at zero.
 template <int FMT, int KJ, int NT>
-__global__ __launch_bounds__(kAttThreads, 2) void k_attend(AttArgs A) {
+__global__ __launch_bounds__(kAttThreads, KJ == 4 ? 1 : 2) void k_attend(AttArgs A) {
     AttUnit w;
     w.h = blockIdx.y;
     const int units = att_plan<16 * NT>(A, blockIdx.x, w);
@@ -497,7 +541,7 @@ size_t kv_attend_bytes(int n_seq, int n_tok, int max_q, int n_head, int n_kv, in
     (void)n_seq;
     (void)n_tok;
     const int rows = att_rows(d, max_q * (n_head / n_kv));
-    return kv_attend_zero_bytes() + (size_t)kAttSlots * rows * (att_dp(d) + 3) * 4;
+    return kv_attend_zero_bytes() + (size_t)kAttSlots * rows * (att_dp(d) + 4) * 4;
 }
 
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
@@ -512,7 +556,7 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, lo
     long long grid = items + (kAttTarget + c.n_kv - 1) / c.n_kv;
     if (grid > most) grid = most;
     if (grid > 65536) grid = 65536;
-    const size_t shm = (size_t)kAttWaves * rows * (dp + 4 + 3) * 4;
+    const size_t shm = ((size_t)kAttWaves * (dp + 4 + 3) + 3) * rows * 4;
     hipError_t e = hipSuccess;
 #define PI_ATT(F, K, N)                                                                                        \
     do {                                                                                                       \

@@ -84,13 +84,15 @@ __device__ __forceinline__ Seq kv_seq(const KvBatch& b, int s) {
     return q;
 }
 
-// Inclusive sum over the wave's lanes.
+// Inclusive sum over the wave's lanes: shifts inside each 16-lane row, then
+// the rows' last lanes broadcast to the rows behind them (DPP, no LDS).
 __device__ __forceinline__ int wave_scan(int v) {
-#pragma unroll
-    for (int off = 1; off < kWave; off <<= 1) {
-        const int o = __shfl_up(v, off, kWave);
-        if (lane_id() >= off) v += o;
-    }
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
     return v;
 }
 
