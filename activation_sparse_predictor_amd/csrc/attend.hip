@@ -29,9 +29,11 @@ namespace pi {
 constexpr int kTile = 64;          // keys a wave takes at a time
 constexpr int kAttWaves = 4;
 constexpr int kAttThreads = kAttWaves * kWave;
-constexpr int kAttTarget = 512;    // workgroups the work is split into, two a CU
+constexpr int kAttRows = 16;       // query rows of a workgroup
 constexpr int kAttMinTiles = 4;    // fewest tiles worth a workgroup of their own
-constexpr int kAttSlots = 2 * kAttTarget;   // units of split items: ceil(t / C) < 2 t / C where t > C
+// workgroups the work is split into: those that run at once, by the registers
+__host__ __device__ constexpr int att_target(int kj) { return kj == 4 ? 256 : kj == 2 ? 512 : 768; }
+constexpr int kAttSlots = 2 * 768;   // pieces of split items: ceil(t / C) < 2 t / C where t > C
 constexpr int kAttCtrStride = 16;  // words between arrival counters
 
 constexpr float kLift = 14.f, kSlack = 1.f, kFloor = 60.f, kNone = -1e30f, kLn2 = 0.69314718055994531f;
@@ -55,7 +57,7 @@ struct AttArgs {
     KvBatch b;
     const h16* q;
     long long q_stride;
-    int n_head, group, window;
+    int n_head, group, window, target;
     float scale2;   // scale * log2(e)
     h16* y;
     float* lse;
@@ -87,10 +89,10 @@ __device__ __forceinline__ int att_tiles(const Seq& q, int window) {
 // round of 64 sequences is one round of loads.  Fills in unit `item`, if there
 // is one, and returns how many there are (of each head).  With at most 2^24
 // rows and 2^10 sequences, whatever the lengths say, the sums stay below 2^31.
-template <int ROWS>
 __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) {
+    constexpr int ROWS = kAttRows;
     const KvBatch& b = A.b;
-    float all = 0.f;   // C only has to be the same everywhere and a little above the quotient
+    float all = 0.f, items = 0.f;   // C only has to be the same everywhere
     Seq q{-1, 0, 0, 0};
     int rt = 0, tiles = 1;
     for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
@@ -102,9 +104,18 @@ __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) 
             tiles = att_tiles(q, A.window);
         }
         all += group_sum<64>((float)rt * (float)tiles);
+        items += group_sum<64>((float)rt);
     }
-    const float want = all * (float)A.c.n_kv * (1.001f / kAttTarget);
-    const int C = want < kAttMinTiles ? kAttMinTiles : (int)want + 1;
+    const float room = (float)A.target / (float)A.c.n_kv;   // workgroups a head has
+    const float want = all / room * 1.001f;                 // a little above: the slots rest on it
+    int C = want < kAttMinTiles ? kAttMinTiles : (int)want + 1;
+    if (b.n_seq <= kWave && items <= room) {
+        // All items can run at once: the smallest C (to a sixteenth) whose rounded-up pieces still do.
+        for (int i = 0; i < 24; ++i) {
+            if (group_sum<64>((float)(rt * ((tiles + C - 1) / C))) <= room) break;
+            C += C / 16 + 1;
+        }
+    }
     int before = 0, slots = 0;
     for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
         const int s = s0 + lane_id();
@@ -162,10 +173,10 @@ __device__ __forceinline__ T pick(const T (&v)[4], int i) {
     return i & 2 ? b : a;
 }
 
-// KJ: 64-dimension steps of a head, NT: 16-row tiles of queries a wave carries.
-template <int FMT, int KJ, int NT>
+// KJ: 64-dimension steps of a head.
+template <int FMT, int KJ>
 __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) {
-    constexpr int ROWS = 16 * NT, DP = 64 * KJ, LD = DP + 4;
+    constexpr int ROWS = kAttRows, DP = 64 * KJ, LD = DP + 4;
     extern __shared__ float lds[];   // [waves][ROWS][LD] outputs, [waves][3][ROWS] statistics
     __shared__ int s_last;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -235,17 +246,15 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
         lookup(tile + kAttWaves, id);
     }
 
-    // this lane's queries: position, and the operand's fragments
-    int pos[NT], lo[NT];
-    f16x8 qf[NT][2 * KJ];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = w.row_tile * ROWS + nt * 16 + n16;
-        const int tok = r / group, head = w.h * group + r % group;
-        const bool live = r < rows_all;
-        pos[nt] = live ? first + tok : -1;
-        lo[nt] = A.window > 0 && pos[nt] - A.window + 1 > 0 ? pos[nt] - A.window + 1 : 0;
-        const h16* qr = A.q + (size_t)(w.q.row0 + (live ? tok : 0)) * A.q_stride + (size_t)head * d;
+    // this lane's query: position, and the operand's fragments
+    const int my_row = w.row_tile * ROWS + n16;
+    const bool live = my_row < rows_all;
+    const int my_tok = live ? my_row / group : 0, my_head = w.h * group + (live ? my_row - my_tok * group : 0);
+    const int pos = live ? first + my_tok : -1;
+    const int lo = A.window > 0 && pos - A.window + 1 > 0 ? pos - A.window + 1 : 0;
+    f16x8 qf[2 * KJ];
+    {
+        const h16* qr = A.q + (size_t)(w.q.row0 + my_tok) * A.q_stride + (size_t)my_head * d;
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
             const int ch = j * 4 + g;
@@ -254,8 +263,8 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
                 a = ld16(qr + ch * 16);
                 e = ld16(qr + ch * 16 + 8);
             }
-            qf[nt][2 * j] = __builtin_bit_cast(f16x8, a);
-            qf[nt][2 * j + 1] = __builtin_bit_cast(f16x8, e);
+            qf[2 * j] = __builtin_bit_cast(f16x8, a);
+            qf[2 * j + 1] = __builtin_bit_cast(f16x8, e);
         }
     }
     // positions that every row of this workgroup attends to need no mask
@@ -267,23 +276,17 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     // and outside these, none attends
     const int any_to = first + row_b, any_from = A.window > 0 ? first + row_a - A.window + 1 : 0;
 
-    float R[NT], M[NT], l[NT];
-    f32x4 O[NT][4 * KJ];
+    float R = kNone, M = kNone, l = 0.f;
+    f32x4 O[4 * KJ];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        R[nt] = M[nt] = kNone;
-        l[nt] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4 * KJ; ++k) O[nt][k] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int k = 0; k < 4 * KJ; ++k) O[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     for (; tile < w.t1; tile += kAttWaves) {
         const int next = tile + kAttWaves;
-        f32x4 S[NT][4];
+        f32x4 S[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) S[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < KJ; ++j) {
                 f16x2 c[8];
@@ -291,11 +294,8 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
                 for (int i = 0; i < 4; ++i) Codes<FMT>::to_f16(kc[t][j][i], c[2 * i], c[2 * i + 1]);
                 f16x8 a = {c[0].x, c[0].y, c[1].x, c[1].y, c[2].x, c[2].y, c[3].x, c[3].y};
                 f16x8 e = {c[4].x, c[4].y, c[5].x, c[5].y, c[6].x, c[6].y, c[7].x, c[7].y};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    S[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[nt][2 * j], S[nt][t], 0, 0, 0);
-                    S[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, qf[nt][2 * j + 1], S[nt][t], 0, 0, 0);
-                }
+                S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[2 * j], S[t], 0, 0, 0);
+                S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, qf[2 * j + 1], S[t], 0, 0, 0);
             }
         }
         if (next < w.t1) load_k(id, next);
@@ -303,44 +303,40 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
         const float kx = pick(ks, g) * A.scale2, vl = pick(vs, g), lv = log2_fast(vl);
         const int key0 = tile * kTile + g * kGran;   // position of this lane's first key
         const bool edge = tile * kTile < free_from || tile * kTile + kTile - 1 > free_to;
-        f16x8 ph[NT][2], pl[NT][2];
+        f16x8 ph[2], pl[2];   // the weights' leading and following halves: to 22 bits, at four more products a tile
+        float x[16];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float x[16];
+        for (int i = 0; i < 16; ++i) x[i] = S[i / 4][i % 4] * kx;
+        if (edge) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = S[nt][i / 4][i % 4] * kx;
-            if (edge) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    x[i] = key0 + i >= lo[nt] && key0 + i <= pos[nt] ? x[i] : -__builtin_inff();
-            }
-            float mx = x[0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[i]);
-            const float mr = max_groups(mx), mw = max_groups(mx + lv);
-            if (__ballot(mr > R[nt] + kSlack || mw > M[nt] + kSlack)) {
-                const float r = fmaxf(R[nt], mr), m = fmaxf(fmaxf(M[nt], mw), r - kFloor);
-                l[nt] *= exp2_fast(R[nt] - r);
-                const float f = exp2_fast(M[nt] - m);
-#pragma unroll
-                for (int k = 0; k < 4 * KJ; ++k) O[nt][k] *= f;
-                R[nt] = r;
-                M[nt] = m;
-            }
-            const float up = vl * exp2_fast(R[nt] - M[nt] + kLift);
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float p = exp2_fast(x[i] - R[nt]);
-                sum += p;
-                float wt = p * up;
-                if (edge) wt = key0 + i >= lo[nt] && key0 + i <= pos[nt] ? wt : 0.f;
-                const f16 hi = (f16)wt;
-                ph[nt][i / 8][i % 8] = hi;
-                pl[nt][i / 8][i % 8] = (f16)(wt - (float)hi);
-            }
-            l[nt] += sum;
+            for (int i = 0; i < 16; ++i) x[i] = key0 + i >= lo && key0 + i <= pos ? x[i] : -__builtin_inff();
         }
+        float mx = x[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[i]);
+        const float mr = max_groups(mx), mw = max_groups(mx + lv);
+        if (__ballot(mr > R + kSlack || mw > M + kSlack)) {
+            const float r = fmaxf(R, mr), m = fmaxf(fmaxf(M, mw), r - kFloor);
+            l *= exp2_fast(R - r);
+            const float f = exp2_fast(M - m);
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k) O[k] *= f;
+            R = r;
+            M = m;
+        }
+        const float up = vl * exp2_fast(R - M + kLift);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float p = exp2_fast(x[i] - R);
+            sum += p;
+            float wt = p * up;
+            if (edge) wt = key0 + i >= lo && key0 + i <= pos ? wt : 0.f;
+            const f16 hi = (f16)wt;
+            ph[i / 8][i % 8] = hi;
+            pl[i / 8][i % 8] = (f16)(wt - (float)hi);
+        }
+        l += sum;
         // fp8 slots that no row here attends to may hold NaN, which a zero weight would not silence
         if (FMT == 1 && (tile * kTile < any_from || tile * kTile + kTile - 1 > any_to)) {
 #pragma unroll
@@ -362,13 +358,10 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
             for (int i = 0; i < 4; ++i) Codes<FMT>::to_f16(vc[k][i], c[2 * i], c[2 * i + 1]);
             f16x8 a = {c[0].x, c[0].y, c[1].x, c[1].y, c[2].x, c[2].y, c[3].x, c[3].y};
             f16x8 e = {c[4].x, c[4].y, c[5].x, c[5].y, c[6].x, c[6].y, c[7].x, c[7].y};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[nt][0], O[nt][k], 0, 0, 0);
-                O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, ph[nt][1], O[nt][k], 0, 0, 0);
-                O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[nt][0], O[nt][k], 0, 0, 0);
-                O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, pl[nt][1], O[nt][k], 0, 0, 0);
-            }
+            O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[0], O[k], 0, 0, 0);
+            O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, ph[1], O[k], 0, 0, 0);
+            O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[0], O[k], 0, 0, 0);
+            O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, pl[1], O[k], 0, 0, 0);
         }
         if (next < w.t1) {
             load_v(id, next);
@@ -384,36 +377,29 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     float* stat = lds + kAttWaves * ROWS * LD;           // [parts][3][ROWS]: R, M, l
     float* done = stat + kAttWaves * 3 * ROWS;           // [3][ROWS]: the workgroup's
     const int rows = rows_all - w.row_tile * ROWS < ROWS ? rows_all - w.row_tile * ROWS : ROWS;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const float sum = sum_groups(l[nt]);
-        if (g == 0 && wave < parts) {
-            stat[(wave * 3 + 0) * ROWS + nt * 16 + n16] = R[nt];
-            stat[(wave * 3 + 1) * ROWS + nt * 16 + n16] = M[nt];
-            stat[(wave * 3 + 2) * ROWS + nt * 16 + n16] = sum;
-        }
+    l = sum_groups(l);
+    if (g == 0 && wave < parts) {
+        stat[(wave * 3 + 0) * ROWS + n16] = R;
+        stat[(wave * 3 + 1) * ROWS + n16] = M;
+        stat[(wave * 3 + 2) * ROWS + n16] = l;
     }
     __syncthreads();
     if (wave < parts) {
+        float Rr = kNone, Mr = kNone, sum = 0.f;
+        for (int p = 0; p < parts; ++p) {
+            Rr = fmaxf(Rr, stat[(p * 3 + 0) * ROWS + n16]);
+            Mr = fmaxf(Mr, stat[(p * 3 + 1) * ROWS + n16]);
+        }
+        const float f = exp2_fast(M - Mr);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = nt * 16 + n16;
-            float Rr = kNone, Mr = kNone, sum = 0.f;
-            for (int p = 0; p < parts; ++p) {
-                Rr = fmaxf(Rr, stat[(p * 3 + 0) * ROWS + r]);
-                Mr = fmaxf(Mr, stat[(p * 3 + 1) * ROWS + r]);
-            }
-            const float f = exp2_fast(M[nt] - Mr);
-#pragma unroll
-            for (int k = 0; k < 4 * KJ; ++k)
-                *reinterpret_cast<f32x4*>(&outs[(wave * ROWS + r) * LD + k * 16 + g * 4]) = O[nt][k] * f;
-            if (wave == 0 && g == 0) {
-                for (int p = 0; p < parts; ++p)
-                    sum = fmaf(stat[(p * 3 + 2) * ROWS + r], exp2_fast(stat[(p * 3 + 0) * ROWS + r] - Rr), sum);
-                done[r] = Rr;
-                done[ROWS + r] = Mr;
-                done[2 * ROWS + r] = sum;
-            }
+        for (int k = 0; k < 4 * KJ; ++k)
+            *reinterpret_cast<f32x4*>(&outs[(wave * ROWS + n16) * LD + k * 16 + g * 4]) = O[k] * f;
+        if (wave == 0 && g == 0) {
+            for (int p = 0; p < parts; ++p)
+                sum = fmaf(stat[(p * 3 + 2) * ROWS + n16], exp2_fast(stat[(p * 3 + 0) * ROWS + n16] - Rr), sum);
+            done[n16] = Rr;
+            done[ROWS + n16] = Mr;
+            done[2 * ROWS + n16] = sum;
         }
     }
     __syncthreads();
@@ -511,65 +497,62 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
 
 // A workgroup takes units until there are none: whatever the lengths on the
 // device say, every piece of every item runs, and the counters end at zero.
-template <int FMT, int KJ, int NT>
-__global__ __launch_bounds__(kAttThreads, KJ == 4 ? 1 : 2) void k_attend(AttArgs A) {
+template <int FMT, int KJ>
+__global__ __launch_bounds__(kAttThreads, KJ == 4 ? 1 : KJ == 2 ? 2 : 3) void k_attend(AttArgs A) {
     AttUnit w;
-    w.h = blockIdx.y;
-    const int units = att_plan<16 * NT>(A, blockIdx.x, w);
-    for (int u = blockIdx.x; u < units;) {
-        attend_unit<FMT, KJ, NT>(A, w);
-        u += gridDim.x;
+    w.h = blockIdx.x;
+    const int units = att_plan(A, blockIdx.y, w);
+    for (int u = blockIdx.y; u < units;) {
+        attend_unit<FMT, KJ>(A, w);
+        u += gridDim.y;
         if (u < units) {
             __syncthreads();   // the next unit uses the same shared memory
-            att_plan<16 * NT>(A, u, w);
+            att_plan(A, u, w);
         }
     }
 }
 
-static int att_rows(int d, int max_rows) { return d > 128 || max_rows <= 16 ? 16 : 32; }
-static int att_dp(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+static int att_kj(int d) { return d <= 64 ? 1 : d <= 128 ? 2 : 4; }
 
-static long long att_row_tiles(int n_seq, int n_tok, int max_q, int group, int rows) {
-    const long long each = (long long)n_seq * (((long long)max_q * group + rows - 1) / rows);
-    const long long all = (long long)n_tok * group / rows + n_seq;
+static long long att_row_tiles(const KvBatch& b, int group) {
+    const long long each = (long long)b.n_seq * (((long long)b.max_q * group + kAttRows - 1) / kAttRows);
+    const long long all = (long long)b.n_tok * group / kAttRows + b.n_seq;
     return each < all ? each : all;
 }
 
 size_t kv_attend_zero_bytes() { return (size_t)kAttSlots * kAttCtrStride * 4; }
 
-size_t kv_attend_bytes(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d) {
-    (void)n_seq;
-    (void)n_tok;
-    const int rows = att_rows(d, max_q * (n_head / n_kv));
-    return kv_attend_zero_bytes() + (size_t)kAttSlots * rows * (att_dp(d) + 4) * 4;
+size_t kv_attend_bytes(int, int, int, int, int, int d) {
+    return kv_attend_zero_bytes() + (size_t)kAttSlots * kAttRows * (64 * att_kj(d) + 4) * 4;
 }
 
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
                             float scale, int window, h16* y, float* lse, char* data, hipStream_t s) {
-    const int group = n_head / c.n_kv;
-    const int rows = att_rows(c.d, b.max_q * group), dp = att_dp(c.d);
-    AttArgs A{c, b, q, q_stride, n_head, group, window, scale * 1.4426950408889634f, y, lse,
+    const int group = n_head / c.n_kv, kj = att_kj(c.d), target = att_target(kj);
+    AttArgs A{c, b, q, q_stride, n_head, group, window, target, scale * 1.4426950408889634f, y, lse,
               reinterpret_cast<uint32_t*>(data), reinterpret_cast<float*>(data + kv_attend_zero_bytes())};
-    const long long items = att_row_tiles(b.n_seq, b.n_tok, b.max_q, group, rows);
+    const long long items = att_row_tiles(b, group);
     const long long cap = ((long long)b.table_stride * c.page + kTile - 1) / kTile;
     const long long most = items * ((cap + kAttMinTiles - 1) / kAttMinTiles);
-    long long grid = items + (kAttTarget + c.n_kv - 1) / c.n_kv;
-    if (grid > most) grid = most;
-    if (grid > 65536) grid = 65536;
-    const size_t shm = ((size_t)kAttWaves * (dp + 4 + 3) + 3) * rows * 4;
+    long long units = items + (target + c.n_kv - 1) / c.n_kv;
+    if (units > most) units = most;
+    if (units > 65535) units = 65535;
+    // heads side by side: the row tiles that read one head's pages run on one
+    // XCD where the heads are a multiple of 8, and share its L2
+    const dim3 grid(c.n_kv, (unsigned)units);
+    const size_t shm = ((size_t)kAttWaves * (64 * kj + 4 + 3) + 3) * kAttRows * 4;
     hipError_t e = hipSuccess;
-#define PI_ATT(F, K, N)                                                                                        \
-    do {                                                                                                       \
-        if (shm > 65536)                                                                                       \
-            e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<F, K, N>),                         \
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);                     \
-        if (e == hipSuccess)                                                                                   \
-            hipLaunchKernelGGL((k_attend<F, K, N>), dim3((unsigned)grid, c.n_kv), dim3(kAttThreads), shm, s, A);       \
+#define PI_ATT(F, K)                                                                               \
+    do {                                                                                           \
+        if (shm > 65536)                                                                           \
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<F, K>),                \
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);         \
+        if (e == hipSuccess) hipLaunchKernelGGL((k_attend<F, K>), grid, dim3(kAttThreads), shm, s, A); \
     } while (0)
-#define PI_ATT_D(F)                                          \
-    if (dp == 64) { if (rows == 16) PI_ATT(F, 1, 1); else PI_ATT(F, 1, 2); }   \
-    else if (dp == 128) { if (rows == 16) PI_ATT(F, 2, 1); else PI_ATT(F, 2, 2); } \
-    else PI_ATT(F, 4, 1)
+#define PI_ATT_D(F)                \
+    if (kj == 1) PI_ATT(F, 1);      \
+    else if (kj == 2) PI_ATT(F, 2); \
+    else PI_ATT(F, 4)
     if (c.fmt == 0) { PI_ATT_D(0); } else { PI_ATT_D(1); }
 #undef PI_ATT_D
 #undef PI_ATT
