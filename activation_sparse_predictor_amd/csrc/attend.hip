@@ -1,18 +1,18 @@
 // Attention over the 8-bit paged cache.
 //
-// For a row (query token, head) and its keys j: x_j = scale log2(e) q . K_j,
-// p_j = 2^(x_j - R), l = sum p_j, y = sum p_j V_j / l, in one pass over the
-// cache with running references in place of R.
+// For a row (query token, head) and its keys j, x_j = scale log2(e) q . K_j and
+// y = sum 2^x_j V_j / sum 2^x_j, in one pass over the cache.
 //
 // K_j = ks code and V_j = vs code, one ks and vs a page and head.  Codes are
 // exact in fp16, so q . code runs on the matrix cores without rounding the
-// cache a second time; ks multiplies the fp32 score and vs the weight.  A
-// weight p vs can lie anywhere between 2^-31 and 2^9 times p, so the weights
-// have a reference of their own: M follows max (x + log2 vs), the weights are
-// w = 2^(x + log2 vs - M + 14), and y = (sum w code) 2^(M - R - 14) / l.  Both
-// references move only when a new maximum is more than 1 above them, so w
-// stays within 2^15 and fp16 holds it, down to 2^-39 of the row's largest; M is
-// kept above R - 60, below which nothing of the row can reach fp16.
+// cache a second time; ks multiplies the fp32 score and vs the weight.  A vs
+// lies anywhere between 2^-31 and 2^9, so the running reference M follows the
+// largest weight with its scale, max (x + log2 vs):
+//   w_j = 2^(x_j + log2 vs_j - M + 14),  l = sum w_j / vs_j,  y = sum w_j code_j / l.
+// M moves only when a maximum is more than 1 above it, so w stays within 2^15
+// and fp16 holds it, down to 2^-39 of the row's largest; l is summed in fp32,
+// where its terms 2^(x - M + 14) always fit.  A page of zeros (vs = 0) takes part
+// as vs = 2^-64: its weights count, and its values stay far below fp16's range.
 //
 // Operands.  A wave takes 64 keys (four granules of 16) a step, as the rows of
 // S^T = K Q^T and the inner axis of O^T = V^T P^T, with 16x16x32 products.
@@ -32,11 +32,11 @@ constexpr int kAttThreads = kAttWaves * kWave;
 constexpr int kAttRows = 16;       // query rows of a workgroup
 constexpr int kAttMinTiles = 4;    // fewest tiles worth a workgroup of their own
 // workgroups the work is split into: those that run at once, by the registers
-__host__ __device__ constexpr int att_target(int kj) { return kj == 4 ? 256 : kj == 2 ? 512 : 768; }
-constexpr int kAttSlots = 2 * 768;   // pieces of split items: ceil(t / C) < 2 t / C where t > C
+__host__ __device__ constexpr int att_target(int kj) { return kj == 4 ? 256 : 512; }
+constexpr int kAttSlots = 2 * 512;   // pieces of split items: ceil(t / C) < 2 t / C where t > C
 constexpr int kAttCtrStride = 16;  // words between arrival counters
 
-constexpr float kLift = 14.f, kSlack = 1.f, kFloor = 60.f, kNone = -1e30f, kLn2 = 0.69314718055994531f;
+constexpr float kLift = 14.f, kSlack = 1.f, kZeroLog = -64.f, kNone = -1e30f, kLn2 = 0.69314718055994531f;
 
 // max over the lanes that hold the same query (lane ^ 16, lane ^ 32)
 __device__ __forceinline__ float max_groups(float v) {
@@ -159,94 +159,89 @@ __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) 
 __device__ __forceinline__ void st16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at, f32x4 v) {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, (int)at, 0, 16);
 }
-__device__ __forceinline__ f32x4 ld16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at) {
-    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, 0, 16));
+__device__ __forceinline__ f32x4 ld16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t from) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, (int)from, 16));
+}
+__device__ __forceinline__ float ld4_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (int)at, 0, 16));
 }
 
-typedef const __attribute__((address_space(4))) int32_t* const_i32;
-typedef const __attribute__((address_space(4))) float* const_f32;
+// A granule of the sequence: where its bytes start in the pools, and its
+// page's scales as the loop uses them.
+struct Gran {
+    uint32_t lo, hi;   // byte offset
+    float kx, lv;      // ks * |scale| * log2(e);  log2 vs
+};
+constexpr int kSegTiles = 128;   // tiles whose granules are looked up at a time
+constexpr int kSegGrans = kSegTiles * (kTile / kGran);
 
-// v[i] for a lane's i in 0 .. 3
-template <class T>
-__device__ __forceinline__ T pick(const T (&v)[4], int i) {
-    const T a = i & 1 ? v[1] : v[0], b = i & 1 ? v[3] : v[2];
-    return i & 2 ? b : a;
+// Eight codes of two words as fp16.
+template <int FMT>
+__device__ __forceinline__ f16x8 codes8(uint32_t a, uint32_t b) {
+    f16x2 c[4];
+    Codes<FMT>::to_f16(a, c[0], c[1]);
+    Codes<FMT>::to_f16(b, c[2], c[3]);
+    return f16x8{c[0].x, c[0].y, c[1].x, c[1].y, c[2].x, c[2].y, c[3].x, c[3].y};
 }
 
-// KJ: 64-dimension steps of a head.
-template <int FMT, int KJ>
+// KJ: 64-dimension steps of a head; FULL: d is all of them.
+template <int FMT, int KJ, bool FULL>
 __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) {
     constexpr int ROWS = kAttRows, DP = 64 * KJ, LD = DP + 4;
-    extern __shared__ float lds[];   // [waves][ROWS][LD] outputs, [waves][3][ROWS] statistics
+    extern __shared__ float lds[];   // while tiles are read: Gran [kSegGrans]; then the joins' arrays
     __shared__ int s_last;
+    Gran* grans = reinterpret_cast<Gran*>(lds);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int lane = lane_id(), n16 = lane & 15, g = lane >> 4;
-    const int d = A.c.d, dc = d / 16, page = A.c.page, group = A.group;
+    const int d = FULL ? DP : A.c.d, dc = d / 16, page = A.c.page, group = A.group;
     const int ctx = w.q.ctx, first = ctx - w.q.n, rows_all = w.q.n * group;
     const int shift = __builtin_ctz(page), last_gran = ctx > 0 ? (ctx - 1) / kGran : 0;
+    const int32_t* table = A.b.table + (size_t)w.q.s * A.b.table_stride;
+    const uint32_t page_bytes = (uint32_t)A.c.n_kv * page * d;   // of all heads: at most 2^26
+    const float scale2 = fabsf(A.scale2);
 
-    // The pages of a tile's four granules and their scales, through the scalar
-    // cache: uniform over the wave, and off the counter that the K and V loads
-    // wait on.  Granules past the end: some page of the sequence, masked.
-    const const_i32 table = (const_i32)(A.b.table + (size_t)w.q.s * A.b.table_stride);
-    const const_f32 k_scale = (const_f32)A.c.k_scale, v_scale = (const_f32)A.c.v_scale;
-    auto gran = [&](int tile, int i) {
-        const int gi = tile * (kTile / kGran) + i;
-        return gi < last_gran ? gi : last_gran;
-    };
-    auto lookup = [&](int tile, int (&id)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) id[i] = ctx > 0 ? table[gran(tile, i) * kGran >> shift] : -1;
-    };
-    auto known = [&](int id) { return id >= 0 && id < A.c.n_pages; };
-    auto scales = [&](const int (&id)[4], float (&ks)[4], float (&vs)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const size_t at = (size_t)(known(id[i]) ? id[i] : 0) * A.c.n_kv + w.h;
-            ks[i] = known(id[i]) ? k_scale[at] : __builtin_nanf("");
-            vs[i] = known(id[i]) ? v_scale[at] : __builtin_nanf("");
+    // looks up the granules of `tiles` tiles from seg on; past the sequence's
+    // end: its last granule, masked later
+    auto fill = [&](int seg, int tiles) {
+        for (int i = threadIdx.x; i < tiles * (kTile / kGran); i += kAttThreads) {
+            int gi = seg * (kTile / kGran) + i;
+            gi = gi < last_gran ? gi : last_gran;
+            int id = ctx > 0 ? table[gi * kGran >> shift] : -1;
+            const bool known = id >= 0 && id < A.c.n_pages;
+            id = known ? id : 0;
+            const size_t si = (size_t)id * A.c.n_kv + w.h;
+            const float ks = A.c.k_scale[si], vs = A.c.v_scale[si];
+            const size_t off = (size_t)id * page_bytes + (size_t)(w.h * page * d) + (size_t)((gi * kGran & (page - 1)) * d);
+            const float nan = __builtin_nanf("");
+            grans[i] = Gran{(uint32_t)off, (uint32_t)(off >> 32), known ? ks * scale2 : nan,
+                            !known ? nan : vs < 0x1p-64f ? kZeroLog : log2_fast(vs)};
         }
-    };
-    auto gran_base = [&](const int (&id)[4], int tile, int i) {   // i: per lane
-        int p = pick(id, i);
-        p = known(p) ? p : 0;
-        return ((size_t)p * A.c.n_kv + w.h) * (size_t)(page * d) + (size_t)((gran(tile, i) * kGran & (page - 1)) * d);
     };
 
     // byte offsets of this lane's pieces inside a granule
     int ko[KJ];
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
-        const int ch = j * 4 + g < dc ? j * 4 + g : dc - 1;   // beyond d: any finite code, its query is 0
+        const int ch = FULL || j * 4 + g < dc ? j * 4 + g : dc - 1;   // beyond d: any finite code, its query is 0
         ko[j] = ch * 64 + (n16 & 3) * 16;
     }
-    const int gk = n16 >> 2;
     u32x4 kc[4][KJ], vc[4 * KJ];
-    auto load_k = [&](const int (&id)[4], int tile) {
-        const uint8_t* at = A.c.k + gran_base(id, tile, gk);
+    auto at = [](const uint8_t* pool, const Gran& e) { return pool + (((size_t)e.hi << 32) | e.lo); };
+    auto load_k = [&](const Gran& e) {
+        const uint8_t* p = at(A.c.k, e) + (FULL ? ko[0] : 0);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < KJ; ++j) kc[t][j] = ld16_stream(at + t * 4 * d + ko[j]);
+            for (int j = 0; j < KJ; ++j) kc[t][j] = ld16_stream(p + t * 4 * d + (FULL ? j * 256 : ko[j]));
     };
-    auto load_v = [&](const int (&id)[4], int tile) {
-        const uint8_t* at = A.c.v + gran_base(id, tile, g) + n16 * 16;
+    auto load_v = [&](const Gran& e) {
+        const uint8_t* p = at(A.c.v, e) + n16 * 16;
 #pragma unroll
-        for (int k = 0; k < 4 * KJ; ++k) vc[k] = ld16_stream(at + (k < dc ? k : dc - 1) * 256);
+        for (int k = 0; k < 4 * KJ; ++k) vc[k] = ld16_stream(p + (FULL || k < dc ? k : dc - 1) * 256);
     };
 
-    int tile = w.t0 + wave;
-    int id[4];
-    float ks[4], vs[4];
-    if (tile < w.t1) {
-        lookup(tile, id);
-        load_k(id, tile);
-        load_v(id, tile);
-        scales(id, ks, vs);
-        lookup(tile + kAttWaves, id);
-    }
-
-    // this lane's query: position, and the operand's fragments
+    // this lane's query: position, and the operand's fragments (negated for a
+    // negative scale, so that kx is never below 0)
     const int my_row = w.row_tile * ROWS + n16;
     const bool live = my_row < rows_all;
     const int my_tok = live ? my_row / group : 0, my_head = w.h * group + (live ? my_row - my_tok * group : 0);
@@ -255,6 +250,7 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     f16x8 qf[2 * KJ];
     {
         const h16* qr = A.q + (size_t)(w.q.row0 + my_tok) * A.q_stride + (size_t)my_head * d;
+        const uint32_t sign = A.scale2 < 0.f ? 0x80008000u : 0u;
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
             const int ch = j * 4 + g;
@@ -263,8 +259,8 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
                 a = ld16(qr + ch * 16);
                 e = ld16(qr + ch * 16 + 8);
             }
-            qf[2 * j] = __builtin_bit_cast(f16x8, a);
-            qf[2 * j + 1] = __builtin_bit_cast(f16x8, e);
+            qf[2 * j] = __builtin_bit_cast(f16x8, a ^ sign);
+            qf[2 * j + 1] = __builtin_bit_cast(f16x8, e ^ sign);
         }
     }
     // positions that every row of this workgroup attends to need no mask
@@ -276,164 +272,166 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     // and outside these, none attends
     const int any_to = first + row_b, any_from = A.window > 0 ? first + row_a - A.window + 1 : 0;
 
-    float R = kNone, M = kNone, l = 0.f;
+    float M = kNone, l = 0.f;
     f32x4 O[4 * KJ];
 #pragma unroll
     for (int k = 0; k < 4 * KJ; ++k) O[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    for (; tile < w.t1; tile += kAttWaves) {
-        const int next = tile + kAttWaves;
-        f32x4 S[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < KJ; ++j) {
-                f16x2 c[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) Codes<FMT>::to_f16(kc[t][j][i], c[2 * i], c[2 * i + 1]);
-                f16x8 a = {c[0].x, c[0].y, c[1].x, c[1].y, c[2].x, c[2].y, c[3].x, c[3].y};
-                f16x8 e = {c[4].x, c[4].y, c[5].x, c[5].y, c[6].x, c[6].y, c[7].x, c[7].y};
-                S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[2 * j], S[t], 0, 0, 0);
-                S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, qf[2 * j + 1], S[t], 0, 0, 0);
-            }
+    for (int seg = w.t0; seg < w.t1; seg += kSegTiles) {
+        const int tiles = w.t1 - seg < kSegTiles ? w.t1 - seg : kSegTiles;
+        if (seg != w.t0) __syncthreads();   // the last segment's entries are no longer read
+        fill(seg, tiles);
+        __syncthreads();
+        int i = wave;   // this wave's tile in the segment
+        Gran e;         // of the lane's V granule
+        if (i < tiles) {
+            load_k(grans[i * 4 + (n16 >> 2)]);
+            e = grans[i * 4 + g];
+            load_v(e);
         }
-        if (next < w.t1) load_k(id, next);
-
-        const float kx = pick(ks, g) * A.scale2, vl = pick(vs, g), lv = log2_fast(vl);
-        const int key0 = tile * kTile + g * kGran;   // position of this lane's first key
-        const bool edge = tile * kTile < free_from || tile * kTile + kTile - 1 > free_to;
-        f16x8 ph[2], pl[2];   // the weights' leading and following halves: to 22 bits, at four more products a tile
-        float x[16];
+        for (; i < tiles; i += kAttWaves) {
+            const int next = i + kAttWaves;
+            const float kx = e.kx, lv = e.lv;
+            f32x4 S[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = S[i / 4][i % 4] * kx;
-        if (edge) {
+            for (int t = 0; t < 4; ++t) {
+                S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = key0 + i >= lo && key0 + i <= pos ? x[i] : -__builtin_inff();
-        }
-        float mx = x[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[i]);
-        const float mr = max_groups(mx), mw = max_groups(mx + lv);
-        if (__ballot(mr > R + kSlack || mw > M + kSlack)) {
-            const float r = fmaxf(R, mr), m = fmaxf(fmaxf(M, mw), r - kFloor);
-            l *= exp2_fast(R - r);
-            const float f = exp2_fast(M - m);
-#pragma unroll
-            for (int k = 0; k < 4 * KJ; ++k) O[k] *= f;
-            R = r;
-            M = m;
-        }
-        const float up = vl * exp2_fast(R - M + kLift);
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float p = exp2_fast(x[i] - R);
-            sum += p;
-            float wt = p * up;
-            if (edge) wt = key0 + i >= lo && key0 + i <= pos ? wt : 0.f;
-            const f16 hi = (f16)wt;
-            ph[i / 8][i % 8] = hi;
-            pl[i / 8][i % 8] = (f16)(wt - (float)hi);
-        }
-        l += sum;
-        // fp8 slots that no row here attends to may hold NaN, which a zero weight would not silence
-        if (FMT == 1 && (tile * kTile < any_from || tile * kTile + kTile - 1 > any_to)) {
-#pragma unroll
-            for (int k = 0; k < 4 * KJ; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k0 = key0 + 4 * i;   // the word's tokens are k0 .. k0 + 3
-                    const int have = any_to + 1 - k0, skip = any_from - k0;
-                    uint32_t v = vc[k][i];
-                    v = have >= 4 ? v : have <= 0 ? 0u : v & ((1u << (8 * have)) - 1u);
-                    v = skip <= 0 ? v : skip >= 4 ? 0u : v & ~((1u << (8 * skip)) - 1u);
-                    vc[k][i] = v;
+                for (int j = 0; j < KJ; ++j) {
+                    S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8<FMT>(kc[t][j].x, kc[t][j].y), qf[2 * j], S[t], 0, 0, 0);
+                    S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes8<FMT>(kc[t][j].z, kc[t][j].w), qf[2 * j + 1], S[t], 0, 0, 0);
                 }
-        }
+            }
+            if (next < tiles) {
+                load_k(grans[next * 4 + (n16 >> 2)]);
+                e = grans[next * 4 + g];
+            }
+
+            const int tile0 = (seg + i) * kTile, key0 = tile0 + g * kGran;   // the tile's first key, and this lane's
+            const bool edge = tile0 < free_from || tile0 + kTile - 1 > free_to;
+            float mx;
+            if (edge) {   // scores of keys that the row does not attend to become -infinity
 #pragma unroll
-        for (int k = 0; k < 4 * KJ; ++k) {
-            f16x2 c[8];
+                for (int k = 0; k < 16; ++k) {
+                    const float x = S[k / 4][k % 4] * kx;
+                    S[k / 4][k % 4] = key0 + k >= lo && key0 + k <= pos ? x : -__builtin_inff();
+                }
+            }
+            mx = S[0][0];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) Codes<FMT>::to_f16(vc[k][i], c[2 * i], c[2 * i + 1]);
-            f16x8 a = {c[0].x, c[0].y, c[1].x, c[1].y, c[2].x, c[2].y, c[3].x, c[3].y};
-            f16x8 e = {c[4].x, c[4].y, c[5].x, c[5].y, c[6].x, c[6].y, c[7].x, c[7].y};
-            O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[0], O[k], 0, 0, 0);
-            O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, ph[1], O[k], 0, 0, 0);
-            O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[0], O[k], 0, 0, 0);
-            O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(e, pl[1], O[k], 0, 0, 0);
-        }
-        if (next < w.t1) {
-            load_v(id, next);
-            scales(id, ks, vs);
-            lookup(next + kAttWaves, id);
+            for (int k = 1; k < 16; ++k) mx = fmaxf(mx, S[k / 4][k % 4]);
+            mx = max_groups(fmaf(mx, edge ? 1.f : kx, lv));
+            if (__ballot(mx > M + kSlack)) {
+                const float m = fmaxf(M, mx), f = exp2_fast(M - m);
+                l *= f;
+#pragma unroll
+                for (int k = 0; k < 4 * KJ; ++k) O[k] *= f;
+                M = m;
+            }
+            // the weights' leading and following halves: to 22 bits, at twice the output's products
+            f16x8 ph[2], pl[2];
+            const float c = lv - M + kLift, by = edge ? 1.f : kx;
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                float wt = exp2_fast(fmaf(S[k / 4][k % 4], by, c));
+                if (edge) wt = key0 + k >= lo && key0 + k <= pos ? wt : 0.f;
+                sum += wt;
+                const f16 hi = (f16)wt;
+                ph[k / 8][k % 8] = hi;
+                pl[k / 8][k % 8] = (f16)(wt - (float)hi);
+            }
+            // a lane that attends to none of its keys adds none, whatever their page's scale is
+            l += edge && sum == 0.f ? 0.f : sum * exp2_fast(-lv);
+            // fp8 slots that no row here attends to may hold NaN, which a zero weight would not silence
+            if (FMT == 1 && (tile0 < any_from || tile0 + kTile - 1 > any_to)) {
+#pragma unroll
+                for (int k = 0; k < 4 * KJ; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int k0 = key0 + 4 * j;   // the word's tokens are k0 .. k0 + 3
+                        const int have = any_to + 1 - k0, skip = any_from - k0;
+                        uint32_t v = vc[k][j];
+                        v = have >= 4 ? v : have <= 0 ? 0u : v & ((1u << (8 * have)) - 1u);
+                        v = skip <= 0 ? v : skip >= 4 ? 0u : v & ~((1u << (8 * skip)) - 1u);
+                        vc[k][j] = v;
+                    }
+            }
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k) {
+                const f16x8 a = codes8<FMT>(vc[k].x, vc[k].y), b = codes8<FMT>(vc[k].z, vc[k].w);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[0], O[k], 0, 0, 0);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, ph[1], O[k], 0, 0, 0);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[0], O[k], 0, 0, 0);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pl[1], O[k], 0, 0, 0);
+            }
+            if (next < tiles) load_v(e);
         }
     }
 
-    // Join the waves that had tiles: statistics first, then every wave brings
-    // its outputs to the common reference and the workgroup adds them up.
+    // Join the waves that had tiles: references first, then every wave brings
+    // its sums to the common one and the workgroup adds them up.
     const int parts = w.t1 - w.t0 < kAttWaves ? w.t1 - w.t0 : kAttWaves;
-    float* outs = lds;                                   // [parts][ROWS][LD]
-    float* stat = lds + kAttWaves * ROWS * LD;           // [parts][3][ROWS]: R, M, l
-    float* done = stat + kAttWaves * 3 * ROWS;           // [3][ROWS]: the workgroup's
+    static_assert(kAttWaves * ROWS * LD * 4 >= kSegGrans * (int)sizeof(Gran), "the statistics lie behind the granules");
+    float* outs = lds;                                   // [parts][ROWS][LD], over the granules
+    float* stat = lds + kAttWaves * ROWS * LD;           // [parts][2][ROWS]: M, l
+    float* done = stat + kAttWaves * 2 * ROWS;           // [2][ROWS]: the workgroup's
     const int rows = rows_all - w.row_tile * ROWS < ROWS ? rows_all - w.row_tile * ROWS : ROWS;
     l = sum_groups(l);
     if (g == 0 && wave < parts) {
-        stat[(wave * 3 + 0) * ROWS + n16] = R;
-        stat[(wave * 3 + 1) * ROWS + n16] = M;
-        stat[(wave * 3 + 2) * ROWS + n16] = l;
+        stat[(wave * 2 + 0) * ROWS + n16] = M;
+        stat[(wave * 2 + 1) * ROWS + n16] = l;
     }
     __syncthreads();
     if (wave < parts) {
-        float Rr = kNone, Mr = kNone, sum = 0.f;
-        for (int p = 0; p < parts; ++p) {
-            Rr = fmaxf(Rr, stat[(p * 3 + 0) * ROWS + n16]);
-            Mr = fmaxf(Mr, stat[(p * 3 + 1) * ROWS + n16]);
-        }
+        float Mr = kNone;
+        for (int p = 0; p < parts; ++p) Mr = fmaxf(Mr, stat[p * 2 * ROWS + n16]);
         const float f = exp2_fast(M - Mr);
 #pragma unroll
         for (int k = 0; k < 4 * KJ; ++k)
             *reinterpret_cast<f32x4*>(&outs[(wave * ROWS + n16) * LD + k * 16 + g * 4]) = O[k] * f;
         if (wave == 0 && g == 0) {
+            float sum = 0.f;
             for (int p = 0; p < parts; ++p)
-                sum = fmaf(stat[(p * 3 + 2) * ROWS + n16], exp2_fast(stat[(p * 3 + 0) * ROWS + n16] - Rr), sum);
-            done[n16] = Rr;
-            done[ROWS + n16] = Mr;
-            done[2 * ROWS + n16] = sum;
+                sum = fmaf(stat[(p * 2 + 1) * ROWS + n16], exp2_fast(stat[p * 2 * ROWS + n16] - Mr), sum);
+            done[n16] = Mr;
+            done[ROWS + n16] = sum;
         }
     }
     __syncthreads();
 
-    // four outputs of a row, from its sum of weights and references in `done`
+    // four outputs of a row, from its sum of weights and reference in `done`
     auto emit = [&](int r, int i, f32x4 o) {
         const int gr = w.row_tile * ROWS + r, tok = gr / group, head = w.h * group + gr - tok * group;
-        const size_t at = (size_t)(w.q.row0 + tok) * A.n_head + head;
+        const size_t to = (size_t)(w.q.row0 + tok) * A.n_head + head;
         const bool empty = first + tok < 0;
-        const float Rr = done[r], sum = done[2 * ROWS + r];
+        const float sum = done[ROWS + r];
         // no weight at all although there are keys: every score was -infinity
-        const float f = sum == 0.f ? __builtin_nanf("") : exp2_fast(done[ROWS + r] - Rr - kLift) / sum;
+        const float f = sum == 0.f ? __builtin_nanf("") : 1.f / sum;
         typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
         f16x4 v;
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = empty ? (f16)0.f : (f16)(o[k] * f);
-        *reinterpret_cast<f16x4*>(A.y + at * d + i) = v;
-        if (A.lse && i == 0) A.lse[at] = empty ? -__builtin_inff() : (Rr + log2_fast(sum)) * kLn2;
+        *reinterpret_cast<f16x4*>(A.y + to * d + i) = v;
+        if (A.lse && i == 0) A.lse[to] = empty ? -__builtin_inff() : (done[r] - kLift + log2_fast(sum)) * kLn2;
     };
-    constexpr int kSlotBytes = ROWS * (DP + 4) * 4;   // outputs [ROWS][DP], then R, M, l and nothing [4][ROWS]
-    const size_t step = (size_t)A.c.n_kv * kSlotBytes;
-    char* item = reinterpret_cast<char*>(A.part) + ((size_t)w.slot * A.c.n_kv + w.h) * kSlotBytes;
-    const __amdgpu_buffer_rsrc_t mine = buf_rsrc(item + w.split * step, kSlotBytes);
+    constexpr int kSlotBytes = ROWS * (DP + 2) * 4;   // outputs [ROWS][DP], then M and l [2][ROWS]
+    // all pieces' results lie in one buffer of at most 2^25 bytes
+    const uint32_t step = (uint32_t)A.c.n_kv * kSlotBytes, item = ((uint32_t)w.slot * A.c.n_kv + w.h) * kSlotBytes;
+    const uint32_t mine = item + w.split * step;
+    const __amdgpu_buffer_rsrc_t part = buf_rsrc(A.part, kAttSlots * kSlotBytes);
     for (int e = threadIdx.x; e < rows * (DP / 4); e += kAttThreads) {
         const int r = e / (DP / 4), i = e % (DP / 4) * 4;
         if (i >= d) continue;
         f32x4 o = *reinterpret_cast<const f32x4*>(&outs[r * LD + i]);
         for (int p = 1; p < parts; ++p) o += *reinterpret_cast<const f32x4*>(&outs[(p * ROWS + r) * LD + i]);
         if (w.splits == 1) emit(r, i, o);
-        else st16_coherent(mine, (uint32_t)(r * DP + i) * 4, o);
+        else st16_coherent(part, mine + (uint32_t)(r * DP + i) * 4, o);
     }
     if (w.splits == 1) return;
-    for (int e = threadIdx.x; e < 3 * ROWS / 4; e += kAttThreads)
-        st16_coherent(mine, (uint32_t)(ROWS * DP + e * 4) * 4, *reinterpret_cast<const f32x4*>(&done[e * 4]));
+    if (threadIdx.x < 2 * ROWS / 4)
+        st16_coherent(part, mine + (uint32_t)(ROWS * DP + threadIdx.x * 4) * 4,
+                      *reinterpret_cast<const f32x4*>(&done[threadIdx.x * 4]));
 
     // the last of the item's pieces to arrive joins them, in their order
     uint32_t* ctr = A.ctr + ((size_t)w.slot * A.c.n_kv + w.h) * kAttCtrStride;
@@ -442,68 +440,74 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     if (threadIdx.x == 0) s_last = fetch_add_acq_rel(ctr, 1u) == (uint32_t)(w.splits - 1);
     __syncthreads();
     if (!s_last) return;
-    // each row's references and sum over the pieces: a row's lanes take a piece each
-    constexpr int kRowLanes = kAttThreads / ROWS;
+    // Each row's reference and sum over the pieces: sixteen lanes a row, a
+    // piece each.  The first outputs are already on their way meanwhile.
+    constexpr int kRowLanes = kAttThreads / ROWS, kBatch = 32;
+    float* fac = outs;   // [kJoin][ROWS]: what each piece is multiplied by
+    constexpr int kJoin = kAttWaves * LD < 256 ? kAttWaves * LD / kBatch * kBatch : 256;   // pieces whose factors fit
+    auto load = [&](f32x4 (&v)[kBatch], int p0, int r, int i) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            v[k] = ld16_coherent(part, (uint32_t)(r * DP + i) * 4, item + (p0 + k < w.splits ? p0 + k : w.splits - 1) * step);
+    };
+    f32x4 v[kBatch];
+    const int e0 = threadIdx.x, r0 = e0 / (DP / 4), i0 = e0 % (DP / 4) * 4;
+    load(v, 0, r0 < ROWS ? r0 : 0, i0);
+    const int sr = threadIdx.x / kRowLanes, sj = threadIdx.x % kRowLanes;
     {
-        const int r = threadIdx.x / kRowLanes, j = threadIdx.x % kRowLanes;
-        float Rr = kNone, Mr = kNone, sum = 0.f;
-        for (int p = j; p < w.splits; p += kRowLanes) {
-            const float* at = reinterpret_cast<const float*>(item + p * step) + ROWS * DP + r;
-            const float pr = ld_coherent(at), pm = ld_coherent(at + ROWS), ps = ld_coherent(at + 2 * ROWS);
-            const float nr = fmaxf(Rr, pr);
-            sum = sum * exp2_fast(Rr - nr) + ps * exp2_fast(pr - nr);
-            Rr = nr;
-            Mr = fmaxf(Mr, pm);
+        float Mr = kNone, sum = 0.f;
+        for (int p = sj; p < w.splits; p += kRowLanes) {
+            const uint32_t st = item + p * step + (ROWS * DP + sr) * 4;
+            const float pm = ld4_coherent(part, st), ps = ld4_coherent(part, st + ROWS * 4);
+            const float m = fmaxf(Mr, pm);
+            sum = sum * exp2_fast(Mr - m) + ps * exp2_fast(pm - m);
+            Mr = m;
         }
 #pragma unroll
         for (int off = 1; off < kRowLanes; off <<= 1) {
-            const float pr = __shfl_xor(Rr, off, kWave), ps = __shfl_xor(sum, off, kWave);
-            const float nr = fmaxf(Rr, pr);
-            sum = sum * exp2_fast(Rr - nr) + ps * exp2_fast(pr - nr);
-            Rr = nr;
-            Mr = fmaxf(Mr, __shfl_xor(Mr, off, kWave));
+            const float pm = __shfl_xor(Mr, off, kWave), ps = __shfl_xor(sum, off, kWave);
+            const float m = fmaxf(Mr, pm);
+            sum = sum * exp2_fast(Mr - m) + ps * exp2_fast(pm - m);
+            Mr = m;
         }
-        if (j == 0) {
-            done[r] = Rr;
-            done[ROWS + r] = Mr;
-            done[2 * ROWS + r] = sum;
+        if (sj == 0) {
+            done[sr] = Mr;
+            done[ROWS + sr] = sum;
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < rows * (DP / 4); e += kAttThreads) {
+    for (int e = e0; e < ROWS * (DP / 4); e += kAttThreads) {
         const int r = e / (DP / 4), i = e % (DP / 4) * 4;
-        if (i >= d) continue;
-        const float Mr = done[ROWS + r];
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int p = 0; p < w.splits; p += 16) {   // sixteen pieces' loads at a time
-            f32x4 v[16];
-            float m[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const char* at = item + (p + k < w.splits ? p + k : p) * step;
-                v[k] = ld16_coherent(buf_rsrc(at, kSlotBytes), (uint32_t)(r * DP + i) * 4);
-                m[k] = ld_coherent(reinterpret_cast<const float*>(at) + ROWS * DP + ROWS + r);
+        for (int p0 = 0; p0 < w.splits; p0 += kJoin) {
+            const int np = w.splits - p0 < kJoin ? w.splits - p0 : kJoin;
+            if (e == e0 || w.splits > kJoin) {   // otherwise the factors are still there
+                __syncthreads();
+                for (int p = sj; p < np; p += kRowLanes)
+                    fac[p * ROWS + sr] = exp2_fast(ld4_coherent(part, item + (p0 + p) * step + (ROWS * DP + sr) * 4) - done[sr]);
+                __syncthreads();
             }
+            for (int p = 0; p < np; p += kBatch) {
+                if (e != e0 || p0 + p > 0) load(v, p0 + p, r, i);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float f = p + k < w.splits ? exp2_fast(m[k] - Mr) : 0.f;
-                if (p + k < w.splits) o += v[k] * f;
+                for (int k = 0; k < kBatch; ++k)
+                    if (p + k < np) o += v[k] * fac[(p + k) * ROWS + r];
             }
         }
-        emit(r, i, o);
+        if (r < rows && i < d) emit(r, i, o);
     }
     if (threadIdx.x == 0) st_flag(ctr, 0u);
 }
 
 // A workgroup takes units until there are none: whatever the lengths on the
 // device say, every piece of every item runs, and the counters end at zero.
-template <int FMT, int KJ>
-__global__ __launch_bounds__(kAttThreads, KJ == 4 ? 1 : KJ == 2 ? 2 : 3) void k_attend(AttArgs A) {
+template <int FMT, int KJ, bool FULL>
+__global__ __launch_bounds__(kAttThreads, KJ == 4 ? 1 : 2) void k_attend(AttArgs A) {
     AttUnit w;
     w.h = blockIdx.x;
     const int units = att_plan(A, blockIdx.y, w);
     for (int u = blockIdx.y; u < units;) {
-        attend_unit<FMT, KJ>(A, w);
+        attend_unit<FMT, KJ, FULL>(A, w);
         u += gridDim.y;
         if (u < units) {
             __syncthreads();   // the next unit uses the same shared memory
@@ -523,7 +527,7 @@ static long long att_row_tiles(const KvBatch& b, int group) {
 size_t kv_attend_zero_bytes() { return (size_t)kAttSlots * kAttCtrStride * 4; }
 
 size_t kv_attend_bytes(int, int, int, int, int, int d) {
-    return kv_attend_zero_bytes() + (size_t)kAttSlots * kAttRows * (64 * att_kj(d) + 4) * 4;
+    return kv_attend_zero_bytes() + (size_t)kAttSlots * kAttRows * (64 * att_kj(d) + 2) * 4;
 }
 
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
@@ -540,19 +544,21 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, lo
     // heads side by side: the row tiles that read one head's pages run on one
     // XCD where the heads are a multiple of 8, and share its L2
     const dim3 grid(c.n_kv, (unsigned)units);
-    const size_t shm = ((size_t)kAttWaves * (64 * kj + 4 + 3) + 3) * kAttRows * 4;
+    const size_t joins = ((size_t)kAttWaves * (64 * kj + 4 + 2) + 2) * kAttRows * 4, looks = kSegGrans * sizeof(Gran);
+    const size_t shm = joins > looks ? joins : looks;
+    const bool full = c.d == 64 * kj;
     hipError_t e = hipSuccess;
-#define PI_ATT(F, K)                                                                               \
+#define PI_ATT(F, K, U)                                                                            \
     do {                                                                                           \
         if (shm > 65536)                                                                           \
-            e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<F, K>),                \
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<F, K, U>),             \
                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);         \
-        if (e == hipSuccess) hipLaunchKernelGGL((k_attend<F, K>), grid, dim3(kAttThreads), shm, s, A); \
+        if (e == hipSuccess) hipLaunchKernelGGL((k_attend<F, K, U>), grid, dim3(kAttThreads), shm, s, A); \
     } while (0)
-#define PI_ATT_D(F)                \
-    if (kj == 1) PI_ATT(F, 1);      \
-    else if (kj == 2) PI_ATT(F, 2); \
-    else PI_ATT(F, 4)
+#define PI_ATT_D(F)                                                          \
+    if (kj == 1) { if (full) PI_ATT(F, 1, true); else PI_ATT(F, 1, false); }  \
+    else if (kj == 2) { if (full) PI_ATT(F, 2, true); else PI_ATT(F, 2, false); } \
+    else { if (full) PI_ATT(F, 4, true); else PI_ATT(F, 4, false); }
     if (c.fmt == 0) { PI_ATT_D(0); } else { PI_ATT_D(1); }
 #undef PI_ATT_D
 #undef PI_ATT
