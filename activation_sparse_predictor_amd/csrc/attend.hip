@@ -8,10 +8,10 @@
 // cache a second time; ks multiplies the fp32 score and vs the weight.  A vs
 // lies anywhere between 2^-31 and 2^9, so the running reference M follows the
 // largest weight with its scale, max (x + log2 vs):
-//   w_j = 2^(x_j + log2 vs_j - M + 14),  l = sum w_j / vs_j,  y = sum w_j code_j / l.
-// M moves only when a maximum is more than 1 above it, so w stays within 2^15
-// and fp16 holds it, down to 2^-39 of the row's largest; l is summed in fp32,
-// where its terms 2^(x - M + 14) always fit.  A page of zeros (vs = 0) takes part
+//   w_j = 2^(x_j + log2 vs_j - M + 15.9),  l = sum w_j / vs_j,  y = sum w_j code_j / l.
+// So w is at most 2^15.9, just inside fp16, which holds it down to 2^-40 of the
+// row's largest; l is summed in fp32, where its terms 2^(x - M + 15.9) always
+// fit.  A page of zeros (vs = 0) takes part
 // as vs = 2^-64: its weights count, and its values stay far below fp16's range.
 //
 // Operands.  A wave takes 64 keys (four granules of 16) a step, as the rows of
@@ -22,167 +22,16 @@
 // operand of the output's products, all share one page, and the V operand is
 // 16 contiguous bytes (a dimension's 16 tokens).  So nothing is shuffled or
 // staged between the two products, and a lane has one ks and one vs a step.
-#include "kv.hpp"
+#include "attend.hpp"
 
 namespace pi {
 
-constexpr int kTile = 64;          // keys a wave takes at a time
 constexpr int kAttWaves = 4;
 constexpr int kAttThreads = kAttWaves * kWave;
-constexpr int kAttRows = 16;       // query rows of a workgroup
-constexpr int kAttMinTiles = 4;    // fewest tiles worth a workgroup of their own
+constexpr int kAttRows = 16;   // query rows of a workgroup
+constexpr int kMinTiles = 4;   // fewest tiles worth a workgroup of their own
 // workgroups the work is split into: those that run at once, by the registers
-__host__ __device__ constexpr int att_target(int kj) { return kj == 4 ? 256 : 512; }
-constexpr int kAttSlots = 2 * 512;   // pieces of split items: ceil(t / C) < 2 t / C where t > C
-constexpr int kAttCtrStride = 16;  // words between arrival counters
-
-constexpr float kLift = 14.f, kSlack = 1.f, kZeroLog = -64.f, kNone = -1e30f, kLn2 = 0.69314718055994531f;
-
-// max over the lanes that hold the same query (lane ^ 16, lane ^ 32)
-__device__ __forceinline__ float max_groups(float v) {
-    const uint32_t u = __float_as_uint(v);
-    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    v = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
-    const uint32_t w = __float_as_uint(v);
-    const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float sum_groups(float v) { return add_swap<32>(add_swap<16>(v)); }
-
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float log2_fast(float x) { return __builtin_amdgcn_logf(x); }
-
-struct AttArgs {
-    KvCache c;
-    KvBatch b;
-    const h16* q;
-    long long q_stride;
-    int n_head, group, window, target;
-    float scale2;   // scale * log2(e)
-    h16* y;
-    float* lse;
-    uint32_t* ctr;
-    float* part;
-};
-
-// What a workgroup works on: `rows` query rows of a sequence from row0 on,
-// tiles [t0, t1), head h, piece `split` of `splits`.
-struct AttUnit {
-    Seq q;
-    int h, row_tile, t0, t1, split, splits, slot;
-};
-
-// First tile of a sequence that any of its rows attends to, and the tiles in all (at least one).
-__device__ __forceinline__ int att_first_tile(const Seq& q, int window) {
-    const int lo = q.ctx - q.n - window + 1;
-    return window > 0 && lo > 0 ? lo / kTile : 0;
-}
-__device__ __forceinline__ int att_tiles(const Seq& q, int window) {
-    const int n = (q.ctx + kTile - 1) / kTile - att_first_tile(q, window);
-    return n > 0 ? n : 1;
-}
-
-// Splits the whole batch's tiles over about kAttTarget workgroups: C tiles a
-// workgroup, the same for every sequence, from the lengths as they are on the
-// device.  Each item (sequence, row tile) becomes ceil(tiles / C) pieces of
-// nearly equal size, for each head.  Every wave computes it for itself: a
-// round of 64 sequences is one round of loads.  Fills in unit `item`, if there
-// is one, and returns how many there are (of each head).  With at most 2^24
-// rows and 2^10 sequences, whatever the lengths say, the sums stay below 2^31.
-__device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) {
-    constexpr int ROWS = kAttRows;
-    const KvBatch& b = A.b;
-    float all = 0.f, items = 0.f;   // C only has to be the same everywhere
-    Seq q{-1, 0, 0, 0};
-    int rt = 0, tiles = 1;
-    for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
-        const int s = s0 + lane_id();
-        rt = 0;
-        if (s < b.n_seq) {
-            q = kv_seq(b, s);
-            rt = (q.n * A.group + ROWS - 1) / ROWS;
-            tiles = att_tiles(q, A.window);
-        }
-        all += group_sum<64>((float)rt * (float)tiles);
-        items += group_sum<64>((float)rt);
-    }
-    const float room = (float)A.target / (float)A.c.n_kv;   // workgroups a head has
-    const float want = all / room * 1.001f;                 // a little above: the slots rest on it
-    int C = want < kAttMinTiles ? kAttMinTiles : (int)want + 1;
-    if (b.n_seq <= kWave && items <= room) {
-        // All items can run at once: the smallest C (to a sixteenth) whose rounded-up pieces still do.
-        for (int i = 0; i < 24; ++i) {
-            if (group_sum<64>((float)(rt * ((tiles + C - 1) / C))) <= room) break;
-            C += C / 16 + 1;
-        }
-    }
-    int before = 0, slots = 0;
-    for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
-        const int s = s0 + lane_id();
-        if (b.n_seq > kWave) {   // otherwise the first loop's values are still there
-            rt = 0;
-            if (s < b.n_seq) {
-                q = kv_seq(b, s);
-                rt = (q.n * A.group + ROWS - 1) / ROWS;
-                tiles = att_tiles(q, A.window);
-            }
-        }
-        const int ns = (tiles + C - 1) / C;
-        const int upto = before + wave_scan(rt * ns), held = ns > 1 ? rt * ns : 0;
-        const int slots_upto = slots + wave_scan(held);
-        const uint64_t hit = __ballot(upto > item);
-        if (hit && before <= item) {
-            const int l = __builtin_ctzll(hit);
-            w.q.s = s0 + l;
-            w.q.row0 = __builtin_amdgcn_readlane(q.row0, l);
-            w.q.n = __builtin_amdgcn_readlane(q.n, l);
-            w.q.ctx = __builtin_amdgcn_readlane(q.ctx, l);
-            w.splits = __builtin_amdgcn_readlane(ns, l);
-            const int T = __builtin_amdgcn_readlane(tiles, l);
-            const int inside = item - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(rt, l) * w.splits);
-            w.row_tile = inside / w.splits;
-            w.split = inside - w.row_tile * w.splits;
-            w.slot = __builtin_amdgcn_readlane(slots_upto, l) - __builtin_amdgcn_readlane(held, l) +
-                     w.row_tile * w.splits;   // the item's first slot
-            const int each = T / w.splits, more = T - each * w.splits;
-            w.t0 = att_first_tile(w.q, A.window) + w.split * each + (w.split < more ? w.split : more);
-            w.t1 = w.t0 + each + (w.split < more ? 1 : 0);
-        }
-        before = __builtin_amdgcn_readlane(upto, kWave - 1);
-        slots = __builtin_amdgcn_readlane(slots_upto, kWave - 1);
-    }
-    return before;
-}
-
-// 16 bytes of a piece's results, written and read past the caches that other
-// XCDs do not see (as the agent-scope atomics do).
-__device__ __forceinline__ void st16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at, f32x4 v) {
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, (int)at, 0, 16);
-}
-__device__ __forceinline__ f32x4 ld16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t from) {
-    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, (int)from, 16));
-}
-__device__ __forceinline__ float ld4_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at) {
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (int)at, 0, 16));
-}
-
-// A granule of the sequence: where its bytes start in the pools, and its
-// page's scales as the loop uses them.
-struct Gran {
-    uint32_t lo, hi;   // byte offset
-    float kx, lv;      // ks * |scale| * log2(e);  log2 vs
-};
-constexpr int kSegTiles = 128;   // tiles whose granules are looked up at a time
-constexpr int kSegGrans = kSegTiles * (kTile / kGran);
-
-// Eight codes of two words as fp16.
-template <int FMT>
-__device__ __forceinline__ f16x8 codes8(uint32_t a, uint32_t b) {
-    f16x2 c[4];
-    Codes<FMT>::to_f16(a, c[0], c[1]);
-    Codes<FMT>::to_f16(b, c[2], c[3]);
-    return f16x8{c[0].x, c[0].y, c[1].x, c[1].y, c[2].x, c[2].y, c[3].x, c[3].y};
-}
+constexpr int single_target(int kj) { return kj == 4 ? 256 : 512; }
 
 // KJ: 64-dimension steps of a head; FULL: d is all of them.
 template <int FMT, int KJ, bool FULL>
@@ -193,31 +42,8 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     Gran* grans = reinterpret_cast<Gran*>(lds);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int lane = lane_id(), n16 = lane & 15, g = lane >> 4;
-    const int d = FULL ? DP : A.c.d, dc = d / 16, page = A.c.page, group = A.group;
+    const int d = FULL ? DP : A.c.d, dc = d / 16, group = A.group;
     const int ctx = w.q.ctx, first = ctx - w.q.n, rows_all = w.q.n * group;
-    const int shift = __builtin_ctz(page), last_gran = ctx > 0 ? (ctx - 1) / kGran : 0;
-    const int32_t* table = A.b.table + (size_t)w.q.s * A.b.table_stride;
-    const uint32_t page_bytes = (uint32_t)A.c.n_kv * page * d;   // of all heads: at most 2^26
-    const float scale2 = fabsf(A.scale2);
-
-    // looks up the granules of `tiles` tiles from seg on; past the sequence's
-    // end: its last granule, masked later
-    auto fill = [&](int seg, int tiles) {
-        for (int i = threadIdx.x; i < tiles * (kTile / kGran); i += kAttThreads) {
-            int gi = seg * (kTile / kGran) + i;
-            gi = gi < last_gran ? gi : last_gran;
-            int id = ctx > 0 ? table[gi * kGran >> shift] : -1;
-            const bool known = id >= 0 && id < A.c.n_pages;
-            id = known ? id : 0;
-            const size_t si = (size_t)id * A.c.n_kv + w.h;
-            const float ks = A.c.k_scale[si], vs = A.c.v_scale[si];
-            const size_t off = (size_t)id * page_bytes + (size_t)(w.h * page * d) + (size_t)((gi * kGran & (page - 1)) * d);
-            const float nan = __builtin_nanf("");
-            grans[i] = Gran{(uint32_t)off, (uint32_t)(off >> 32), known ? ks * scale2 : nan,
-                            !known ? nan : vs < 0x1p-64f ? kZeroLog : log2_fast(vs)};
-        }
-    };
-
     // byte offsets of this lane's pieces inside a granule
     int ko[KJ];
 #pragma unroll
@@ -226,16 +52,15 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
         ko[j] = ch * 64 + (n16 & 3) * 16;
     }
     u32x4 kc[4][KJ], vc[4 * KJ];
-    auto at = [](const uint8_t* pool, const Gran& e) { return pool + (((size_t)e.hi << 32) | e.lo); };
     auto load_k = [&](const Gran& e) {
-        const uint8_t* p = at(A.c.k, e) + (FULL ? ko[0] : 0);
+        const uint8_t* p = gran_at(A.c.k, e) + (FULL ? ko[0] : 0);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int j = 0; j < KJ; ++j) kc[t][j] = ld16_stream(p + t * 4 * d + (FULL ? j * 256 : ko[j]));
     };
     auto load_v = [&](const Gran& e) {
-        const uint8_t* p = at(A.c.v, e) + n16 * 16;
+        const uint8_t* p = gran_at(A.c.v, e) + n16 * 16;
 #pragma unroll
         for (int k = 0; k < 4 * KJ; ++k) vc[k] = ld16_stream(p + (FULL || k < dc ? k : dc - 1) * 256);
     };
@@ -280,7 +105,7 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     for (int seg = w.t0; seg < w.t1; seg += kSegTiles) {
         const int tiles = w.t1 - seg < kSegTiles ? w.t1 - seg : kSegTiles;
         if (seg != w.t0) __syncthreads();   // the last segment's entries are no longer read
-        fill(seg, tiles);
+        att_lookup(A, w, d, seg * (kTile / kGran), tiles * (kTile / kGran), threadIdx.x, kAttThreads, grans);
         __syncthreads();
         int i = wave;   // this wave's tile in the segment
         Gran e;         // of the lane's V granule
@@ -321,7 +146,7 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
 #pragma unroll
             for (int k = 1; k < 16; ++k) mx = fmaxf(mx, S[k / 4][k % 4]);
             mx = max_groups(fmaf(mx, edge ? 1.f : kx, lv));
-            if (__ballot(mx > M + kSlack)) {
+            if (__ballot(mx > M)) {
                 const float m = fmaxf(M, mx), f = exp2_fast(M - m);
                 l *= f;
 #pragma unroll
@@ -343,19 +168,11 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
             }
             // a lane that attends to none of its keys adds none, whatever their page's scale is
             l += edge && sum == 0.f ? 0.f : sum * exp2_fast(-lv);
-            // fp8 slots that no row here attends to may hold NaN, which a zero weight would not silence
             if (FMT == 1 && (tile0 < any_from || tile0 + kTile - 1 > any_to)) {
 #pragma unroll
                 for (int k = 0; k < 4 * KJ; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int k0 = key0 + 4 * j;   // the word's tokens are k0 .. k0 + 3
-                        const int have = any_to + 1 - k0, skip = any_from - k0;
-                        uint32_t v = vc[k][j];
-                        v = have >= 4 ? v : have <= 0 ? 0u : v & ((1u << (8 * have)) - 1u);
-                        v = skip <= 0 ? v : skip >= 4 ? 0u : v & ~((1u << (8 * skip)) - 1u);
-                        vc[k][j] = v;
-                    }
+                    for (int j = 0; j < 4; ++j) vc[k][j] = keep_tokens(vc[k][j], key0 + 4 * j, any_from, any_to);
             }
 #pragma unroll
             for (int k = 0; k < 4 * KJ; ++k) {
@@ -371,7 +188,7 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
 
     // Join the waves that had tiles: references first, then every wave brings
     // its sums to the common one and the workgroup adds them up.
-    const int parts = w.t1 - w.t0 < kAttWaves ? w.t1 - w.t0 : kAttWaves;
+    const int mine_n = w.t1 - w.t0, parts = mine_n < 1 ? 1 : mine_n < kAttWaves ? mine_n : kAttWaves;
     static_assert(kAttWaves * ROWS * LD * 4 >= kSegGrans * (int)sizeof(Gran), "the statistics lie behind the granules");
     float* outs = lds;                                   // [parts][ROWS][LD], over the granules
     float* stat = lds + kAttWaves * ROWS * LD;           // [parts][2][ROWS]: M, l
@@ -505,49 +322,56 @@ template <int FMT, int KJ, bool FULL>
 __global__ __launch_bounds__(kAttThreads, KJ == 4 ? 1 : 2) void k_attend(AttArgs A) {
     AttUnit w;
     w.h = blockIdx.x;
-    const int units = att_plan(A, blockIdx.y, w);
+    const int units = att_plan<kAttRows>(A, blockIdx.y, w);
     for (int u = blockIdx.y; u < units;) {
         attend_unit<FMT, KJ, FULL>(A, w);
         u += gridDim.y;
         if (u < units) {
             __syncthreads();   // the next unit uses the same shared memory
-            att_plan(A, u, w);
+            att_plan<kAttRows>(A, u, w);
         }
     }
 }
 
-static int att_kj(int d) { return d <= 64 ? 1 : d <= 128 ? 2 : 4; }
-
-static long long att_row_tiles(const KvBatch& b, int group) {
-    const long long each = (long long)b.n_seq * (((long long)b.max_q * group + kAttRows - 1) / kAttRows);
-    const long long all = (long long)b.n_tok * group / kAttRows + b.n_seq;
-    return each < all ? each : all;
-}
-
 size_t kv_attend_zero_bytes() { return (size_t)kAttSlots * kAttCtrStride * 4; }
 
-size_t kv_attend_bytes(int, int, int, int, int, int d) {
-    return kv_attend_zero_bytes() + (size_t)kAttSlots * kAttRows * (64 * att_kj(d) + 2) * 4;
+// Sequences with more rows than this go to the prompt kernel.
+constexpr int kSingleRows = 64;
+
+size_t kv_attend_bytes(int, int, int max_q, int n_head, int n_kv, int d) {
+    const int kj = att_kj(d);
+    size_t rows = (size_t)2 * single_target(kj) * kAttRows;
+    if ((long long)max_q * (n_head / n_kv) > kSingleRows) {
+        const size_t more = (size_t)2 * 256 * prompt_rows(kj);
+        rows = more > rows ? more : rows;
+    }
+    return kv_attend_zero_bytes() + rows * (64 * kj + 2) * 4;
 }
 
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
                             float scale, int window, h16* y, float* lse, char* data, hipStream_t s) {
-    const int group = n_head / c.n_kv, kj = att_kj(c.d), target = att_target(kj);
-    AttArgs A{c, b, q, q_stride, n_head, group, window, target, scale * 1.4426950408889634f, y, lse,
+    const int group = n_head / c.n_kv, kj = att_kj(c.d);
+    const long long most_rows = (long long)b.max_q * group;
+    AttArgs A{c, b, q, q_stride, n_head, group, window, 0, 0x7FFFFFFF, single_target(kj), kMinTiles,
+              scale * 1.4426950408889634f, y, lse,
               reinterpret_cast<uint32_t*>(data), reinterpret_cast<float*>(data + kv_attend_zero_bytes())};
-    const long long items = att_row_tiles(b, group);
-    const long long cap = ((long long)b.table_stride * c.page + kTile - 1) / kTile;
-    const long long most = items * ((cap + kAttMinTiles - 1) / kAttMinTiles);
-    long long units = items + (target + c.n_kv - 1) / c.n_kv;
-    if (units > most) units = most;
-    if (units > 65535) units = 65535;
+    hipError_t e = hipSuccess;
+    if (most_rows > kSingleRows) {
+        // rows of long and short sequences: each kernel takes its own (they
+        // share the workspace, one after the other)
+        A.upto = kSingleRows;
+        AttArgs P = A;
+        P.above = kSingleRows;
+        P.upto = 0x7FFFFFFF;
+        e = launch_attend_prompt(P, s);
+        if (e != hipSuccess || b.n_tok == (long long)b.n_seq * b.max_q) return e;   // no short ones
+    }
     // heads side by side: the row tiles that read one head's pages run on one
     // XCD where the heads are a multiple of 8, and share its L2
-    const dim3 grid(c.n_kv, (unsigned)units);
+    const dim3 grid(c.n_kv, att_grid(A, kAttRows));
     const size_t joins = ((size_t)kAttWaves * (64 * kj + 4 + 2) + 2) * kAttRows * 4, looks = kSegGrans * sizeof(Gran);
     const size_t shm = joins > looks ? joins : looks;
     const bool full = c.d == 64 * kj;
-    hipError_t e = hipSuccess;
 #define PI_ATT(F, K, U)                                                                            \
     do {                                                                                           \
         if (shm > 65536)                                                                           \

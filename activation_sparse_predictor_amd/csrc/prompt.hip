@@ -1,0 +1,338 @@
+// Attention of many rows over the 8-bit paged cache (prompts).
+//
+// The mathematics, the references and the operands' order are those of
+// attend.hip.  Here the matrix cores are the bound: a workgroup of eight waves
+// carries 256 rows (128 for heads above 128 dimensions), 32 a wave, and the
+// waves share every tile of 64 keys through LDS, where it is kept as fp16 in
+// the order of the operands' fragments (1 KB each, a lane's 16 bytes in lane
+// order: no bank conflicts).  Each thread turns its 16-byte pieces of codes
+// into fp16 once for the workgroup.  Two tiles are held: while one is used the
+// next is written, and the one after is on its way in registers, so one
+// barrier a tile is all.  A fragment read from LDS serves the wave's two
+// 16-row operands.  The weights are rounded to fp16 once (2^-11 a weight, as
+// large as the rounding of the output itself): the second half that attend.hip
+// keeps would cost half as many products again.
+#include "attend.hpp"
+
+namespace pi {
+
+constexpr int kProWaves = 8;
+constexpr int kProThreads = kProWaves * kWave;
+constexpr int kProTarget = 256;     // one workgroup a CU
+constexpr int kProMinTiles = 8;     // fewest tiles worth a workgroup of their own
+constexpr int kProRing = 2 * kSegTiles;
+
+// The waves' LDS writes are done and all of them are here.  Unlike
+// __syncthreads this does not wait for the loads of the tile after next.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
+
+template <int FMT, int KJ, bool FULL>
+__device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) {
+    constexpr int NT = KJ == 4 ? 1 : 2, ROWS = kProWaves * 16 * NT, DP = 64 * KJ;
+    static_assert(ROWS == prompt_rows(KJ), "rows of a workgroup");
+    constexpr int kFrags = 16 * KJ;   // of a tile: 8 KJ of K, 8 KJ of V
+    extern __shared__ u32x4 frags[];  // [2][kFrags][64]
+    __shared__ Gran grans[kProRing * (kTile / kGran)];
+    __shared__ float done[2][ROWS];
+    __shared__ int s_last;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int lane = lane_id(), n16 = lane & 15, g = lane >> 4;
+    const int d = FULL ? DP : A.c.d, dc = d / 16, group = A.group;
+    const int first = w.q.ctx - w.q.n, rows_all = w.q.n * group;
+    const int n = w.t1 - w.t0;
+
+    auto fill = [&](int x, int count) {   // tiles [x, x + count) of this unit, into their places of the ring
+        att_lookup(A, w, d, (w.t0 + x) * (kTile / kGran), count * (kTile / kGran), threadIdx.x, kProThreads,
+                   &grans[(x & (kProRing - 1)) * (kTile / kGran)]);
+    };
+
+    // rows and positions: the workgroup's, this wave's, this lane's
+    auto last_tok = [&](int r) {
+        const int t = r / group;
+        return t < w.q.n ? t : w.q.n - 1;
+    };
+    const int row_w = w.row_tile * ROWS, row_v = row_w + wave * 16 * NT;
+    const int any_to = first + last_tok(row_w + ROWS - 1);
+    const int any_from = A.window > 0 ? first + row_w / group - A.window + 1 : 0;
+    const bool idle = row_v >= rows_all;
+    const int v_to = idle ? -1 : first + last_tok(row_v + 16 * NT - 1), v_free_to = first + row_v / group;
+    const int v_from = A.window > 0 ? first + row_v / group - A.window + 1 : 0;
+    const int v_free_from = A.window > 0 ? v_to - A.window + 1 : 0;
+    int pos[NT], lo[NT];
+    f16x8 qf[NT][2 * KJ];
+    const uint32_t sign = A.scale2 < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = row_v + nt * 16 + n16;
+        const bool live = r < rows_all;
+        const int tok = live ? r / group : 0, head = w.h * group + (live ? r - tok * group : 0);
+        pos[nt] = live ? first + tok : -1;
+        lo[nt] = A.window > 0 && pos[nt] - A.window + 1 > 0 ? pos[nt] - A.window + 1 : 0;
+        const h16* qr = A.q + (size_t)(w.q.row0 + tok) * A.q_stride + (size_t)head * d;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+            const int ch = j * 4 + g;
+            u32x4 a = {0u, 0u, 0u, 0u}, e = a;
+            if (live && ch < dc) {
+                a = ld16(qr + ch * 16);
+                e = ld16(qr + ch * 16 + 8);
+            }
+            qf[nt][2 * j] = __builtin_bit_cast(f16x8, a ^ sign);
+            qf[nt][2 * j + 1] = __builtin_bit_cast(f16x8, e ^ sign);
+        }
+    }
+
+    // This thread's KJ pieces of a tile's codes: of the 4 KJ groups of 64
+    // pieces of K, then the 4 KJ of V, wave v takes groups v, v + 8, ...
+    u32x4 st[KJ];
+    auto is_k = [&](int i) { return wave + 8 * i < 4 * KJ; };
+    auto load = [&](int x) {
+        const Gran* gr = &grans[(x & (kProRing - 1)) * (kTile / kGran)];
+#pragma unroll
+        for (int i = 0; i < KJ; ++i) {
+            const int un = wave + 8 * i;
+            u32x4 v = {Codes<FMT>::kZero4, Codes<FMT>::kZero4, Codes<FMT>::kZero4, Codes<FMT>::kZero4};
+            if (is_k(i)) {
+                const int t = un / KJ, ch = un % KJ * 4 + g;
+                if (FULL || ch < dc) v = ld16(gran_at(A.c.k, gr[n16 >> 2]) + t * 4 * d + ch * 64 + (n16 & 3) * 16);
+            } else {
+                const int dt = un - 4 * KJ;
+                if (FULL || dt < dc) v = ld16(gran_at(A.c.v, gr[g]) + (dt * 16 + n16) * 16);
+            }
+            st[i] = v;
+        }
+    };
+    auto store = [&](int x) {
+        const int tile0 = (w.t0 + x) * kTile, key0 = tile0 + g * kGran;
+        const bool edge = FMT == 1 && (tile0 < any_from || tile0 + kTile - 1 > any_to);
+        u32x4* to = frags + (x & 1) * kFrags * 64 + lane;
+#pragma unroll
+        for (int i = 0; i < KJ; ++i) {
+            const int un = wave + 8 * i;
+            u32x4 v = st[i];
+            if (edge && !is_k(i)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = keep_tokens(v[j], key0 + 4 * j, any_from, any_to);
+            }
+            const int f = is_k(i) ? (un / KJ) * 2 * KJ + un % KJ * 2 : 8 * KJ + (un - 4 * KJ) * 2;
+            to[f * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(v.x, v.y));
+            to[(f + 1) * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(v.z, v.w));
+        }
+    };
+
+    float M[NT], l[NT];
+    f32x4 O[NT][4 * KJ];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        M[nt] = kNone;
+        l[nt] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4 * KJ; ++k) O[nt][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    if (n > 0) {
+        fill(0, n < kSegTiles ? n : kSegTiles);
+        __syncthreads();
+        load(0);
+        store(0);
+        if (n > 1) load(1);
+        lds_barrier();
+    }
+    for (int x = 0; x < n; ++x) {
+        if (x % kSegTiles == 0 && x + kSegTiles < n) {   // the next segment, in the half of the ring that is done with
+            const int left = n - x - kSegTiles;
+            fill(x + kSegTiles, left < kSegTiles ? left : kSegTiles);
+        }
+        if (x + 1 < n) store(x + 1);
+        if (x + 2 < n) load(x + 2);
+        const int tile0 = (w.t0 + x) * kTile;
+        if (tile0 <= v_to && tile0 + kTile - 1 >= v_from) {
+            const Gran* gr = &grans[(x & (kProRing - 1)) * (kTile / kGran)];
+            const float kx = gr[g].kx, lv = gr[g].lv;
+            const u32x4* kf = frags + (x & 1) * kFrags * 64 + lane;
+            f32x4 S[NT][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) S[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 2 * KJ; ++k) {
+                    const f16x8 a = __builtin_bit_cast(f16x8, kf[(t * 2 * KJ + k) * 64]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) S[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[nt][k], S[nt][t], 0, 0, 0);
+                }
+            }
+            const int key0 = tile0 + g * kGran;
+            const bool edge = tile0 < v_free_from || tile0 + kTile - 1 > v_free_to;
+            f16x8 ph[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if (edge) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float v = S[nt][k / 4][k % 4] * kx;
+                        S[nt][k / 4][k % 4] = key0 + k >= lo[nt] && key0 + k <= pos[nt] ? v : -__builtin_inff();
+                    }
+                }
+                float mx = S[nt][0][0];
+#pragma unroll
+                for (int k = 1; k < 16; ++k) mx = fmaxf(mx, S[nt][k / 4][k % 4]);
+                const float by = edge ? 1.f : kx;
+                mx = max_groups(fmaf(mx, by, lv));
+                if (__ballot(mx > M[nt])) {
+                    const float m = fmaxf(M[nt], mx), f = exp2_fast(M[nt] - m);
+                    l[nt] *= f;
+#pragma unroll
+                    for (int k = 0; k < 4 * KJ; ++k) O[nt][k] *= f;
+                    M[nt] = m;
+                }
+                const float c = lv - M[nt] + kLift;
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float wt = exp2_fast(fmaf(S[nt][k / 4][k % 4], by, c));
+                    if (edge) wt = key0 + k >= lo[nt] && key0 + k <= pos[nt] ? wt : 0.f;
+                    sum += wt;
+                    ph[nt][k / 8][k % 8] = (f16)wt;
+                }
+                // a lane that attends to none of its keys adds none, whatever their page's scale is
+                l[nt] += edge && sum == 0.f ? 0.f : sum * exp2_fast(-lv);
+            }
+            const u32x4* vf = kf + 8 * KJ * 64;
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k) {
+                const f16x8 a = __builtin_bit_cast(f16x8, vf[2 * k * 64]), b = __builtin_bit_cast(f16x8, vf[(2 * k + 1) * 64]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[nt][0], O[nt][k], 0, 0, 0);
+                    O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, ph[nt][1], O[nt][k], 0, 0, 0);
+                }
+            }
+        }
+        lds_barrier();
+    }
+
+    // a row's outputs are spread over the four lanes of one n16
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    auto emit = [&](int r, int i, f32x4 o, float m, float sum) {
+        const int gr = row_w + r, tok = gr / group, head = w.h * group + gr - tok * group;
+        const size_t to = (size_t)(w.q.row0 + tok) * A.n_head + head;
+        const bool empty = first + tok < 0;
+        // no weight at all although there are keys: every score was -infinity
+        const float f = sum == 0.f ? __builtin_nanf("") : 1.f / sum;
+        f16x4 v;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = empty ? (f16)0.f : (f16)(o[k] * f);
+        *reinterpret_cast<f16x4*>(A.y + to * d + i) = v;
+        if (A.lse && i == 0) A.lse[to] = empty ? -__builtin_inff() : (m - kLift + log2_fast(sum)) * kLn2;
+    };
+    constexpr int kSlotBytes = ROWS * (DP + 2) * 4;   // outputs [ROWS][DP], then M and l [2][ROWS]
+    const uint32_t step = (uint32_t)A.c.n_kv * kSlotBytes, item = ((uint32_t)w.slot * A.c.n_kv + w.h) * kSlotBytes;
+    const uint32_t mine = item + w.split * step;
+    const __amdgpu_buffer_rsrc_t part = buf_rsrc(A.part, 2u * kProTarget * kSlotBytes);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = wave * 16 * NT + nt * 16 + n16;
+        const float sum = sum_groups(l[nt]);
+        const bool live = row_w + r < rows_all;
+#pragma unroll
+        for (int k = 0; k < 4 * KJ; ++k) {
+            const int i = k * 16 + g * 4;
+            if (!live || i >= d) continue;
+            if (w.splits == 1) emit(r, i, O[nt][k], M[nt], sum);
+            else st16_coherent(part, mine + (uint32_t)(r * DP + i) * 4, O[nt][k]);
+        }
+        if (w.splits > 1 && live && g == 0) {
+            float* st2 = reinterpret_cast<float*>(reinterpret_cast<char*>(A.part) + mine) + ROWS * DP + r;
+            st_coherent(st2, M[nt]);
+            st_coherent(st2 + ROWS, sum);
+        }
+    }
+    if (w.splits == 1) return;
+
+    // the last of the item's pieces to arrive joins them, in their order
+    uint32_t* ctr = A.ctr + ((size_t)w.slot * A.c.n_kv + w.h) * kAttCtrStride;
+    wait_own_memory();
+    __syncthreads();
+    if (threadIdx.x == 0) s_last = fetch_add_acq_rel(ctr, 1u) == (uint32_t)(w.splits - 1);
+    __syncthreads();
+    if (!s_last) return;
+    const int rows = rows_all - row_w < ROWS ? rows_all - row_w : ROWS;
+    for (int r = threadIdx.x; r < rows; r += kProThreads) {
+        float m = kNone, sum = 0.f;
+        for (int p = 0; p < w.splits; ++p) {
+            const uint32_t at = item + p * step + (ROWS * DP + r) * 4;
+            const float pm = ld4_coherent(part, at), ps = ld4_coherent(part, at + ROWS * 4), nm = fmaxf(m, pm);
+            sum = sum * exp2_fast(m - nm) + ps * exp2_fast(pm - nm);
+            m = nm;
+        }
+        done[0][r] = m;
+        done[1][r] = sum;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < rows * (DP / 4); e += kProThreads) {
+        const int r = e / (DP / 4), i = e % (DP / 4) * 4;
+        if (i >= d) continue;
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        constexpr int kBatch = 8;
+        for (int p0 = 0; p0 < w.splits; p0 += kBatch) {
+            f32x4 v[kBatch];
+            float m[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const uint32_t from = item + (p0 + k < w.splits ? p0 + k : w.splits - 1) * step;
+                v[k] = ld16_coherent(part, (uint32_t)(r * DP + i) * 4, from);
+                m[k] = ld4_coherent(part, from + (ROWS * DP + r) * 4);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (p0 + k < w.splits) o += v[k] * exp2_fast(m[k] - done[0][r]);
+        }
+        emit(r, i, o, done[0][r], done[1][r]);
+    }
+    if (threadIdx.x == 0) st_flag(ctr, 0u);
+}
+
+template <int FMT, int KJ, bool FULL>
+__global__ __launch_bounds__(kProThreads, 2) void k_attend_prompt(AttArgs A) {
+    constexpr int ROWS = prompt_rows(KJ);
+    AttUnit w;
+    w.h = blockIdx.x;
+    const int units = att_plan<ROWS>(A, blockIdx.y, w);
+    for (int u = blockIdx.y; u < units;) {
+        prompt_unit<FMT, KJ, FULL>(A, w);
+        u += gridDim.y;
+        if (u < units) {
+            __syncthreads();   // the next unit uses the same shared memory
+            att_plan<ROWS>(A, u, w);
+        }
+    }
+}
+
+hipError_t launch_attend_prompt(AttArgs A, hipStream_t s) {
+    const int kj = att_kj(A.c.d);
+    A.target = kProTarget;
+    A.min_tiles = kProMinTiles;
+    const dim3 grid(A.c.n_kv, att_grid(A, prompt_rows(kj)));
+    const size_t shm = (size_t)2 * 16 * kj * 1024;
+    const bool full = A.c.d == 64 * kj;
+    hipError_t e = hipSuccess;
+#define PI_PRO(F, K, U)                                                                                   \
+    do {                                                                                                  \
+        if (shm + 24576 > 65536)                                                                          \
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_prompt<F, K, U>),             \
+                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);                \
+        if (e == hipSuccess) hipLaunchKernelGGL((k_attend_prompt<F, K, U>), grid, dim3(kProThreads), shm, s, A); \
+    } while (0)
+#define PI_PRO_D(F)                                                          \
+    if (kj == 1) { if (full) PI_PRO(F, 1, true); else PI_PRO(F, 1, false); }  \
+    else if (kj == 2) { if (full) PI_PRO(F, 2, true); else PI_PRO(F, 2, false); } \
+    else { if (full) PI_PRO(F, 4, true); else PI_PRO(F, 4, false); }
+    if (A.c.fmt == 0) { PI_PRO_D(0); } else { PI_PRO_D(1); }
+#undef PI_PRO_D
+#undef PI_PRO
+    if (e != hipSuccess) return e;
+    return hipGetLastError();
+}
+
+}  // namespace pi
