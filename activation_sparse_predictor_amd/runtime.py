@@ -303,36 +303,49 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _kv_args(cache: dict, batch: dict, device):
-    """The C descriptors of a cache and a batch on `device`."""
+_U8, _F16, _F32, _I32 = torch.uint8, torch.float16, torch.float32, torch.int32
+
+
+def _kv_args(cache: dict, batch: dict, device: int):
+    """The C descriptors of a cache and a batch on the GPU `device` (-1: the host)."""
     k, v, ks, vs = cache["k"], cache["v"], cache["k_scale"], cache["v_scale"]
     start, ctx, table = batch["q_start"], batch["ctx"], batch["table"]
-    _need(cache["fmt"] in B.KV_FMTS, "cache fmt must be 'int8' or 'fp8'")
-    _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype == torch.uint8,
-          "cache k and v must be n_pages x n_kv x page x d bytes")
-    _need(ks.shape == vs.shape == k.shape[:2] and ks.dtype == vs.dtype == torch.float32,
-          "cache scales must be n_pages x n_kv floats")
-    n_seq = ctx.shape[0]
-    _need(ctx.dim() == 1 and start.shape == (n_seq + 1,) and table.dim() == 2 and table.shape[0] == n_seq,
-          "batch arrays must be q_start (n_seq + 1), ctx (n_seq) and table (n_seq x pages)")
-    _need(start.dtype == ctx.dtype == table.dtype == torch.int32, "batch arrays must be int32")
-    for t in (k, v, ks, vs, start, ctx, table):
-        _need(t.is_contiguous() and t.device == device, "cache and batch tensors must be contiguous and on one device")
-    n_pages, n_kv, page, d = k.shape
-    return (B.KvCache(B.KV_FMTS[cache["fmt"]], n_pages, n_kv, page, d, k.data_ptr(), v.data_ptr(), ks.data_ptr(),
+    fmt = B.KV_FMTS.get(cache["fmt"])
+    shape, n_seq, rows = k.shape, ctx.shape, table.shape
+    # one expression: this runs before every launch of a decode step
+    if not (fmt is not None and len(shape) == 4 and v.shape == shape and k.dtype is _U8 and v.dtype is _U8
+            and ks.shape == vs.shape == shape[:2] and ks.dtype is _F32 and vs.dtype is _F32
+            and len(n_seq) == 1 and len(rows) == 2 and rows[0] == n_seq[0] and start.shape == (n_seq[0] + 1,)
+            and start.dtype is _I32 and ctx.dtype is _I32 and table.dtype is _I32
+            and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
+            and start.is_contiguous() and ctx.is_contiguous() and table.is_contiguous()
+            and k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == start.get_device()
+            == ctx.get_device() == table.get_device() == device):
+        raise ValueError("a cache is fmt ('int8' or 'fp8'), k and v (n_pages x n_kv x page x d uint8), k_scale and v_scale "
+                         "(n_pages x n_kv float32); a batch is q_start (n_seq + 1), ctx (n_seq) and table (n_seq x pages), "
+                         "int32, with n_tok and max_q; all contiguous and on one device")
+    return (B.KvCache(fmt, shape[0], shape[1], shape[2], shape[3], k.data_ptr(), v.data_ptr(), ks.data_ptr(),
                       vs.data_ptr()),
-            B.KvBatch(n_seq, batch["n_tok"], batch["max_q"], table.shape[1], start.data_ptr(), ctx.data_ptr(),
+            B.KvBatch(n_seq[0], batch["n_tok"], batch["max_q"], rows[1], start.data_ptr(), ctx.data_ptr(),
                       table.data_ptr()))
 
 
 def _kv_rows(t: torch.Tensor, n_tok: int, heads: Optional[int], d: int, name: str, stride: bool = True) -> int:
     """Checks n_tok x heads x d fp16 rows; returns the elements between tokens."""
-    _need(t.dtype == torch.float16 and t.dim() == 3 and t.shape[0] == n_tok and t.shape[2] == d
-          and (heads is None or t.shape[1] == heads), f"{name} must be fp16, n_tok x heads x d")
-    heads = t.shape[1]
-    _need((t.stride(2) == 1 or d == 1) and (t.stride(1) == d or heads == 1) and (stride or t.is_contiguous()),
-          f"{name}: the heads of a token must be contiguous" if stride else f"{name} must be contiguous")
-    return t.stride(0) if n_tok > 1 else heads * d
+    shape = t.shape
+    if not (t.dtype is _F16 and len(shape) == 3 and shape[0] == n_tok and shape[2] == d
+            and (heads is None or shape[1] == heads)):
+        raise ValueError(f"{name} must be fp16, n_tok x heads x d")
+    if t.is_contiguous():
+        return shape[1] * d
+    if not (stride and (t.stride(2) == 1 or d == 1) and (t.stride(1) == d or shape[1] == 1)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous" if stride else f"{name} must be contiguous")
+    return t.stride(0) if n_tok > 1 else shape[1] * d
+
+
+# the current stream's handle, without making a torch.cuda.Stream of it
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _elsewhere(stream, device, tensors, call):
@@ -354,39 +367,47 @@ def _elsewhere(stream, device, tensors, call):
         return out
 
 
-def _is_elsewhere(stream, device) -> bool:
-    _need(device.type == "cuda", "tensors must be on the GPU")
-    return stream is not None or device.index != torch.cuda.current_device()
+def _is_elsewhere(stream, device: int) -> bool:
+    if device < 0:
+        raise ValueError("tensors must be on the GPU")
+    return stream is not None or device != torch.cuda.current_device()
 
 
 def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, batch: dict, stream=None) -> None:
     """pi_kv_append: quantises k and v (n_tok x n_kv x d fp16, tokens any
     multiple of 8 elements apart) into the batch's places of the cache."""
-    if _is_elsewhere(stream, k.device):
+    dev = k.get_device()
+    if _is_elsewhere(stream, dev):
         return _elsewhere(stream, k.device, (k, v, *cache.values(), *batch.values()),
                           lambda: kv_append(cache, k, v, batch))
-    c, b = _kv_args(cache, batch, k.device)
+    c, b = _kv_args(cache, batch, dev)
     ks = _kv_rows(k, b.n_tok, c.n_kv, c.d, "k")
     vs = _kv_rows(v, b.n_tok, c.n_kv, c.d, "v")
-    _need(v.device == k.device, "k and v must be on one device")
-    B.check(B.pi_kv_append(c, b, k, ks, v, vs), "pi_kv_append")
+    _need(v.get_device() == dev, "k and v must be on one device")
+    B.check(B.pi_kv_append(c, b, k, ks, v, vs, _raw_stream(dev)), "pi_kv_append")
 
 
 def kv_read(cache: dict, batch: dict, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """pi_kv_read: the stored keys and values of the batch's tokens (n_tok x n_kv x d fp16)."""
-    dev = cache["k"].device
+    codes = cache["k"]
+    dev = codes.get_device()
     if _is_elsewhere(stream, dev):
-        return _elsewhere(stream, dev, (k, v, *cache.values(), *batch.values()), lambda: kv_read(cache, batch, k, v))
+        return _elsewhere(stream, codes.device, (k, v, *cache.values(), *batch.values()),
+                          lambda: kv_read(cache, batch, k, v))
     c, b = _kv_args(cache, batch, dev)
+    shape = (b.n_tok, c.n_kv, c.d)
     if k is None:
-        k = torch.empty(b.n_tok, c.n_kv, c.d, dtype=torch.float16, device=dev)
+        k = torch.empty(shape, dtype=_F16, device=codes.device)
+    else:
+        _kv_rows(k, *shape, "k", stride=False)
+        _need(k.get_device() == dev, "k must be on the cache's device")
     if v is None:
-        v = torch.empty(b.n_tok, c.n_kv, c.d, dtype=torch.float16, device=dev)
-    for t, name in ((k, "k"), (v, "v")):
-        _kv_rows(t, b.n_tok, c.n_kv, c.d, name, stride=False)
-        _need(t.device == dev, "k and v must be on the cache's device")
-    B.check(B.pi_kv_read(c, b, k, v), "pi_kv_read")
+        v = torch.empty(shape, dtype=_F16, device=codes.device)
+    else:
+        _kv_rows(v, *shape, "v", stride=False)
+        _need(v.get_device() == dev, "v must be on the cache's device")
+    B.check(B.pi_kv_read(c, b, k, v, _raw_stream(dev)), "pi_kv_read")
     return k, v
 
 
@@ -406,32 +427,38 @@ def kv_attend(cache: dict, q: torch.Tensor, batch: dict, y: Optional[torch.Tenso
     of 8 elements apart) over the cache; scale defaults to 1 / sqrt(d), window 0
     is none, lse (n_tok x n_head floats) is filled if given.  Without ws, each
     stream has a workspace of its own."""
-    if _is_elsewhere(stream, q.device):
+    dev = q.get_device()
+    if _is_elsewhere(stream, dev):
         return _elsewhere(stream, q.device, (q, y, lse, ws, *cache.values(), *batch.values()),
                           lambda: kv_attend(cache, q, batch, y, scale, window, lse, ws))
-    dev = q.device
     c, b = _kv_args(cache, batch, dev)
-    qs = _kv_rows(q, b.n_tok, None, c.d, "q")
+    d = c.d
+    qs = _kv_rows(q, b.n_tok, None, d, "q")
     heads = q.shape[1]
     if y is None:
-        y = torch.empty(b.n_tok, heads, c.d, dtype=torch.float16, device=dev)
+        y = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
-        _kv_rows(y, b.n_tok, heads, c.d, "y", stride=False)
-        _need(y.device == dev, "y must be on q's device")
+        _kv_rows(y, b.n_tok, heads, d, "y", stride=False)
+        _need(y.get_device() == dev, "y must be on q's device")
     if lse is not None:
-        _need(lse.shape == (b.n_tok, heads) and lse.dtype == torch.float32 and lse.is_contiguous()
-              and lse.device == dev, "lse must be n_tok x n_head floats")
-    st = torch.cuda.current_stream().cuda_stream
-    if ws is None:
-        key = (dev.index, st)
-        if key not in _KV_WS:
-            _KV_WS[key] = Workspace(dev)
-        ws, wsb = _KV_WS[key].get(B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, c.d))
-    else:
-        _need(ws.device == dev and ws.is_contiguous(), "ws must be contiguous and on q's device")
-        wsb = ws.numel() * ws.element_size()
-    B.check(B.pi_kv_attend(c, b, q, qs, heads, c.d ** -0.5 if scale is None else float(scale), int(window), y, lse, ws,
-                           wsb, st), "pi_kv_attend")
+        _need(lse.shape == (b.n_tok, heads) and lse.dtype is _F32 and lse.is_contiguous()
+              and lse.get_device() == dev, "lse must be n_tok x n_head floats")
+    st = _raw_stream(dev)
+    scale = d ** -0.5 if scale is None else float(scale)
+    if ws is not None:
+        _need(ws.get_device() == dev and ws.is_contiguous(), "ws must be contiguous and on q's device")
+        size = ws.numel() * ws.element_size()
+        B.check(B.pi_kv_attend(c, b, q, qs, heads, scale, int(window), y, lse, ws, size, st), "pi_kv_attend")
+        return y
+    own = _KV_WS.get((dev, st))
+    if own is None:
+        own = _KV_WS[(dev, st)] = Workspace(q.device)
+    size = 0 if own.buf is None else own.buf.numel()
+    status = B.pi_kv_attend(c, b, q, qs, heads, scale, int(window), y, lse, own.buf, size, st)
+    if status == B.PI_ERR_WORKSPACE:   # too small for these sizes: nothing was launched
+        buf, size = own.get(B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, d))
+        status = B.pi_kv_attend(c, b, q, qs, heads, scale, int(window), y, lse, buf, size, st)
+    B.check(status, "pi_kv_attend")
     return y
 
 

@@ -109,14 +109,14 @@ def test_runtime_refuses_what_it_cannot_pass_on():
     for f in (lambda: R.kv_append(c, x, x, b), lambda: R.kv_read(c, b), lambda: R.kv_attend(c, x, b)):
         with pytest.raises(ValueError):
             f()
-    assert R._kv_args(c, b, torch.device("cpu"))[1].n_seq == 2
+    assert R._kv_args(c, b, -1)[1].n_seq == 2
     for change in (dict(fmt="int4"), dict(k=c["k"].float()), dict(v=c["v"][:2]), dict(k_scale=c["k_scale"].double()),
                    dict(k=c["k"].transpose(0, 1).contiguous().transpose(0, 1))):
         with pytest.raises(ValueError):
-            R._kv_args({**c, **change}, b, torch.device("cpu"))
+            R._kv_args({**c, **change}, b, -1)
     for change in (dict(ctx=b["ctx"].long()), dict(table=b["table"][:1]), dict(q_start=b["q_start"][:2])):
         with pytest.raises(ValueError):
-            R._kv_args(c, {**b, **change}, torch.device("cpu"))
+            R._kv_args(c, {**b, **change}, -1)
     assert R._kv_rows(x, 3, 2, 64, "k") == 128
     assert R._kv_rows(torch.zeros(3, 5, 128, dtype=torch.float16)[:, 1].view(3, 2, 64), 3, 2, 64, "k") == 640
     for t in (x.float(), x[:2], x[:, :1], x.transpose(0, 1), torch.zeros(3, 64, 2, dtype=torch.float16).transpose(1, 2)):
