@@ -134,18 +134,20 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
 
             const int tile0 = (seg + i) * kTile, key0 = tile0 + g * kGran;   // the tile's first key, and this lane's
             const bool edge = tile0 < free_from || tile0 + kTile - 1 > free_to;
-            float mx;
             if (edge) {   // scores of keys that the row does not attend to become -infinity
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const float x = S[k / 4][k % 4] * kx;
-                    S[k / 4][k % 4] = key0 + k >= lo && key0 + k <= pos ? x : -__builtin_inff();
+                    S[k / 4][k % 4] = k >= lo - key0 && k <= pos - key0 ? x : -__builtin_inff();
                 }
             }
-            mx = S[0][0];
+            float mx = S[0][0];
 #pragma unroll
             for (int k = 1; k < 16; ++k) mx = fmaxf(mx, S[k / 4][k % 4]);
-            mx = max_groups(fmaf(mx, edge ? 1.f : kx, lv));
+            // a lane that attends to none of its keys adds nothing, whatever their page's scale is
+            const bool none = edge && mx == -__builtin_inff();
+            const float by = edge ? 1.f : kx;
+            mx = max_groups(fmaf(mx, by, lv));
             if (__ballot(mx > M)) {
                 const float m = fmaxf(M, mx), f = exp2_fast(M - m);
                 l *= f;
@@ -155,19 +157,17 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
             }
             // the weights' leading and following halves: to 22 bits, at twice the output's products
             f16x8 ph[2], pl[2];
-            const float c = lv - M + kLift, by = edge ? 1.f : kx;
+            const float c = none ? 0.f : lv - M + kLift, unscale = none ? 0.f : exp2_fast(-lv);
             float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-                float wt = exp2_fast(fmaf(S[k / 4][k % 4], by, c));
-                if (edge) wt = key0 + k >= lo && key0 + k <= pos ? wt : 0.f;
+                const float wt = exp2_fast(fmaf(S[k / 4][k % 4], by, c));
                 sum += wt;
                 const f16 hi = (f16)wt;
                 ph[k / 8][k % 8] = hi;
                 pl[k / 8][k % 8] = (f16)(wt - (float)hi);
             }
-            // a lane that attends to none of its keys adds none, whatever their page's scale is
-            l += edge && sum == 0.f ? 0.f : sum * exp2_fast(-lv);
+            l = fmaf(sum, unscale, l);
             if (FMT == 1 && (tile0 < any_from || tile0 + kTile - 1 > any_to)) {
 #pragma unroll
                 for (int k = 0; k < 4 * KJ; ++k)

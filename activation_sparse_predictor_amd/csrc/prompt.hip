@@ -85,7 +85,7 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     // This thread's KJ pieces of a tile's codes: of the 4 KJ groups of 64
     // pieces of K, then the 4 KJ of V, wave v takes groups v, v + 8, ...
     u32x4 st[KJ];
-    auto is_k = [&](int i) { return wave + 8 * i < 4 * KJ; };
+    auto is_k = [&](int i) { return KJ == 1 ? wave < 4 : i < KJ / 2; };
     auto load = [&](int x) {
         const Gran* gr = &grans[(x & (kProRing - 1)) * (kTile / kGran)];
 #pragma unroll
@@ -150,18 +150,32 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
             const Gran* gr = &grans[(x & (kProRing - 1)) * (kTile / kGran)];
             const float kx = gr[g].kx, lv = gr[g].lv;
             const u32x4* kf = frags + (x & 1) * kFrags * 64 + lane;
+            // Fragments are read a group of products ahead (the compiler alone reads one and waits for it).
             f32x4 S[NT][4];
+            f16x8 ka[2][2 * KJ];
+#pragma unroll
+            for (int k = 0; k < 2 * KJ; ++k) ka[0][k] = __builtin_bit_cast(f16x8, kf[k * 64]);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
+                if (t < 3) {
+#pragma unroll
+                    for (int k = 0; k < 2 * KJ; ++k) ka[(t + 1) % 2][k] = __builtin_bit_cast(f16x8, kf[((t + 1) * 2 * KJ + k) * 64]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) S[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < 2 * KJ; ++k) {
-                    const f16x8 a = __builtin_bit_cast(f16x8, kf[(t * 2 * KJ + k) * 64]);
+                for (int k = 0; k < 2 * KJ; ++k)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) S[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qf[nt][k], S[nt][t], 0, 0, 0);
-                }
+                    for (int nt = 0; nt < NT; ++nt)
+                        S[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ka[t % 2][k], qf[nt][k], S[nt][t], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            const u32x4* vf = kf + 8 * KJ * 64;
+            f16x8 va[2][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) va[0][k] = __builtin_bit_cast(f16x8, vf[k * 64]);
+            __builtin_amdgcn_sched_barrier(0);
             const int key0 = tile0 + g * kGran;
             const bool edge = tile0 < v_free_from || tile0 + kTile - 1 > v_free_to;
             f16x8 ph[NT][2];
@@ -171,12 +185,14 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const float v = S[nt][k / 4][k % 4] * kx;
-                        S[nt][k / 4][k % 4] = key0 + k >= lo[nt] && key0 + k <= pos[nt] ? v : -__builtin_inff();
+                        S[nt][k / 4][k % 4] = k >= lo[nt] - key0 && k <= pos[nt] - key0 ? v : -__builtin_inff();
                     }
                 }
                 float mx = S[nt][0][0];
 #pragma unroll
                 for (int k = 1; k < 16; ++k) mx = fmaxf(mx, S[nt][k / 4][k % 4]);
+                // a lane that attends to none of its keys adds nothing, whatever their page's scale is
+                const bool none = edge && mx == -__builtin_inff();
                 const float by = edge ? 1.f : kx;
                 mx = max_groups(fmaf(mx, by, lv));
                 if (__ballot(mx > M[nt])) {
@@ -186,27 +202,29 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
                     for (int k = 0; k < 4 * KJ; ++k) O[nt][k] *= f;
                     M[nt] = m;
                 }
-                const float c = lv - M[nt] + kLift;
+                const float c = none ? 0.f : lv - M[nt] + kLift, unscale = none ? 0.f : exp2_fast(-lv);
                 float sum = 0.f;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    float wt = exp2_fast(fmaf(S[nt][k / 4][k % 4], by, c));
-                    if (edge) wt = key0 + k >= lo[nt] && key0 + k <= pos[nt] ? wt : 0.f;
+                    const float wt = exp2_fast(fmaf(S[nt][k / 4][k % 4], by, c));
                     sum += wt;
                     ph[nt][k / 8][k % 8] = (f16)wt;
                 }
-                // a lane that attends to none of its keys adds none, whatever their page's scale is
-                l[nt] += edge && sum == 0.f ? 0.f : sum * exp2_fast(-lv);
+                l[nt] = fmaf(sum, unscale, l[nt]);
             }
-            const u32x4* vf = kf + 8 * KJ * 64;
 #pragma unroll
-            for (int k = 0; k < 4 * KJ; ++k) {
-                const f16x8 a = __builtin_bit_cast(f16x8, vf[2 * k * 64]), b = __builtin_bit_cast(f16x8, vf[(2 * k + 1) * 64]);
+            for (int k = 0; k < 2 * KJ; ++k) {   // two 16-dimension tiles at a time
+                if (k + 1 < 2 * KJ) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[nt][0], O[nt][k], 0, 0, 0);
-                    O[nt][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, ph[nt][1], O[nt][k], 0, 0, 0);
+                    for (int i = 0; i < 4; ++i) va[(k + 1) % 2][i] = __builtin_bit_cast(f16x8, vf[((k + 1) * 4 + i) * 64]);
                 }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        O[nt][2 * k + i / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va[k % 2][i], ph[nt][i % 2], O[nt][2 * k + i / 2], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         lds_barrier();
