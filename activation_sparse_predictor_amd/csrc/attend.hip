@@ -8,10 +8,10 @@
 // cache a second time; ks multiplies the fp32 score and vs the weight.  A vs
 // lies anywhere between 2^-31 and 2^9, so the running reference M follows the
 // largest weight with its scale, max (x + log2 vs):
-//   w_j = 2^(x_j + log2 vs_j - M + 15.9),  l = sum w_j / vs_j,  y = sum w_j code_j / l.
-// So w is at most 2^15.9, just inside fp16, which holds it down to 2^-40 of the
-// row's largest; l is summed in fp32, where its terms 2^(x - M + 15.9) always
-// fit.  A page of zeros (vs = 0) takes part
+//   w_j = 2^(x_j + log2 vs_j - M + 15.7),  l = sum w_j / vs_j,  y = sum w_j code_j / l.
+// M moves when a maximum is more than 0.25 above it, so w is at most 2^15.95,
+// just inside fp16, which holds it down to 2^-40 of the row's largest; l is
+// summed in fp32, where its terms 2^(x - M + 15.7) always fit.  A page of zeros (vs = 0) takes part
 // as vs = 2^-64: its weights count, and its values stay far below fp16's range.
 //
 // Operands.  A wave takes 64 keys (four granules of 16) a step, as the rows of
@@ -147,9 +147,9 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
             // a lane that attends to none of its keys adds nothing, whatever their page's scale is
             const bool none = edge && mx == -__builtin_inff();
             const float by = edge ? 1.f : kx;
-            mx = max_groups(fmaf(mx, by, lv));
-            if (__ballot(mx > M)) {
-                const float m = fmaxf(M, mx), f = exp2_fast(M - m);
+            mx = fmaf(mx, by, lv);
+            if (__ballot(mx > M + kSlack)) {
+                const float m = fmaxf(M, max_groups(mx)), f = exp2_fast(M - m);
                 l *= f;
 #pragma unroll
                 for (int k = 0; k < 4 * KJ; ++k) O[k] *= f;
@@ -342,7 +342,7 @@ size_t kv_attend_bytes(int, int, int max_q, int n_head, int n_kv, int d) {
     const int kj = att_kj(d);
     size_t rows = (size_t)2 * single_target(kj) * kAttRows;
     if ((long long)max_q * (n_head / n_kv) > kSingleRows) {
-        const size_t more = (size_t)2 * 256 * prompt_rows(kj);
+        const size_t more = (size_t)kAttSlots * prompt_rows(kj);
         rows = more > rows ? more : rows;
     }
     return kv_attend_zero_bytes() + rows * (64 * kj + 2) * 4;

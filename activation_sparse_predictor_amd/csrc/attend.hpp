@@ -13,7 +13,7 @@ constexpr int kAttMaxTarget = 512;   // most workgroups that the work is split i
 constexpr int kAttSlots = 2 * kAttMaxTarget;
 constexpr int kAttCtrStride = 16;    // words between arrival counters
 
-constexpr float kLift = 15.9f, kZeroLog = -64.f, kNone = -1e30f, kLn2 = 0.69314718055994531f;
+constexpr float kLift = 15.7f, kSlack = 0.25f, kZeroLog = -64.f, kNone = -1e30f, kLn2 = 0.69314718055994531f;
 
 // max over the lanes that hold the same query (lane ^ 16, lane ^ 32)
 __device__ __forceinline__ float max_groups(float v) {
@@ -236,7 +236,7 @@ inline unsigned att_grid(const AttArgs& A, int rows) {
 __host__ __device__ constexpr int att_kj(int d) { return d <= 64 ? 1 : d <= 128 ? 2 : 4; }
 
 // prompt.hip
-constexpr int prompt_rows(int kj) { return kj == 4 ? 128 : 256; }
+constexpr int prompt_rows(int kj) { return kj == 4 ? 64 : 128; }
 hipError_t launch_attend_prompt(AttArgs A, hipStream_t s);
 
 }  // namespace pi

@@ -1,26 +1,28 @@
 // Attention of many rows over the 8-bit paged cache (prompts).
 //
 // The mathematics, the references and the operands' order are those of
-// attend.hip.  Here the matrix cores are the bound: a workgroup of eight waves
-// carries 256 rows (128 for heads above 128 dimensions), 32 a wave, and the
-// waves share every tile of 64 keys through LDS, where it is kept as fp16 in
-// the order of the operands' fragments (1 KB each, a lane's 16 bytes in lane
-// order: no bank conflicts).  Each thread turns its 16-byte pieces of codes
-// into fp16 once for the workgroup.  Two tiles are held: while one is used the
-// next is written, and the one after is on its way in registers, so one
-// barrier a tile is all.  A fragment read from LDS serves the wave's two
-// 16-row operands.  The weights are rounded to fp16 once (2^-11 a weight, as
-// large as the rounding of the output itself): the second half that attend.hip
-// keeps would cost half as many products again.
+// attend.hip.  Here the matrix cores are the bound, and next to them LDS: a
+// workgroup of four waves carries 128 rows (64 for heads above 128 dimensions),
+// 32 a wave, and the waves share every tile of 64 keys through LDS, where it is
+// kept as fp16 in the order of the operands' fragments (1 KB each, a lane's 16
+// bytes in lane order: no bank conflicts).  Each thread turns its 16-byte
+// pieces of codes into fp16 once for the workgroup.  Two tiles are held: while
+// one is used the next is written, and the one after is on its way in
+// registers, so one barrier a tile is all.  A fragment read from LDS serves the
+// wave's two 16-row operands.  Two workgroups share a CU, so that one's weights
+// (vector work) run beside the other's products.  The weights are rounded to
+// fp16 once (2^-11 a weight, as large as the rounding of the output itself):
+// the second half that attend.hip keeps would cost half as many products again.
 #include "attend.hpp"
 
 namespace pi {
 
-constexpr int kProWaves = 8;
+constexpr int kProWaves = 4;
 constexpr int kProThreads = kProWaves * kWave;
-constexpr int kProTarget = 256;     // one workgroup a CU
+constexpr int pro_target(int kj) { return kj == 4 ? 256 : 512; }   // workgroups that run at once, by LDS
 constexpr int kProMinTiles = 8;     // fewest tiles worth a workgroup of their own
-constexpr int kProRing = 2 * kSegTiles;
+constexpr int kProSeg = 64;         // tiles whose granules are looked up at a time
+constexpr int kProRing = 2 * kProSeg;
 
 // The waves' LDS writes are done and all of them are here.  Unlike
 // __syncthreads this does not wait for the loads of the tile after next.
@@ -35,8 +37,10 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     __shared__ Gran grans[kProRing * (kTile / kGran)];
     __shared__ float done[2][ROWS];
     __shared__ int s_last;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int lane = lane_id(), n16 = lane & 15, g = lane >> 4;
+    // (settled, so that what follows from them is not kept in registers from
+    // unit to unit)
+    const int lane = settle(lane_id()), wave = __builtin_amdgcn_readfirstlane(settle((int)threadIdx.x) / kWave);
+    const int n16 = lane & 15, g = lane >> 4;
     const int d = FULL ? DP : A.c.d, dc = d / 16, group = A.group;
     const int first = w.q.ctx - w.q.n, rows_all = w.q.n * group;
     const int n = w.t1 - w.t0;
@@ -82,41 +86,37 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         }
     }
 
-    // This thread's KJ pieces of a tile's codes: of the 4 KJ groups of 64
-    // pieces of K, then the 4 KJ of V, wave v takes groups v, v + 8, ...
-    u32x4 st[KJ];
-    auto is_k = [&](int i) { return KJ == 1 ? wave < 4 : i < KJ / 2; };
-    auto load = [&](int x) {
+    // This thread's 2 KJ pieces of a tile's codes: of the 4 KJ groups of 64
+    // pieces of K, then the 4 KJ of V, wave v takes groups v, v + 4, ...
+    u32x4 st[2 * KJ];
+    auto load = [&](int x) __attribute__((always_inline)) {
         const Gran* gr = &grans[(x & (kProRing - 1)) * (kTile / kGran)];
+        const uint8_t* kp = gran_at(A.c.k, gr[n16 >> 2]) + (n16 & 3) * 16;
+        const uint8_t* vp = gran_at(A.c.v, gr[g]) + n16 * 16;
 #pragma unroll
         for (int i = 0; i < KJ; ++i) {
-            const int un = wave + 8 * i;
-            u32x4 v = {Codes<FMT>::kZero4, Codes<FMT>::kZero4, Codes<FMT>::kZero4, Codes<FMT>::kZero4};
-            if (is_k(i)) {
-                const int t = un / KJ, ch = un % KJ * 4 + g;
-                if (FULL || ch < dc) v = ld16(gran_at(A.c.k, gr[n16 >> 2]) + t * 4 * d + ch * 64 + (n16 & 3) * 16);
-            } else {
-                const int dt = un - 4 * KJ;
-                if (FULL || dt < dc) v = ld16(gran_at(A.c.v, gr[g]) + (dt * 16 + n16) * 16);
-            }
-            st[i] = v;
+            const int un = wave + 4 * i, t = un / KJ, ch = un % KJ * 4 + g;
+            const u32x4 zero = {Codes<FMT>::kZero4, Codes<FMT>::kZero4, Codes<FMT>::kZero4, Codes<FMT>::kZero4};
+            st[i] = st[KJ + i] = zero;
+            if (FULL || ch < dc) st[i] = ld16(kp + t * 4 * d + ch * 64);
+            if (FULL || un < dc) st[KJ + i] = ld16(vp + un * 256);
         }
     };
-    auto store = [&](int x) {
+    auto store = [&](int x) __attribute__((always_inline)) {
         const int tile0 = (w.t0 + x) * kTile, key0 = tile0 + g * kGran;
-        const bool edge = FMT == 1 && (tile0 < any_from || tile0 + kTile - 1 > any_to);
         u32x4* to = frags + (x & 1) * kFrags * 64 + lane;
+        if (FMT == 1 && (tile0 < any_from || tile0 + kTile - 1 > any_to)) {   // slots that no row here attends to may hold NaN
 #pragma unroll
-        for (int i = 0; i < KJ; ++i) {
-            const int un = wave + 8 * i;
-            u32x4 v = st[i];
-            if (edge && !is_k(i)) {
+            for (int i = KJ; i < 2 * KJ; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = keep_tokens(v[j], key0 + 4 * j, any_from, any_to);
-            }
-            const int f = is_k(i) ? (un / KJ) * 2 * KJ + un % KJ * 2 : 8 * KJ + (un - 4 * KJ) * 2;
-            to[f * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(v.x, v.y));
-            to[(f + 1) * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(v.z, v.w));
+                for (int j = 0; j < 4; ++j) st[i][j] = keep_tokens(st[i][j], key0 + 4 * j, any_from, any_to);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * KJ; ++i) {
+            const int un = wave + 4 * (i % KJ);
+            const int f = i < KJ ? (un / KJ) * 2 * KJ + un % KJ * 2 : 8 * KJ + un * 2;
+            to[f * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(st[i].x, st[i].y));
+            to[(f + 1) * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(st[i].z, st[i].w));
         }
     };
 
@@ -131,7 +131,7 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     }
 
     if (n > 0) {
-        fill(0, n < kSegTiles ? n : kSegTiles);
+        fill(0, n < kProSeg ? n : kProSeg);
         __syncthreads();
         load(0);
         store(0);
@@ -139,9 +139,9 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         lds_barrier();
     }
     for (int x = 0; x < n; ++x) {
-        if (x % kSegTiles == 0 && x + kSegTiles < n) {   // the next segment, in the half of the ring that is done with
-            const int left = n - x - kSegTiles;
-            fill(x + kSegTiles, left < kSegTiles ? left : kSegTiles);
+        if (x % kProSeg == 0 && x + kProSeg < n) {   // the next segment, in the half of the ring that is done with
+            const int left = n - x - kProSeg;
+            fill(x + kProSeg, left < kProSeg ? left : kProSeg);
         }
         if (x + 1 < n) store(x + 1);
         if (x + 2 < n) load(x + 2);
@@ -194,9 +194,9 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
                 // a lane that attends to none of its keys adds nothing, whatever their page's scale is
                 const bool none = edge && mx == -__builtin_inff();
                 const float by = edge ? 1.f : kx;
-                mx = max_groups(fmaf(mx, by, lv));
-                if (__ballot(mx > M[nt])) {
-                    const float m = fmaxf(M[nt], mx), f = exp2_fast(M[nt] - m);
+                mx = fmaf(mx, by, lv);
+                if (__ballot(mx > M[nt] + kSlack)) {
+                    const float m = fmaxf(M[nt], max_groups(mx)), f = exp2_fast(M[nt] - m);
                     l[nt] *= f;
 #pragma unroll
                     for (int k = 0; k < 4 * KJ; ++k) O[nt][k] *= f;
@@ -230,9 +230,10 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         lds_barrier();
     }
 
-    // a row's outputs are spread over the four lanes of one n16
+    // A row's outputs are spread over the four lanes of one n16.
+    const int tid = settle((int)threadIdx.x), n16e = settle(lane) & 15, ge = settle(lane) >> 4;
     typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-    auto emit = [&](int r, int i, f32x4 o, float m, float sum) {
+    auto emit = [&](int r, int i, f32x4 o, float m, float sum) __attribute__((always_inline)) {
         const int gr = row_w + r, tok = gr / group, head = w.h * group + gr - tok * group;
         const size_t to = (size_t)(w.q.row0 + tok) * A.n_head + head;
         const bool empty = first + tok < 0;
@@ -246,22 +247,22 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     };
     constexpr int kSlotBytes = ROWS * (DP + 2) * 4;   // outputs [ROWS][DP], then M and l [2][ROWS]
     const uint32_t step = (uint32_t)A.c.n_kv * kSlotBytes, item = ((uint32_t)w.slot * A.c.n_kv + w.h) * kSlotBytes;
-    const uint32_t mine = item + w.split * step;
-    const __amdgpu_buffer_rsrc_t part = buf_rsrc(A.part, 2u * kProTarget * kSlotBytes);
+    const uint32_t at_mine = item + w.split * step;
+    const __amdgpu_buffer_rsrc_t part = buf_rsrc(A.part, (uint32_t)kAttSlots * kSlotBytes);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int r = wave * 16 * NT + nt * 16 + n16;
+        const int r = wave * 16 * NT + nt * 16 + n16e;
         const float sum = sum_groups(l[nt]);
         const bool live = row_w + r < rows_all;
 #pragma unroll
         for (int k = 0; k < 4 * KJ; ++k) {
-            const int i = k * 16 + g * 4;
+            const int i = k * 16 + ge * 4;
             if (!live || i >= d) continue;
             if (w.splits == 1) emit(r, i, O[nt][k], M[nt], sum);
-            else st16_coherent(part, mine + (uint32_t)(r * DP + i) * 4, O[nt][k]);
+            else st16_coherent(part, at_mine + (uint32_t)(r * DP + i) * 4, O[nt][k]);
         }
-        if (w.splits > 1 && live && g == 0) {
-            float* st2 = reinterpret_cast<float*>(reinterpret_cast<char*>(A.part) + mine) + ROWS * DP + r;
+        if (w.splits > 1 && live && ge == 0) {
+            float* st2 = reinterpret_cast<float*>(reinterpret_cast<char*>(A.part) + at_mine) + ROWS * DP + r;
             st_coherent(st2, M[nt]);
             st_coherent(st2 + ROWS, sum);
         }
@@ -272,11 +273,11 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     uint32_t* ctr = A.ctr + ((size_t)w.slot * A.c.n_kv + w.h) * kAttCtrStride;
     wait_own_memory();
     __syncthreads();
-    if (threadIdx.x == 0) s_last = fetch_add_acq_rel(ctr, 1u) == (uint32_t)(w.splits - 1);
+    if (tid == 0) s_last = fetch_add_acq_rel(ctr, 1u) == (uint32_t)(w.splits - 1);
     __syncthreads();
     if (!s_last) return;
     const int rows = rows_all - row_w < ROWS ? rows_all - row_w : ROWS;
-    for (int r = threadIdx.x; r < rows; r += kProThreads) {
+    for (int r = tid; r < rows; r += kProThreads) {
         float m = kNone, sum = 0.f;
         for (int p = 0; p < w.splits; ++p) {
             const uint32_t at = item + p * step + (ROWS * DP + r) * 4;
@@ -288,27 +289,35 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         done[1][r] = sum;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < rows * (DP / 4); e += kProThreads) {
-        const int r = e / (DP / 4), i = e % (DP / 4) * 4;
-        if (i >= d) continue;
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        constexpr int kBatch = 8;
-        for (int p0 = 0; p0 < w.splits; p0 += kBatch) {
-            f32x4 v[kBatch];
-            float m[kBatch];
+    constexpr int kAtOnce = 4;   // outputs a thread loads of a piece at a time
+    static_assert(ROWS * (DP / 4) % (kProThreads * kAtOnce) == 0, "whole rounds");
+    for (int e0 = tid; e0 < ROWS * (DP / 4); e0 += kProThreads * kAtOnce) {
+        f32x4 o[kAtOnce];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const uint32_t from = item + (p0 + k < w.splits ? p0 + k : w.splits - 1) * step;
-                v[k] = ld16_coherent(part, (uint32_t)(r * DP + i) * 4, from);
-                m[k] = ld4_coherent(part, from + (ROWS * DP + r) * 4);
+        for (int k = 0; k < kAtOnce; ++k) o[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int p = 0; p < w.splits; ++p) {
+            f32x4 v[kAtOnce];
+            float m[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int e = e0 + k * kProThreads;
+                v[k] = ld16_coherent(part, (uint32_t)e * 16, item + p * step);
+                m[k] = ld4_coherent(part, item + p * step + (ROWS * DP + e / (DP / 4)) * 4);
             }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (p0 + k < w.splits) o += v[k] * exp2_fast(m[k] - done[0][r]);
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int r = (e0 + k * kProThreads) / (DP / 4);   // rows that nobody has are added up and left
+                o[k] += v[k] * exp2_fast(m[k] - done[0][r]);
+            }
         }
-        emit(r, i, o, done[0][r], done[1][r]);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int e = e0 + k * kProThreads, r = e / (DP / 4), i = e % (DP / 4) * 4;
+            if (r < rows && i < d) emit(r, i, o[k], done[0][r], done[1][r]);
+        }
     }
-    if (threadIdx.x == 0) st_flag(ctr, 0u);
+    if (tid == 0) st_flag(ctr, 0u);
 }
 
 template <int FMT, int KJ, bool FULL>
@@ -329,7 +338,7 @@ __global__ __launch_bounds__(kProThreads, 2) void k_attend_prompt(AttArgs A) {
 
 hipError_t launch_attend_prompt(AttArgs A, hipStream_t s) {
     const int kj = att_kj(A.c.d);
-    A.target = kProTarget;
+    A.target = pro_target(kj);
     A.min_tiles = kProMinTiles;
     const dim3 grid(A.c.n_kv, att_grid(A, prompt_rows(kj)));
     const size_t shm = (size_t)2 * 16 * kj * 1024;
@@ -337,7 +346,7 @@ hipError_t launch_attend_prompt(AttArgs A, hipStream_t s) {
     hipError_t e = hipSuccess;
 #define PI_PRO(F, K, U)                                                                                   \
     do {                                                                                                  \
-        if (shm + 24576 > 65536)                                                                          \
+        if (shm + 16384 > 65536)                                                                          \
             e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_prompt<F, K, U>),             \
                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);                \
         if (e == hipSuccess) hipLaunchKernelGGL((k_attend_prompt<F, K, U>), grid, dim3(kProThreads), shm, s, A); \
