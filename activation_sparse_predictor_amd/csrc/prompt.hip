@@ -30,6 +30,7 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 
 template <int FMT, int KJ, bool FULL>
 __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) {
+    static_assert(kProWaves == 4 && kProWaves % KJ == 0, "a thread's pieces");
     constexpr int NT = KJ == 4 ? 1 : 2, ROWS = kProWaves * 16 * NT, DP = 64 * KJ;
     static_assert(ROWS == prompt_rows(KJ), "rows of a workgroup");
     constexpr int kFrags = 16 * KJ;   // of a tile: 8 KJ of K, 8 KJ of V
@@ -87,19 +88,21 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     }
 
     // This thread's 2 KJ pieces of a tile's codes: of the 4 KJ groups of 64
-    // pieces of K, then the 4 KJ of V, wave v takes groups v, v + 4, ...
+    // pieces of K, then the 4 KJ of V, wave v takes groups v, v + 4, ..., which
+    // lie a fixed distance apart.
     u32x4 st[2 * KJ];
+    const uint8_t* const k0 = A.c.k + (wave / KJ) * 4 * d + (wave % KJ * 4 + g) * 64 + (n16 & 3) * 16;
+    const uint8_t* const v0 = A.c.v + (wave * 16 + n16) * 16;
     auto load = [&](int x) __attribute__((always_inline)) {
         const Gran* gr = &grans[(x & (kProRing - 1)) * (kTile / kGran)];
-        const uint8_t* kp = gran_at(A.c.k, gr[n16 >> 2]) + (n16 & 3) * 16;
-        const uint8_t* vp = gran_at(A.c.v, gr[g]) + n16 * 16;
+        const uint8_t* const kp = gran_at(k0, gr[n16 >> 2]);
+        const uint8_t* const vp = gran_at(v0, gr[g]);
 #pragma unroll
         for (int i = 0; i < KJ; ++i) {
-            const int un = wave + 4 * i, t = un / KJ, ch = un % KJ * 4 + g;
             const u32x4 zero = {Codes<FMT>::kZero4, Codes<FMT>::kZero4, Codes<FMT>::kZero4, Codes<FMT>::kZero4};
             st[i] = st[KJ + i] = zero;
-            if (FULL || ch < dc) st[i] = ld16(kp + t * 4 * d + ch * 64);
-            if (FULL || un < dc) st[KJ + i] = ld16(vp + un * 256);
+            if (FULL || wave % KJ * 4 + g < dc) st[i] = ld16(kp + i * (kProWaves / KJ) * 4 * d);
+            if (FULL || wave + 4 * i < dc) st[KJ + i] = ld16(vp + i * kProWaves * 256);
         }
     };
     auto store = [&](int x) __attribute__((always_inline)) {
@@ -233,17 +236,28 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     // A row's outputs are spread over the four lanes of one n16.
     const int tid = settle((int)threadIdx.x), n16e = settle(lane) & 15, ge = settle(lane) >> 4;
     typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-    auto emit = [&](int r, int i, f32x4 o, float m, float sum) __attribute__((always_inline)) {
+    // where row r's outputs go, and what its sums are multiplied by
+    struct Out {
+        h16* y;
+        float* lse;
+        float f;
+        bool empty;
+    };
+    auto out_of = [&](int r, float sum) __attribute__((always_inline)) {
         const int gr = row_w + r, tok = gr / group, head = w.h * group + gr - tok * group;
         const size_t to = (size_t)(w.q.row0 + tok) * A.n_head + head;
-        const bool empty = first + tok < 0;
         // no weight at all although there are keys: every score was -infinity
-        const float f = sum == 0.f ? __builtin_nanf("") : 1.f / sum;
+        return Out{A.y + to * d, A.lse ? A.lse + to : nullptr, sum == 0.f ? __builtin_nanf("") : 1.f / sum,
+                   first + tok < 0};
+    };
+    auto emit = [&](const Out& q, int i, f32x4 o) __attribute__((always_inline)) {
         f16x4 v;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = empty ? (f16)0.f : (f16)(o[k] * f);
-        *reinterpret_cast<f16x4*>(A.y + to * d + i) = v;
-        if (A.lse && i == 0) A.lse[to] = empty ? -__builtin_inff() : (m - kLift + log2_fast(sum)) * kLn2;
+        for (int k = 0; k < 4; ++k) v[k] = q.empty ? (f16)0.f : (f16)(o[k] * q.f);
+        *reinterpret_cast<f16x4*>(q.y + i) = v;
+    };
+    auto emit_lse = [&](const Out& q, float m, float sum) __attribute__((always_inline)) {
+        if (q.lse) *q.lse = q.empty ? -__builtin_inff() : (m - kLift + log2_fast(sum)) * kLn2;
     };
     constexpr int kSlotBytes = ROWS * (DP + 2) * 4;   // outputs [ROWS][DP], then M and l [2][ROWS]
     const uint32_t step = (uint32_t)A.c.n_kv * kSlotBytes, item = ((uint32_t)w.slot * A.c.n_kv + w.h) * kSlotBytes;
@@ -253,18 +267,22 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     for (int nt = 0; nt < NT; ++nt) {
         const int r = wave * 16 * NT + nt * 16 + n16e;
         const float sum = sum_groups(l[nt]);
-        const bool live = row_w + r < rows_all;
+        if (row_w + r >= rows_all) continue;
+        if (w.splits == 1) {
+            const Out q = out_of(r, sum);
 #pragma unroll
-        for (int k = 0; k < 4 * KJ; ++k) {
-            const int i = k * 16 + ge * 4;
-            if (!live || i >= d) continue;
-            if (w.splits == 1) emit(r, i, O[nt][k], M[nt], sum);
-            else st16_coherent(part, at_mine + (uint32_t)(r * DP + i) * 4, O[nt][k]);
-        }
-        if (w.splits > 1 && live && ge == 0) {
-            float* st2 = reinterpret_cast<float*>(reinterpret_cast<char*>(A.part) + at_mine) + ROWS * DP + r;
-            st_coherent(st2, M[nt]);
-            st_coherent(st2 + ROWS, sum);
+            for (int k = 0; k < 4 * KJ; ++k)
+                if (FULL || k < dc) emit(q, k * 16 + ge * 4, O[nt][k]);
+            if (ge == 0) emit_lse(q, M[nt], sum);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k)
+                if (FULL || k < dc) st16_coherent(part, at_mine + (uint32_t)(r * DP + k * 16 + ge * 4) * 4, O[nt][k]);
+            if (ge == 0) {
+                float* st2 = reinterpret_cast<float*>(reinterpret_cast<char*>(A.part) + at_mine) + ROWS * DP + r;
+                st_coherent(st2, M[nt]);
+                st_coherent(st2 + ROWS, sum);
+            }
         }
     }
     if (w.splits == 1) return;
@@ -314,7 +332,10 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
             const int e = e0 + k * kProThreads, r = e / (DP / 4), i = e % (DP / 4) * 4;
-            if (r < rows && i < d) emit(r, i, o[k], done[0][r], done[1][r]);
+            if (r >= rows || i >= d) continue;
+            const Out q = out_of(r, done[1][r]);
+            emit(q, i, o[k]);
+            if (i == 0) emit_lse(q, done[0][r], done[1][r]);
         }
     }
     if (tid == 0) st_flag(ctr, 0u);
