@@ -22,21 +22,21 @@
 // operand of the output's products, all share one page, and the V operand is
 // 16 contiguous bytes (a dimension's 16 tokens).  So nothing is shuffled or
 // staged between the two products, and a lane has one ks and one vs a step.
+#include <type_traits>
+
 #include "attend.hpp"
 
 namespace pi {
 
-constexpr int kAttWaves = 4;
-constexpr int kAttThreads = kAttWaves * kWave;
 constexpr int kAttRows = 16;   // query rows of a workgroup
 constexpr int kMinTiles = 4;   // fewest tiles worth a workgroup of their own
 // workgroups the work is split into: those that run at once, by the registers
-constexpr int single_target(int kj) { return kj == 4 ? 256 : 512; }
+constexpr int single_target(int kj, int waves) { return kj == 4 || waves == 8 ? 256 : 512; }
 
-// KJ: 64-dimension steps of a head; FULL: d is all of them.
-template <int FMT, int KJ, bool FULL>
+// KJ: 64-dimension steps of a head; FULL: d is all of them; WAVES: of a workgroup.
+template <int FMT, int KJ, bool FULL, int WAVES>
 __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) {
-    constexpr int ROWS = kAttRows, DP = 64 * KJ, LD = DP + 4;
+    constexpr int kAttWaves = WAVES, kAttThreads = WAVES * kWave, ROWS = kAttRows, DP = 64 * KJ, LD = DP + 4;
     extern __shared__ float lds[];   // while tiles are read: Gran [kSegGrans]; then the joins' arrays
     __shared__ int s_last;
     Gran* grans = reinterpret_cast<Gran*>(lds);
@@ -259,19 +259,20 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     if (!s_last) return;
     // Each row's reference and sum over the pieces: sixteen lanes a row, a
     // piece each.  The first outputs are already on their way meanwhile.
-    constexpr int kRowLanes = kAttThreads / ROWS, kBatch = 32;
-    float* fac = outs;   // [kJoin][ROWS]: what each piece is multiplied by
-    constexpr int kJoin = kAttWaves * LD < 256 ? kAttWaves * LD / kBatch * kBatch : 256;   // pieces whose factors fit
-    auto load = [&](f32x4 (&v)[kBatch], int p0, int r, int i) {
+    auto join = [&](auto batch) __attribute__((always_inline)) {
+        constexpr int kBatch = decltype(batch)::value;   // pieces loaded at a time
+        constexpr int kRowLanes = kAttThreads / ROWS;
+        constexpr int kJoin = kAttWaves * LD < 256 ? kAttWaves * LD / 32 * 32 : 256;   // pieces whose factors fit
+        float* fac = outs;   // [kJoin][ROWS]: what each piece is multiplied by
+        auto load = [&](f32x4 (&v)[kBatch], int p0, int r, int i) __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            v[k] = ld16_coherent(part, (uint32_t)(r * DP + i) * 4, item + (p0 + k < w.splits ? p0 + k : w.splits - 1) * step);
-    };
-    f32x4 v[kBatch];
-    const int e0 = threadIdx.x, r0 = e0 / (DP / 4), i0 = e0 % (DP / 4) * 4;
-    load(v, 0, r0 < ROWS ? r0 : 0, i0);
-    const int sr = threadIdx.x / kRowLanes, sj = threadIdx.x % kRowLanes;
-    {
+            for (int k = 0; k < kBatch; ++k)
+                v[k] = ld16_coherent(part, (uint32_t)(r * DP + i) * 4, item + (p0 + k < w.splits ? p0 + k : w.splits - 1) * step);
+        };
+        f32x4 v[kBatch];
+        const int e0 = threadIdx.x, r0 = e0 / (DP / 4), i0 = e0 % (DP / 4) * 4;
+        load(v, 0, r0 < ROWS ? r0 : 0, i0);
+        const int sr = threadIdx.x / kRowLanes, sj = threadIdx.x % kRowLanes;
         float Mr = kNone, sum = 0.f;
         for (int p = sj; p < w.splits; p += kRowLanes) {
             const uint32_t st = item + p * step + (ROWS * DP + sr) * 4;
@@ -291,40 +292,45 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
             done[sr] = Mr;
             done[ROWS + sr] = sum;
         }
-    }
-    __syncthreads();
-    for (int e = e0; e < ROWS * (DP / 4); e += kAttThreads) {
-        const int r = e / (DP / 4), i = e % (DP / 4) * 4;
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int p0 = 0; p0 < w.splits; p0 += kJoin) {
-            const int np = w.splits - p0 < kJoin ? w.splits - p0 : kJoin;
-            if (e == e0 || w.splits > kJoin) {   // otherwise the factors are still there
-                __syncthreads();
-                for (int p = sj; p < np; p += kRowLanes)
-                    fac[p * ROWS + sr] = exp2_fast(ld4_coherent(part, item + (p0 + p) * step + (ROWS * DP + sr) * 4) - done[sr]);
-                __syncthreads();
-            }
-            for (int p = 0; p < np; p += kBatch) {
-                if (e != e0 || p0 + p > 0) load(v, p0 + p, r, i);
+        __syncthreads();
+        // (every thread takes every round: there are barriers in them)
+        for (int e = e0; e - e0 < ROWS * (DP / 4); e += kAttThreads) {
+            const int r = e / (DP / 4), i = e % (DP / 4) * 4;
+            const bool has = r < rows && i < d;
+            f32x4 o = {0.f, 0.f, 0.f, 0.f};
+            for (int p0 = 0; p0 < w.splits; p0 += kJoin) {
+                const int np = w.splits - p0 < kJoin ? w.splits - p0 : kJoin;
+                if (e == e0 || w.splits > kJoin) {   // otherwise the factors are still there
+                    __syncthreads();
+                    for (int p = sj; p < np; p += kRowLanes)
+                        fac[p * ROWS + sr] = exp2_fast(ld4_coherent(part, item + (p0 + p) * step + (ROWS * DP + sr) * 4) - done[sr]);
+                    __syncthreads();
+                }
+                if (!has) continue;
+                for (int p = 0; p < np; p += kBatch) {
+                    if (e != e0 || p0 + p > 0) load(v, p0 + p, r, i);
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k)
-                    if (p + k < np) o += v[k] * fac[(p + k) * ROWS + r];
+                    for (int k = 0; k < kBatch; ++k)
+                        if (p + k < np) o += v[k] * fac[(p + k) * ROWS + r];
+                }
             }
+            if (has) emit(r, i, o);
         }
-        if (r < rows && i < d) emit(r, i, o);
-    }
+    };
+    if (w.splits <= 8) join(std::integral_constant<int, 8>{});
+    else join(std::integral_constant<int, 32>{});
     if (threadIdx.x == 0) st_flag(ctr, 0u);
 }
 
 // A workgroup takes units until there are none: whatever the lengths on the
 // device say, every piece of every item runs, and the counters end at zero.
-template <int FMT, int KJ, bool FULL>
-__global__ __launch_bounds__(kAttThreads, KJ == 4 ? 1 : 2) void k_attend(AttArgs A) {
+template <int FMT, int KJ, bool FULL, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave, KJ == 4 ? 1 : 2) void k_attend(AttArgs A) {
     AttUnit w;
     w.h = blockIdx.x;
     const int units = att_plan<kAttRows>(A, blockIdx.y, w);
     for (int u = blockIdx.y; u < units;) {
-        attend_unit<FMT, KJ, FULL>(A, w);
+        attend_unit<FMT, KJ, FULL, WAVES>(A, w);
         u += gridDim.y;
         if (u < units) {
             __syncthreads();   // the next unit uses the same shared memory
@@ -340,22 +346,52 @@ constexpr int kSingleRows = 64;
 
 size_t kv_attend_bytes(int, int, int max_q, int n_head, int n_kv, int d) {
     const int kj = att_kj(d);
-    size_t rows = (size_t)2 * single_target(kj) * kAttRows;
-    if ((long long)max_q * (n_head / n_kv) > kSingleRows) {
-        const size_t more = (size_t)kAttSlots * prompt_rows(kj);
-        rows = more > rows ? more : rows;
-    }
+    size_t rows = (size_t)kAttSlots * kAttRows;
+    if ((long long)max_q * (n_head / n_kv) > kSingleRows) rows = (size_t)kAttSlots * prompt_rows(kj);
     return kv_attend_zero_bytes() + rows * (64 * kj + 2) * 4;
+}
+
+template <int FMT, int KJ, bool FULL, int WAVES>
+static hipError_t launch_single(const AttArgs& A, hipStream_t s) {
+    constexpr size_t joins = ((size_t)WAVES * (64 * KJ + 4 + 2) + 2) * kAttRows * 4, looks = kSegGrans * sizeof(Gran);
+    constexpr size_t shm = joins > looks ? joins : looks;
+    if (shm > 65536) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<FMT, KJ, FULL, WAVES>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);
+        if (e != hipSuccess) return e;
+    }
+    // heads side by side: the row tiles that read one head's pages run on one
+    // XCD where the heads are a multiple of 8, and share its L2
+    hipLaunchKernelGGL((k_attend<FMT, KJ, FULL, WAVES>), dim3(A.c.n_kv, att_grid(A, kAttRows)), dim3(WAVES * kWave), shm,
+                       s, A);
+    return hipGetLastError();
+}
+
+template <int FMT>
+static hipError_t launch_singles(AttArgs A, hipStream_t s) {
+    const int kj = att_kj(A.c.d);
+    const bool full = A.c.d == 64 * kj;
+    // Where all items run at once, one eight-wave workgroup a CU each: half as
+    // many pieces to join (16 sequences of 4 x 8 rows, window 4097: 39 us
+    // against 61 with four waves; 131072 tokens: 36 against 44).  Where there
+    // are more, two four-wave workgroups a CU, one's start and end beside the
+    // other's loads (64 sequences of 72 heads: 242 us against 290 with eight).
+    const int waves = kj < 4 && att_most_row_tiles(A.b, A.group, kAttRows) * A.c.n_kv <= 256 ? 8 : 4;
+    A.target = single_target(kj, waves);
+    A.min_tiles = kMinTiles;
+    if (kj == 4) return full ? launch_single<FMT, 4, true, 4>(A, s) : launch_single<FMT, 4, false, 4>(A, s);
+    if (kj == 2 && waves == 8) return full ? launch_single<FMT, 2, true, 8>(A, s) : launch_single<FMT, 2, false, 8>(A, s);
+    if (kj == 2) return full ? launch_single<FMT, 2, true, 4>(A, s) : launch_single<FMT, 2, false, 4>(A, s);
+    if (waves == 8) return full ? launch_single<FMT, 1, true, 8>(A, s) : launch_single<FMT, 1, false, 8>(A, s);
+    return full ? launch_single<FMT, 1, true, 4>(A, s) : launch_single<FMT, 1, false, 4>(A, s);
 }
 
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
                             float scale, int window, h16* y, float* lse, char* data, hipStream_t s) {
-    const int group = n_head / c.n_kv, kj = att_kj(c.d);
+    const int group = n_head / c.n_kv;
     const long long most_rows = (long long)b.max_q * group;
-    AttArgs A{c, b, q, q_stride, n_head, group, window, 0, 0x7FFFFFFF, single_target(kj), kMinTiles,
-              scale * 1.4426950408889634f, y, lse,
+    AttArgs A{c, b, q, q_stride, n_head, group, window, 0, 0x7FFFFFFF, 0, 0, scale * 1.4426950408889634f, y, lse,
               reinterpret_cast<uint32_t*>(data), reinterpret_cast<float*>(data + kv_attend_zero_bytes())};
-    hipError_t e = hipSuccess;
     if (most_rows > kSingleRows) {
         // rows of long and short sequences: each kernel takes its own (they
         // share the workspace, one after the other)
@@ -363,31 +399,10 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, lo
         AttArgs P = A;
         P.above = kSingleRows;
         P.upto = 0x7FFFFFFF;
-        e = launch_attend_prompt(P, s);
+        const hipError_t e = launch_attend_prompt(P, s);
         if (e != hipSuccess || b.n_tok == (long long)b.n_seq * b.max_q) return e;   // no short ones
     }
-    // heads side by side: the row tiles that read one head's pages run on one
-    // XCD where the heads are a multiple of 8, and share its L2
-    const dim3 grid(c.n_kv, att_grid(A, kAttRows));
-    const size_t joins = ((size_t)kAttWaves * (64 * kj + 4 + 2) + 2) * kAttRows * 4, looks = kSegGrans * sizeof(Gran);
-    const size_t shm = joins > looks ? joins : looks;
-    const bool full = c.d == 64 * kj;
-#define PI_ATT(F, K, U)                                                                            \
-    do {                                                                                           \
-        if (shm > 65536)                                                                           \
-            e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<F, K, U>),             \
-                                    hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);         \
-        if (e == hipSuccess) hipLaunchKernelGGL((k_attend<F, K, U>), grid, dim3(kAttThreads), shm, s, A); \
-    } while (0)
-#define PI_ATT_D(F)                                                          \
-    if (kj == 1) { if (full) PI_ATT(F, 1, true); else PI_ATT(F, 1, false); }  \
-    else if (kj == 2) { if (full) PI_ATT(F, 2, true); else PI_ATT(F, 2, false); } \
-    else { if (full) PI_ATT(F, 4, true); else PI_ATT(F, 4, false); }
-    if (c.fmt == 0) { PI_ATT_D(0); } else { PI_ATT_D(1); }
-#undef PI_ATT_D
-#undef PI_ATT
-    if (e != hipSuccess) return e;
-    return hipGetLastError();
+    return c.fmt == 0 ? launch_singles<0>(A, s) : launch_singles<1>(A, s);
 }
 
 }  // namespace pi

@@ -222,7 +222,7 @@ inline long long att_most_row_tiles(const KvBatch& b, int group, int rows) {
     const long long all = (long long)b.n_tok * group / rows + b.n_seq;
     return each < all ? each : all;
 }
-// Units of one head that the plan can come to.
+// Units of one head that the plan can come to (more would be taken in turn).
 inline unsigned att_grid(const AttArgs& A, int rows) {
     const long long items = att_most_row_tiles(A.b, A.group, rows);
     const long long cap = ((long long)A.b.table_stride * A.c.page + kTile - 1) / kTile;
