@@ -341,13 +341,22 @@ __global__ __launch_bounds__(WAVES * kWave, KJ == 4 ? 1 : 2) void k_attend(AttAr
 
 size_t kv_attend_zero_bytes() { return (size_t)kAttSlots * kAttCtrStride * 4; }
 
-// Sequences with more rows than this go to the prompt kernel.
-constexpr int kSingleRows = 64;
+// Whether sequences with many rows go to the prompt kernel, and how many are
+// many.  Where the 16-row items of all heads are at most what runs at once
+// (two workgroups a CU), this kernel's split over the context serves them
+// better (64 rows on 8192 tokens, 8 kv heads: 22 us against 51; 128 x 128 rows
+// of 56 heads on 1024: 22 against 31); beyond that every item reads its keys
+// again, and the prompt kernel is faster from 33 rows on (8 sequences of 56
+// heads on 2048 tokens, 33 rows each: 79 us against 99, 128 rows: 96 against 243).
+constexpr int kSingleRows = 32;
+static bool uses_prompt(const KvBatch& b, int group, int n_kv) {
+    return (long long)b.max_q * group > kSingleRows && att_most_row_tiles(b, group, kAttRows) * n_kv > 512;
+}
 
-size_t kv_attend_bytes(int, int, int max_q, int n_head, int n_kv, int d) {
+size_t kv_attend_bytes(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d) {
     const int kj = att_kj(d);
-    size_t rows = (size_t)kAttSlots * kAttRows;
-    if ((long long)max_q * (n_head / n_kv) > kSingleRows) rows = (size_t)kAttSlots * prompt_rows(kj);
+    const KvBatch b{n_seq, n_tok, max_q, 0, 0, nullptr, nullptr, nullptr};
+    const size_t rows = (size_t)kAttSlots * (uses_prompt(b, n_head / n_kv, n_kv) ? prompt_rows(kj) : kAttRows);
     return kv_attend_zero_bytes() + rows * (64 * kj + 2) * 4;
 }
 
@@ -389,10 +398,9 @@ static hipError_t launch_singles(AttArgs A, hipStream_t s) {
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
                             float scale, int window, h16* y, float* lse, char* data, hipStream_t s) {
     const int group = n_head / c.n_kv;
-    const long long most_rows = (long long)b.max_q * group;
     AttArgs A{c, b, q, q_stride, n_head, group, window, 0, 0x7FFFFFFF, 0, 0, scale * 1.4426950408889634f, y, lse,
               reinterpret_cast<uint32_t*>(data), reinterpret_cast<float*>(data + kv_attend_zero_bytes())};
-    if (most_rows > kSingleRows) {
+    if (uses_prompt(b, group, c.n_kv)) {
         // rows of long and short sequences: each kernel takes its own (they
         // share the workspace, one after the other)
         A.upto = kSingleRows;
