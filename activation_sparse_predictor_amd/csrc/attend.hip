@@ -28,6 +28,7 @@
 
 namespace pi {
 
+constexpr float kLift = 15.7f, kSlack = 0.25f;   // of the references, above
 constexpr int kAttRows = 16;   // query rows of a workgroup
 constexpr int kMinTiles = 4;   // fewest tiles worth a workgroup of their own
 // workgroups the work is split into: those that run at once, by the registers

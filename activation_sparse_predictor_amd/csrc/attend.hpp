@@ -13,7 +13,7 @@ constexpr int kAttMaxTarget = 512;   // most workgroups that the work is split i
 constexpr int kAttSlots = 2 * kAttMaxTarget;
 constexpr int kAttCtrStride = 16;    // words between arrival counters
 
-constexpr float kLift = 15.7f, kSlack = 0.25f, kZeroLog = -64.f, kNone = -1e30f, kLn2 = 0.69314718055994531f;
+constexpr float kZeroLog = -64.f, kNone = -1e30f, kLn2 = 0.69314718055994531f;
 
 // max over the lanes that hold the same query (lane ^ 16, lane ^ 32)
 __device__ __forceinline__ float max_groups(float v) {

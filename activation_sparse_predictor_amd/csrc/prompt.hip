@@ -17,6 +17,11 @@
 
 namespace pi {
 
+// The reference moves when a maximum is more than 2.9 above it, which after a
+// row's first tiles hardly happens (a move multiplies all outputs; with 0.25,
+// as in attend.hip, moves took a tenth of the time).  fp16 then holds a weight
+// down to 2^-37 of the row's largest.
+constexpr float kLift = 13.f, kSlack = 2.9f;
 constexpr int kProWaves = 4;
 constexpr int kProThreads = kProWaves * kWave;
 constexpr int pro_target(int kj) { return kj == 4 ? 256 : 512; }   // workgroups that run at once, by LDS
@@ -105,22 +110,17 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
             if (FULL || wave + 4 * i < dc) st[KJ + i] = ld16(vp + i * kProWaves * 256);
         }
     };
-    auto store = [&](int x) __attribute__((always_inline)) {
+    auto store = [&](int x, int i) __attribute__((always_inline)) {   // piece i
         const int tile0 = (w.t0 + x) * kTile, key0 = tile0 + g * kGran;
-        u32x4* to = frags + (x & 1) * kFrags * 64 + lane;
-        if (FMT == 1 && (tile0 < any_from || tile0 + kTile - 1 > any_to)) {   // slots that no row here attends to may hold NaN
+        u32x4* to = frags + ((x & 1) * kFrags + 2 * wave) * 64 + lane;
+        u32x4 v = st[i];
+        if (FMT == 1 && i >= KJ && (tile0 < any_from || tile0 + kTile - 1 > any_to)) {   // slots that no row here attends to may hold NaN
 #pragma unroll
-            for (int i = KJ; i < 2 * KJ; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) st[i][j] = keep_tokens(st[i][j], key0 + 4 * j, any_from, any_to);
+            for (int j = 0; j < 4; ++j) v[j] = keep_tokens(v[j], key0 + 4 * j, any_from, any_to);
         }
-#pragma unroll
-        for (int i = 0; i < 2 * KJ; ++i) {
-            const int un = wave + 4 * (i % KJ);
-            const int f = i < KJ ? (un / KJ) * 2 * KJ + un % KJ * 2 : 8 * KJ + un * 2;
-            to[f * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(st[i].x, st[i].y));
-            to[(f + 1) * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(st[i].z, st[i].w));
-        }
+        // group u of K makes fragments 2 u and 2 u + 1 of the tile, group u of V 8 KJ + 2 u and the next
+        to[i * 2 * kProWaves * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(v.x, v.y));
+        to[(i * 2 * kProWaves + 1) * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(v.z, v.w));
     };
 
     float M[NT], l[NT];
@@ -137,7 +137,8 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         fill(0, n < kProSeg ? n : kProSeg);
         __syncthreads();
         load(0);
-        store(0);
+#pragma unroll
+        for (int i = 0; i < 2 * KJ; ++i) store(0, i);
         if (n > 1) load(1);
         lds_barrier();
     }
@@ -146,7 +147,10 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
             const int left = n - x - kProSeg;
             fill(x + kProSeg, left < kProSeg ? left : kProSeg);
         }
-        if (x + 1 < n) store(x + 1);
+        if (x + 1 < n) {
+#pragma unroll
+            for (int i = 0; i < 2 * KJ; ++i) store(x + 1, i);
+        }
         if (x + 2 < n) load(x + 2);
         const int tile0 = (w.t0 + x) * kTile;
         if (tile0 <= v_to && tile0 + kTile - 1 >= v_from) {
