@@ -122,3 +122,13 @@ def test_runtime_refuses_what_it_cannot_pass_on():
     for t in (x.float(), x[:2], x[:, :1], x.transpose(0, 1), torch.zeros(3, 64, 2, dtype=torch.float16).transpose(1, 2)):
         with pytest.raises(ValueError):
             R._kv_rows(t, 3, 2, 64, "k")
+
+
+def test_rows_above_the_limit_refused():
+    """n_tok * n_head / n_kv above PI_KV_MAX_ROWS: attention refuses, append and read do not count heads."""
+    b = batch(n_tok=1 << 20, max_q=1 << 20)
+    st = B.pi_kv_attend(cache(n_kv=1), b, A, 64 * 64, 64, 0.1, 0, A, None, A, 1 << 40, 0)
+    assert st == UNSUP and "PI_KV_MAX_ROWS" in B.last_error()
+    with pytest.raises(B.PiError) as e:
+        B.pi_kv_workspace_size(2, 1 << 20, 1 << 20, 64, 1, 64)
+    assert e.value.status == UNSUP
