@@ -399,6 +399,7 @@ static hipError_t launch_singles(AttArgs A, hipStream_t s) {
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
                             float scale, int window, h16* y, float* lse, char* data, hipStream_t s) {
     const int group = n_head / c.n_kv;
+    if (window > 0x3FFFFFFF) window = 0;   // above any length (and positions less it would pass 32 bits)
     AttArgs A{c, b, q, q_stride, n_head, group, window, 0, 0x7FFFFFFF, 0, 0, scale * 1.4426950408889634f, y, lse,
               reinterpret_cast<uint32_t*>(data), reinterpret_cast<float*>(data + kv_attend_zero_bytes())};
     if (uses_prompt(b, group, c.n_kv)) {

@@ -539,3 +539,14 @@ def test_broken_lengths_stay_inside():
     k, v = R.kv_read(cache, bad)
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("n", [1, 20, 90])
+def test_attend_widest_windows(n):
+    """A window as wide as the type is no window, also for rows before position 0."""
+    ctx = [n // 2 + 1, 200, 0]
+    cache, rows = filled(ctx, 2, 64, 16, "int8")
+    batch, q = R.kv_batch([n, 1, n], ctx, [r or [0] for r in rows], DEV), queries(2 * n + 1, 8, 64)
+    y0 = check_attend(cache, batch, q)
+    for window in (2 ** 31 - 1, 2 ** 30, 2 ** 30 - 1, 201):
+        assert torch.equal(check_attend(cache, batch, q, window=window), y0)
