@@ -163,12 +163,12 @@ __global__ __launch_bounds__(256) void k_kv_append(KvCache c, KvBatch b, const h
         const int g = u / dp * kGran;
         if (g >= e || (g + kGran <= a && !grew)) continue;
         u32x4* at = reinterpret_cast<u32x4*>(dst + (size_t)u * 32);
-        // the granule's new codes, for both dimensions, [a, e) of them to be used
+        // the granule's new codes for both dimensions, [a, e) of them to be used
         u32x4 n[2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t lo4 = Codes<FMT>::kZero4, hi4 = lo4;
-            if (!zero) {
+            if (!zero && g + 4 * j + 3 >= a && g + 4 * j < e) {
                 const uint32_t p = x[i][4 * j], y = x[i][4 * j + 1], z = x[i][4 * j + 2], w = x[i][4 * j + 3];
                 lo4 = encode4_f16<FMT>((p & 0xFFFFu) | (y << 16), (z & 0xFFFFu) | (w << 16), s, inv);
                 hi4 = encode4_f16<FMT>((p >> 16) | (y & 0xFFFF0000u), (z >> 16) | (w & 0xFFFF0000u), s, inv);
@@ -176,14 +176,25 @@ __global__ __launch_bounds__(256) void k_kv_append(KvCache c, KvBatch b, const h
             n[0][j] = lo4;
             n[1][j] = hi4;
         }
-        if (g < a || e < g + kGran) {   // keep, or round again, what is not new
+        if (g >= a && g + kGran <= e) {
+            at[0] = n[0];
+            at[1] = n[1];
+        } else if (!grew) {   // single bytes, without waiting for what lies between them
+            uint8_t* b = reinterpret_cast<uint8_t*>(at);
+#pragma unroll
+            for (int t = 0; t < kGran; ++t) {
+                if (g + t < a || g + t >= e) continue;
+                b[t] = (uint8_t)(n[0][t / 4] >> (t % 4 * 8));
+                b[kGran + t] = (uint8_t)(n[1][t / 4] >> (t % 4 * 8));
+            }
+        } else {   // the older codes rounded again, and what lies behind the new ones kept
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const u32x4 o = at[k];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int t = g + 4 * j;
-                    const uint32_t again = grew ? requant4<FMT>(o[j], r) : o[j];
+                    const uint32_t again = t < a ? requant4<FMT>(o[j], r) : 0u;
                     uint32_t keep = 0u;
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
@@ -193,9 +204,9 @@ __global__ __launch_bounds__(256) void k_kv_append(KvCache c, KvBatch b, const h
                     n[k][j] = keep;
                 }
             }
+            at[0] = n[0];
+            at[1] = n[1];
         }
-        at[0] = n[0];
-        at[1] = n[1];
     }
 }
 
