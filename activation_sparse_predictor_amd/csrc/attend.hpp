@@ -157,6 +157,10 @@ __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) 
 __device__ __forceinline__ void st16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at, f32x4 v) {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, (int)at, 0, 16);
 }
+__device__ __forceinline__ void st8_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at, float a, float b) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(a), __float_as_uint(b)}, r, (int)at, 0, 16);
+}
 __device__ __forceinline__ f32x4 ld16_coherent(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t from) {
     return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, (int)from, 16));
 }

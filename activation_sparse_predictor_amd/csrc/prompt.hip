@@ -41,7 +41,6 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     constexpr int kFrags = 16 * KJ;   // of a tile: 8 KJ of K, 8 KJ of V
     extern __shared__ u32x4 frags[];  // [2][kFrags][64]
     __shared__ Gran grans[kProRing * (kTile / kGran)];
-    __shared__ float done[2][ROWS];
     __shared__ int s_last;
     // (settled, so that what follows from them is not kept in registers from
     // unit to unit)
@@ -143,6 +142,15 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         lds_barrier();
     }
     for (int x = 0; x < n; ++x) {
+        // Of the two workgroups of a CU the younger one's waves get what the
+        // older one's leave.  A priority that falls every second tile, and starts
+        // again, keeps the two abreast, so that they end together.
+        switch (x / 2 & 3) {
+            case 0: __builtin_amdgcn_s_setprio(3); break;
+            case 1: __builtin_amdgcn_s_setprio(2); break;
+            case 2: __builtin_amdgcn_s_setprio(1); break;
+            default: __builtin_amdgcn_s_setprio(0);
+        }
         if (x % kProSeg == 0 && x + kProSeg < n) {   // the next segment, in the half of the ring that is done with
             const int left = n - x - kProSeg;
             fill(x + kProSeg, left < kProSeg ? left : kProSeg);
@@ -237,112 +245,115 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         lds_barrier();
     }
 
-    // A row's outputs are spread over the four lanes of one n16.
+    // The item's pieces are joined by the one that is done last, which keeps its
+    // own results in registers: only the others' travel, as their lanes hold them.
     const int tid = settle((int)threadIdx.x), n16e = settle(lane) & 15, ge = settle(lane) >> 4;
-    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-    // where row r's outputs go, and what its sums are multiplied by
-    struct Out {
-        h16* y;
-        float* lse;
-        float f;
-        bool empty;
-    };
-    auto out_of = [&](int r, float sum) __attribute__((always_inline)) {
-        const int gr = row_w + r, tok = gr / group, head = w.h * group + gr - tok * group;
-        const size_t to = (size_t)(w.q.row0 + tok) * A.n_head + head;
-        // no weight at all although there are keys: every score was -infinity
-        return Out{A.y + to * d, A.lse ? A.lse + to : nullptr, sum == 0.f ? __builtin_nanf("") : 1.f / sum,
-                   first + tok < 0};
-    };
-    auto emit = [&](const Out& q, int i, f32x4 o) __attribute__((always_inline)) {
-        f16x4 v;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = q.empty ? (f16)0.f : (f16)(o[k] * q.f);
-        *reinterpret_cast<f16x4*>(q.y + i) = v;
-    };
-    auto emit_lse = [&](const Out& q, float m, float sum) __attribute__((always_inline)) {
-        if (q.lse) *q.lse = q.empty ? -__builtin_inff() : (m - kLift + log2_fast(sum)) * kLn2;
-    };
-    constexpr int kSlotBytes = ROWS * (DP + 2) * 4;   // outputs [ROWS][DP], then M and l [2][ROWS]
-    const uint32_t step = (uint32_t)A.c.n_kv * kSlotBytes, item = ((uint32_t)w.slot * A.c.n_kv + w.h) * kSlotBytes;
-    const uint32_t at_mine = item + w.split * step;
-    const __amdgpu_buffer_rsrc_t part = buf_rsrc(A.part, (uint32_t)kAttSlots * kSlotBytes);
+    for (int nt = 0; nt < NT; ++nt) l[nt] = sum_groups(l[nt]);
+    if (w.splits > 1) {
+        constexpr int kSlotBytes = ROWS * (DP + 2) * 4;   // [NT][4 KJ][threads] of four outputs, then [ROWS] of M and l
+        const uint32_t step = (uint32_t)A.c.n_kv * kSlotBytes, item = ((uint32_t)w.slot * A.c.n_kv + w.h) * kSlotBytes;
+        const __amdgpu_buffer_rsrc_t part = buf_rsrc(A.part, (uint32_t)kAttSlots * kSlotBytes);
+        const uint32_t at_o = (uint32_t)tid * 16, at_m = (uint32_t)(ROWS * DP + (wave * 16 * NT + n16e) * 2) * 4;
+        uint32_t* ctr = A.ctr + ((size_t)w.slot * A.c.n_kv + w.h) * kAttCtrStride;   // pieces done, pieces written
+        if (tid == 0) s_last = fetch_add(ctr, 1u) == (uint32_t)(w.splits - 1);
+        __syncthreads();
+        if (!s_last) {
+            const uint32_t mine = item + w.split * step;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int k = 0; k < 4 * KJ; ++k)
+                    if (FULL || k < dc) st16_coherent(part, mine + at_o + (nt * 4 * KJ + k) * kProThreads * 16, O[nt][k]);
+                if (ge == 0) st8_coherent(part, mine + at_m + nt * 128, M[nt], l[nt]);
+            }
+            wait_own_memory();
+            __syncthreads();
+            if (tid == 0) fetch_add(ctr + 1, 1u);
+            return;
+        }
+        // The others are done and running: nothing that they wait for is held here.
+        if (tid == 0) {
+            while (ld_flag(ctr + 1) < (uint32_t)(w.splits - 1)) __builtin_amdgcn_s_sleep(1);
+            st_flag(ctr, 0u);
+            st_flag(ctr + 1, 0u);
+        }
+        __syncthreads();
+        float m[NT], sum[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) m[nt] = M[nt], sum[nt] = 0.f;
+        for (int p = 0; p < w.splits; ++p) {
+            if (p == w.split) continue;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) m[nt] = fmaxf(m[nt], ld4_coherent(part, item + p * step + at_m + nt * 128));
+        }
+        f32x4 o[NT][4 * KJ];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k) o[nt][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int p = 0; p < w.splits; ++p) {   // in their order, whoever joins them
+            f32x4 v[NT][4 * KJ];
+            float f[NT], pl[NT];
+            if (p == w.split) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    f[nt] = M[nt], pl[nt] = l[nt];
+#pragma unroll
+                    for (int k = 0; k < 4 * KJ; ++k) v[nt][k] = O[nt][k];
+                }
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    f[nt] = ld4_coherent(part, item + p * step + at_m + nt * 128);
+                    pl[nt] = ld4_coherent(part, item + p * step + at_m + nt * 128 + 4);
+#pragma unroll
+                    for (int k = 0; k < 4 * KJ; ++k) {
+                        v[nt][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        if (FULL || k < dc) v[nt][k] = ld16_coherent(part, at_o + (nt * 4 * KJ + k) * kProThreads * 16, item + p * step);
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                f[nt] = exp2_fast(f[nt] - m[nt]);
+                sum[nt] = fmaf(pl[nt], f[nt], sum[nt]);
+#pragma unroll
+                for (int k = 0; k < 4 * KJ; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[nt][k][j] = fmaf(v[nt][k][j], f[nt], o[nt][k][j]);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            M[nt] = m[nt], l[nt] = sum[nt];
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k) O[nt][k] = o[nt][k];
+        }
+    }
+
+    // A row's outputs are spread over the four lanes of one n16.
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int r = wave * 16 * NT + nt * 16 + n16e;
-        const float sum = sum_groups(l[nt]);
-        if (row_w + r >= rows_all) continue;
-        if (w.splits == 1) {
-            const Out q = out_of(r, sum);
+        const int row = row_w + wave * 16 * NT + nt * 16 + n16e;
+        if (row >= rows_all) continue;
+        const int tok = row / group, head = w.h * group + row - tok * group;
+        const size_t to = (size_t)(w.q.row0 + tok) * A.n_head + head;
+        const bool empty = first + tok < 0;
+        // no weight at all although there are keys: every score was -infinity
+        const float f = l[nt] == 0.f ? __builtin_nanf("") : 1.f / l[nt];
 #pragma unroll
-            for (int k = 0; k < 4 * KJ; ++k)
-                if (FULL || k < dc) emit(q, k * 16 + ge * 4, O[nt][k]);
-            if (ge == 0) emit_lse(q, M[nt], sum);
-        } else {
+        for (int k = 0; k < 4 * KJ; ++k) {
+            if (!FULL && k >= dc) continue;
+            f16x4 v;
 #pragma unroll
-            for (int k = 0; k < 4 * KJ; ++k)
-                if (FULL || k < dc) st16_coherent(part, at_mine + (uint32_t)(r * DP + k * 16 + ge * 4) * 4, O[nt][k]);
-            if (ge == 0) {
-                float* st2 = reinterpret_cast<float*>(reinterpret_cast<char*>(A.part) + at_mine) + ROWS * DP + r;
-                st_coherent(st2, M[nt]);
-                st_coherent(st2 + ROWS, sum);
-            }
+            for (int j = 0; j < 4; ++j) v[j] = empty ? (f16)0.f : (f16)(O[nt][k][j] * f);
+            *reinterpret_cast<f16x4*>(A.y + to * d + k * 16 + ge * 4) = v;
         }
+        if (A.lse && ge == 0) A.lse[to] = empty ? -__builtin_inff() : (M[nt] - kLift + log2_fast(l[nt])) * kLn2;
     }
-    if (w.splits == 1) return;
-
-    // the last of the item's pieces to arrive joins them, in their order
-    uint32_t* ctr = A.ctr + ((size_t)w.slot * A.c.n_kv + w.h) * kAttCtrStride;
-    wait_own_memory();
-    __syncthreads();
-    if (tid == 0) s_last = fetch_add_acq_rel(ctr, 1u) == (uint32_t)(w.splits - 1);
-    __syncthreads();
-    if (!s_last) return;
-    const int rows = rows_all - row_w < ROWS ? rows_all - row_w : ROWS;
-    for (int r = tid; r < rows; r += kProThreads) {
-        float m = kNone, sum = 0.f;
-        for (int p = 0; p < w.splits; ++p) {
-            const uint32_t at = item + p * step + (ROWS * DP + r) * 4;
-            const float pm = ld4_coherent(part, at), ps = ld4_coherent(part, at + ROWS * 4), nm = fmaxf(m, pm);
-            sum = sum * exp2_fast(m - nm) + ps * exp2_fast(pm - nm);
-            m = nm;
-        }
-        done[0][r] = m;
-        done[1][r] = sum;
-    }
-    __syncthreads();
-    constexpr int kAtOnce = 4;   // outputs a thread loads of a piece at a time
-    static_assert(ROWS * (DP / 4) % (kProThreads * kAtOnce) == 0, "whole rounds");
-    for (int e0 = tid; e0 < ROWS * (DP / 4); e0 += kProThreads * kAtOnce) {
-        f32x4 o[kAtOnce];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) o[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int p = 0; p < w.splits; ++p) {
-            f32x4 v[kAtOnce];
-            float m[kAtOnce];
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                const int e = e0 + k * kProThreads;
-                v[k] = ld16_coherent(part, (uint32_t)e * 16, item + p * step);
-                m[k] = ld4_coherent(part, item + p * step + (ROWS * DP + e / (DP / 4)) * 4);
-            }
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                const int r = (e0 + k * kProThreads) / (DP / 4);   // rows that nobody has are added up and left
-                o[k] += v[k] * exp2_fast(m[k] - done[0][r]);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const int e = e0 + k * kProThreads, r = e / (DP / 4), i = e % (DP / 4) * 4;
-            if (r >= rows || i >= d) continue;
-            const Out q = out_of(r, done[1][r]);
-            emit(q, i, o[k]);
-            if (i == 0) emit_lse(q, done[0][r], done[1][r]);
-        }
-    }
-    if (tid == 0) st_flag(ctr, 0u);
 }
 
 template <int FMT, int KJ, bool FULL>
