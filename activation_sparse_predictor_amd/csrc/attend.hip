@@ -344,16 +344,17 @@ __global__ __launch_bounds__(WAVES * kWave, KJ == 4 ? 1 : 2) void k_attend(AttAr
 
 size_t kv_attend_zero_bytes() { return (size_t)kAttSlots * kAttCtrStride * 4; }
 
-// Whether sequences with many rows go to the prompt kernel, and how many are
-// many.  Where the 16-row items of all heads are at most what runs at once
-// (two workgroups a CU), this kernel's split over the context serves them
-// better (64 rows on 8192 tokens, 8 kv heads: 22 us against 51; 128 x 128 rows
-// of 56 heads on 1024: 22 against 31); beyond that every item reads its keys
-// again, and the prompt kernel is faster from 33 rows on (8 sequences of 56
-// heads on 2048 tokens, 33 rows each: 79 us against 99, 128 rows: 96 against 243).
-constexpr int kSingleRows = 32;
+// Whether sequences of more rows than one item holds go to the prompt kernel.
+// Where the 16-row items of all heads are few, this kernel's split over the
+// context serves them better (one sequence, 64 rows of each of 8 kv heads on
+// 30000 tokens, 32 items: 35 us against 80; 512 tokens of 12 heads of 64, 384
+// items: 9.5 against 16).  With more, every item reads its keys again, and the
+// prompt kernel is faster (1024 rows of 8 kv heads on 8192 tokens, 512 items: 61
+// us against 93; 8 sequences of 56 heads on 2000 tokens: 64 against 70 with 20
+// rows each, 85 against 232 with 128).
+constexpr int kSingleItems = 384;
 static bool uses_prompt(const KvBatch& b, int group, int n_kv) {
-    return (long long)b.max_q * group > kSingleRows && att_most_row_tiles(b, group, kAttRows) * n_kv > 512;
+    return (long long)b.max_q * group > kAttRows && att_most_row_tiles(b, group, kAttRows) * n_kv > kSingleItems;
 }
 
 size_t kv_attend_bytes(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d) {
@@ -407,9 +408,9 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, lo
     if (uses_prompt(b, group, c.n_kv)) {
         // rows of long and short sequences: each kernel takes its own (they
         // share the workspace, one after the other)
-        A.upto = kSingleRows;
+        A.upto = kAttRows;
         AttArgs P = A;
-        P.above = kSingleRows;
+        P.above = kAttRows;
         P.upto = 0x7FFFFFFF;
         const hipError_t e = launch_attend_prompt(P, s);
         if (e != hipSuccess || b.n_tok == (long long)b.n_seq * b.max_q) return e;   // no short ones
