@@ -22,6 +22,14 @@
 // operand of the output's products, all share one page, and the V operand is
 // 16 contiguous bytes (a dimension's 16 tokens).  So nothing is shuffled or
 // staged between the two products, and a lane has one ks and one vs a step.
+//
+// What bounds it: the cache's bytes, read once, at up to 6.1 TB/s (64 ragged
+// sequences of 72 heads, 1.48 GB: 242 us).  Below that a call's fixed chain
+// shows: lengths, table, scales, first codes (6 us) and the joins (3-4 us):
+// 161 MB in 38 us, 134 MB in 34, 129 MB in 39 with 32 rows a head; 7.5 us for
+// one sequence of 128 tokens.  The weights as a leading and a following fp16
+// half keep 22 bits where the products are free: the matrix cores are busy a
+// tenth of the time.
 #include <type_traits>
 
 #include "attend.hpp"

@@ -9,6 +9,11 @@
 // One group of 1 or 4 waves owns a (block, head, matrix) from its largest
 // value to its codes, so the new tokens' values are read once and stay in
 // registers while the scale is found, and nothing is shared between groups.
+// Measured: 16384 tokens of 8 heads of 128 written in 25 us (4.0 TB/s) and read
+// back in 20 (5.0 TB/s); 32 ragged sequences, 82 thousand tokens, read in 102-106
+// us (4.8-5.0 TB/s; a large copy reaches 4.9).  One token a sequence is latency:
+// the lengths, the table, the values and the scale, the codes, one after the
+// other: 4.6 us a launch for one sequence, 7 for 64.
 #include "kv.hpp"
 
 namespace pi {

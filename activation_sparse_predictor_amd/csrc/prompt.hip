@@ -13,6 +13,14 @@
 // (vector work) run beside the other's products.  The weights are rounded to
 // fp16 once (2^-11 a weight, as large as the rounding of the output itself):
 // the second half that attend.hip keeps would cost half as many products again.
+//
+// Measured: 2048 tokens of 56 heads of 128 (60 GFLOP) in 85-89 us, 680-700
+// TFLOP/s; 509 tokens of 64 heads beside seven short sequences (65 GFLOP) in
+// 97-105, of which the other kernel's 17.  A large matrix product reaches 1.4
+// PFLOP/s.  What is between: a tile's 64 products of a wave (1024 cycles) stand
+// beside 230 vector instructions (weights, codes to fp16; five cycles each, more
+// beside another wave's products) and 32 fragments from LDS.  LDS is a quarter
+// busy, without bank conflicts.
 #include "attend.hpp"
 
 namespace pi {
