@@ -3,7 +3,8 @@
 The computation lives in the HIP library libpi.so (C ABI in include/pi.h):
 predictor MLP -> ordered index compaction -> gathered up/gate GEMV ->
 neuron-major W_down accumulate, plus the offline profile and hot-first
-reorder.  `binding` exposes the C entry points under the same names and
+reorder.  Beside it, the attention half of a decoder layer: an 8-bit paged
+cache and attention over it (the pi_kv_* calls).  `binding` exposes the C entry points under the same names and
 `runtime` adds device-buffer plumbing (workspaces, layer bundles).
 """
 

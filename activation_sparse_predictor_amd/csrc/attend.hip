@@ -394,9 +394,10 @@ static hipError_t launch_singles(AttArgs A, hipStream_t s) {
     const bool full = A.c.d == 64 * kj;
     // Where all items run at once, one eight-wave workgroup a CU each: half as
     // many pieces to join (16 sequences of 4 x 8 rows, window 4097: 39 us
-    // against 61 with four waves; 131072 tokens: 36 against 44).  Where there
+    // against 44 with four waves; 131072 tokens: 34 against 35.5).  Where there
     // are more, two four-wave workgroups a CU, one's start and end beside the
-    // other's loads (64 sequences of 72 heads: 242 us against 290 with eight).
+    // other's loads (32 ragged sequences of 8 kv heads: 38 us against 48 with
+    // eight; 64 of 72 heads: 242 against 295).
     const int waves = kj < 4 && att_most_row_tiles(A.b, A.group, kAttRows) * A.c.n_kv <= 256 ? 8 : 4;
     A.target = single_target(kj, waves);
     A.min_tiles = kMinTiles;

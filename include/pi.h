@@ -533,9 +533,9 @@ typedef struct pi_kv_batch {   /* read by the host during the call; the arrays a
  *
  * Errors (all three calls): INVALID_ARG for NULL pointers, an unknown fmt,
  * counts out of range, n_head not a multiple of n_kv, a negative window, a
- * stride below a row; UNSUPPORTED for more than PI_KV_MAX_ROWS rows, a page size or d not listed, a stride
- * not a multiple of 8, or misalignment (fp16 tensors, k and v 16 bytes, the
- * others 4).
+ * stride below a row; UNSUPPORTED for more than PI_KV_MAX_ROWS rows, a page
+ * size or d not listed, a stride not a multiple of 8, or misalignment (fp16
+ * tensors, k and v 16 bytes, the others 4).
  */
 pi_status pi_kv_append(const pi_kv_cache* cache, const pi_kv_batch* batch,
                        const pi_half* k, int64_t k_stride, const pi_half* v, int64_t v_stride,
@@ -565,8 +565,9 @@ pi_status pi_kv_read(const pi_kv_cache* cache, const pi_kv_batch* batch,
  * cache: append them first.  A token with nothing to attend to (negative
  * position) gets y = 0, lse = -infinity.  y: n_tok x n_head x d fp16; lse:
  * n_tok x n_head floats, or NULL.  Codes become fp16 exactly, products are
- * fp16 x fp16 with fp32 sums, the softmax's statistics are fp32.  Slots outside
- * A may hold anything, NaN included.
+ * fp16 x fp16 with fp32 sums, the softmax's statistics are fp32, its weights
+ * enter the product with V as fp16 (with many rows once, otherwise as a leading
+ * and a following half).  Slots outside A may hold anything, NaN included.
  *
  * Work is split over the sequences' actual lengths, which the kernels read on
  * the device; the split, and with it the order of the sums, is a function of
