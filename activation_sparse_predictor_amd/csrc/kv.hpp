@@ -10,12 +10,9 @@ namespace pi {
 // A page's bytes come in granules of 16 tokens, 16 d bytes for K and for V.
 constexpr int kGran = 16;
 
-// Byte of (token t, dimension i) inside a page and head.
-__device__ __forceinline__ int k_byte(int t, int i, int d) {
-    return (t >> 2) * 4 * d + (i >> 4) * 64 + (t & 3) * 16 + (i & 15);
-}
-__device__ __forceinline__ int v_byte(int t, int i, int d) { return (t >> 4) * 16 * d + i * 16 + (t & 15); }
-
+// Inside a page and head, the byte of token t and dimension i is
+//   K: (t / 4) * 4 d + (i / 16) * 64 + (t % 4) * 16 + i % 16
+//   V: (t / 16) * 16 d + i * 16 + t % 16
 // First byte of a page and head; pages * heads * bytes pass 32 bits.
 __device__ __forceinline__ size_t page_base(const KvCache& c, int id, int h) {
     return ((size_t)id * c.n_kv + h) * (size_t)(c.page * c.d);
