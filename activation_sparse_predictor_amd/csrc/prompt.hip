@@ -10,17 +10,20 @@
 // one is used the next is written, and the one after is on its way in
 // registers, so one barrier a tile is all.  A fragment read from LDS serves the
 // wave's two 16-row operands.  Two workgroups share a CU, so that one's weights
-// (vector work) run beside the other's products.  The weights are rounded to
-// fp16 once (2^-11 a weight, as large as the rounding of the output itself):
-// the second half that attend.hip keeps would cost half as many products again.
+// (vector work) run beside the other's products.  As in attend.hip the weights
+// enter as a leading and a following fp16 half (21 bits), so that which kernel a
+// call's sizes choose does not show in a row's precision.  Rounded to fp16 once
+// they cost a third fewer products (93-97 us against 112-115 below), but an
+// error of 2^-11 a weight, as large as the rounding of the output itself.
 //
-// Measured: 2048 tokens of 56 heads of 128 (60 GFLOP) in 85-89 us, 680-700
+// Measured: 2048 tokens of 56 heads of 128 (60 GFLOP) in 112-115 us, 520-540
 // TFLOP/s; 509 tokens of 64 heads beside seven short sequences (65 GFLOP) in
-// 97-105, of which the other kernel's 17.  A large matrix product reaches 1.4
-// PFLOP/s.  What is between: a tile's 64 products of a wave (1024 cycles) stand
-// beside 230 vector instructions (weights, codes to fp16; five cycles each, more
-// beside another wave's products) and 32 fragments from LDS.  LDS is a quarter
-// busy, without bank conflicts.
+// 123, of which the other kernel's 17.  A large matrix product reaches 1.4
+// PFLOP/s, and the following halves are half as many products again.  What is
+// between: a tile's 96 products of a wave (1536 cycles) stand beside 250 vector
+// instructions (weights, codes to fp16; five cycles each, more beside another
+// wave's products) and 32 fragments from LDS.  LDS is a quarter busy, without
+// bank conflicts.
 #include "attend.hpp"
 
 namespace pi {
@@ -40,6 +43,9 @@ constexpr int kProRing = 2 * kProSeg;
 // The waves' LDS writes are done and all of them are here.  Unlike
 // __syncthreads this does not wait for the loads of the tile after next.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
+
+// Two numbers as fp16, rounded towards zero.
+__device__ __forceinline__ f16x2 cut2(float a, float b) { return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(a, b)); }
 
 template <int FMT, int KJ, bool FULL>
 __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) {
@@ -130,6 +136,7 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         to[(i * 2 * kProWaves + 1) * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(v.z, v.w));
     };
 
+    const float minus = settle(-1.f);   // (a constant would turn the differences below into a conversion and a subtraction each)
     float M[NT], l[NT];
     f32x4 O[NT][4 * KJ];
 #pragma unroll
@@ -201,7 +208,7 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
             __builtin_amdgcn_sched_barrier(0);
             const int key0 = tile0 + g * kGran;
             const bool edge = tile0 < v_free_from || tile0 + kTile - 1 > v_free_to;
-            f16x8 ph[NT][2];
+            f16x8 ph[NT][2], pl[NT][2];   // the weights' leading and following halves
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 if (edge) {
@@ -228,10 +235,15 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
                 const float c = none ? 0.f : lv - M[nt] + kLift, unscale = none ? 0.f : exp2_fast(-lv);
                 float sum = 0.f;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float wt = exp2_fast(fmaf(S[nt][k / 4][k % 4], by, c));
-                    sum += wt;
-                    ph[nt][k / 8][k % 8] = (f16)wt;
+                for (int k = 0; k < 16; k += 2) {
+                    const float a = exp2_fast(fmaf(S[nt][k / 4][k % 4], by, c));
+                    const float b = exp2_fast(fmaf(S[nt][k / 4][k % 4 + 1], by, c));
+                    sum += a;
+                    sum += b;
+                    // (towards zero, two a conversion: what the first leaves the second takes up)
+                    const f16x2 hi = cut2(a, b), more = cut2(fmaf((float)hi.x, minus, a), fmaf((float)hi.y, minus, b));
+                    ph[nt][k / 8][k % 8] = hi.x, ph[nt][k / 8][k % 8 + 1] = hi.y;
+                    pl[nt][k / 8][k % 8] = more.x, pl[nt][k / 8][k % 8 + 1] = more.y;
                 }
                 l[nt] = fmaf(sum, unscale, l[nt]);
             }
@@ -245,8 +257,11 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        O[nt][2 * k + i / 2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(va[k % 2][i], ph[nt][i % 2], O[nt][2 * k + i / 2], 0, 0, 0);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        f32x4& o = O[nt][2 * k + i / 2];
+                        o = __builtin_amdgcn_mfma_f32_16x16x32_f16(va[k % 2][i], ph[nt][i % 2], o, 0, 0, 0);
+                        o = __builtin_amdgcn_mfma_f32_16x16x32_f16(va[k % 2][i], pl[nt][i % 2], o, 0, 0, 0);
+                    }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }

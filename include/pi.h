@@ -566,8 +566,8 @@ pi_status pi_kv_read(const pi_kv_cache* cache, const pi_kv_batch* batch,
  * position) gets y = 0, lse = -infinity.  y: n_tok x n_head x d fp16; lse:
  * n_tok x n_head floats, or NULL.  Codes become fp16 exactly, products are
  * fp16 x fp16 with fp32 sums, the softmax's statistics are fp32, its weights
- * enter the product with V as fp16 (with many rows once, otherwise as a leading
- * and a following half).  Slots outside A may hold anything, NaN included.
+ * enter the product with V as a leading and a following fp16 half (21 bits).
+ * Slots outside A may hold anything, NaN included.
  *
  * Work is split over the sequences' actual lengths, which the kernels read on
  * the device; the split, and with it the order of the sums, is a function of
