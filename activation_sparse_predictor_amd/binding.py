@@ -41,6 +41,7 @@ PI_NOALLOC_SCRATCH_BYTES = 4 << 20   # the static scratch of pi_ffn_decode_noall
 PI_KV_INT8 = 0
 PI_KV_FP8 = 1
 PI_KV_MAX_SEQ = 1024
+PI_KV_WS_ZERO_BYTES = 8192 + 65536   # of a workspace of pi_kv_attend alone, what has to be zero-filled once
 
 KV_FMTS = {"int8": PI_KV_INT8, "fp8": PI_KV_FP8}
 KINDS = {"relu": PI_FFN_RELU, "reglu": PI_FFN_REGLU, "swiglu": PI_FFN_SWIGLU}

@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "attend.hpp"
+#include "pi.h"
 
 namespace pi {
 
@@ -351,6 +352,7 @@ __global__ __launch_bounds__(WAVES * kWave, KJ == 4 ? 1 : 2) void k_attend(AttAr
 }
 
 size_t kv_attend_zero_bytes() { return (size_t)kAttSlots * kAttCtrStride * 4; }
+static_assert(kSyncBytes + (size_t)kAttSlots * kAttCtrStride * 4 == PI_KV_WS_ZERO_BYTES, "header and counters");
 
 // Whether sequences of more rows than one item holds go to the prompt kernel.
 // Where the 16-row items of all heads are few, this kernel's split over the

@@ -343,7 +343,8 @@ def _kv_rows(t: torch.Tensor, n_tok: int, heads: Optional[int], d: int, name: st
     return t.stride(0) if n_tok > 1 else shape[1] * d
 
 
-# the current stream's handle, without making a torch.cuda.Stream of it
+# whether the current stream is being captured, and its handle, without making a torch.cuda.Stream of it
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
@@ -425,8 +426,10 @@ def kv_attend(cache: dict, q: torch.Tensor, batch: dict, y: Optional[torch.Tenso
               ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pi_kv_attend: attention of q (n_tok x n_head x d fp16, tokens any multiple
     of 8 elements apart) over the cache; scale defaults to 1 / sqrt(d), window 0
-    is none, lse (n_tok x n_head floats) is filled if given.  Without ws, each
-    stream has a workspace of its own."""
+    is none, lse (n_tok x n_head floats) is filled if given.  Without ws, the
+    eager calls of a stream share a workspace, and a call inside torch.cuda.graph
+    has its own, allocated from the graph's pool and cleared in the capture (2 us
+    a replay; a ws from kv_workspace, kept with the graph, saves them)."""
     dev = q.get_device()
     if _is_elsewhere(stream, dev):
         return _elsewhere(stream, q.device, (q, y, lse, ws, *cache.values(), *batch.values()),
@@ -448,6 +451,16 @@ def kv_attend(cache: dict, q: torch.Tensor, batch: dict, y: Optional[torch.Tenso
     if ws is not None:
         _need(ws.get_device() == dev and ws.is_contiguous(), "ws must be contiguous and on q's device")
         size = ws.numel() * ws.element_size()
+        B.check(B.pi_kv_attend(c, b, q, qs, heads, scale, int(window), y, lse, ws, size, st), "pi_kv_attend")
+        return y
+    if _capturing():
+        # A graph's workspace is its alone: what other captures or eager calls on
+        # this stream do is not replayed with it, and a kept buffer may be
+        # replaced by a larger one.  The capture's pool holds the memory as long
+        # as the graph lives and gives it to later allocations of the capture.
+        size = B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, d)
+        ws = torch.empty(size, dtype=_U8, device=q.device)
+        ws[:B.PI_KV_WS_ZERO_BYTES].zero_()
         B.check(B.pi_kv_attend(c, b, q, qs, heads, scale, int(window), y, lse, ws, size, st), "pi_kv_attend")
         return y
     own = _KV_WS.get((dev, st))

@@ -490,6 +490,8 @@ typedef enum pi_kv_fmt {
 #define PI_KV_MAX_PAGE 256
 #define PI_KV_MAX_TOKENS (1 << 20)
 #define PI_KV_MAX_ROWS (1 << 24)    /* pi_kv_attend: n_tok * n_head / n_kv */
+#define PI_KV_WS_ZERO_BYTES (8192 + 65536)   /* of a workspace used for pi_kv_attend alone, the
+                                                leading bytes that have to be zero-filled once */
 
 typedef struct pi_kv_cache {   /* read by the host during the call; k .. v_scale are device pointers */
     int fmt;                   /* pi_kv_fmt */

@@ -132,3 +132,58 @@ def test_rows_above_the_limit_refused():
     with pytest.raises(B.PiError) as e:
         B.pi_kv_workspace_size(2, 1 << 20, 1 << 20, 64, 1, 64)
     assert e.value.status == UNSUP
+
+
+LEAD = 8192 + 65536   # a workspace's header and attention's counters: what has to be zero
+
+
+@pytest.fixture
+def pretend(monkeypatch):
+    """kv_attend over a stand-in for the library's call, on host tensors: what
+    it is given, and the workspace's leading words, are noted."""
+    seen, state = [], {"capturing": False}
+
+    def attend(c, b, q, qs, heads, scale, window, y, lse, ws, size, st):
+        need = B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, c.d)
+        if ws is None or size < need:
+            return WS
+        seen.append({"ws": ws, "at": ws.data_ptr(), "clean": not torch.any(ws[:LEAD]), "window": window})
+        ws[:LEAD].fill_(1)
+        return B.PI_OK
+
+    monkeypatch.setattr(B, "pi_kv_attend", attend)
+    monkeypatch.setattr(R, "_is_elsewhere", lambda stream, dev: False)
+    monkeypatch.setattr(R, "_raw_stream", lambda dev: 7)
+    monkeypatch.setattr(R, "_capturing", lambda: state["capturing"], raising=False)
+    monkeypatch.setattr(R, "_KV_WS", {})
+    c = R.kv_cache(40, 2, 64, device="cpu")
+
+    def call(new=1, capturing=False, **kw):
+        state["capturing"] = capturing
+        b = R.kv_batch([new], [new], [list(range(40))], device="cpu")
+        R.kv_attend(c, torch.zeros(new, 128, 64, dtype=torch.float16), b, **kw)
+        return seen.pop()
+    return call
+
+
+def test_each_captured_call_has_a_workspace_of_its_own(pretend):
+    """Without ws: eager calls of a stream share one that grows; a captured call
+    gets its own, zeroed inside the capture, that no other call meets and that
+    no growth gives away."""
+    graphs = [pretend(capturing=True) for _ in range(2)]   # before any eager call
+    assert R._KV_WS == {} or all(w.buf is None for w in R._KV_WS.values())
+    small = pretend()
+    assert pretend()["at"] == small["at"]
+    graphs.append(pretend(capturing=True))
+    large = pretend(new=500)
+    assert large["at"] != small["at"] and pretend()["at"] == large["at"]
+    graphs.append(pretend(capturing=True))
+    at = [g["at"] for g in graphs]
+    assert len(set(at)) == len(at) and small["at"] not in at and large["at"] not in at
+    assert all(g["clean"] for g in graphs) and small["clean"] and large["clean"]
+
+
+def test_a_workspace_that_is_passed_is_used_also_under_capture(pretend):
+    ws = R.kv_workspace(1, 1, 1, 128, 2, 64, device="cpu")
+    for capturing in (False, True):
+        assert pretend(capturing=capturing, ws=ws)["at"] == ws.data_ptr()
