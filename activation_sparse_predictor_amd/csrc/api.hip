@@ -817,12 +817,21 @@ pi_status pi_kv_attend(const pi_kv_cache* cache, const pi_kv_batch* batch, const
     // one key for every shape: the counters have one place, and each call leaves them zero
     const LayoutKey key{kOpKvAttend, 0, 0, 0, 0};
     hipError_t e = hipSuccess;
-    if (ws_needs_clear(ws, key)) e = pi::launch_zero(data, pi::kv_attend_zero_bytes(), s);
+    bool captured = false;   // a clear that runs when its graph is replayed, and not now
+    if (ws_needs_clear(ws, key)) {
+        hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+        e = hipStreamIsCapturing(s, &st);
+        captured = st != hipStreamCaptureStatusNone;
+        if (e == hipSuccess) e = pi::launch_zero(data, pi::kv_attend_zero_bytes(), s);
+    }
     if (e == hipSuccess)
         e = pi::launch_kv_attend(c, b, reinterpret_cast<const pi::h16*>(q), q_stride, n_head, scale, window,
                                  reinterpret_cast<pi::h16*>(y), lse, data, s);
     if (e != hipSuccess) return hip_fail(e, "pi_kv_attend");
-    ws_record(ws, key);
+    // The next call, in another graph or in none, cannot rely on a captured
+    // clear, nor on what the workspace held before the graph's replays.
+    if (captured) ws_forget(ws);
+    else ws_record(ws, key);
     return ok();
 }
 

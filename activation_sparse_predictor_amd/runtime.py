@@ -428,7 +428,7 @@ def kv_attend(cache: dict, q: torch.Tensor, batch: dict, y: Optional[torch.Tenso
     of 8 elements apart) over the cache; scale defaults to 1 / sqrt(d), window 0
     is none, lse (n_tok x n_head floats) is filled if given.  Without ws, the
     eager calls of a stream share a workspace, and a call inside torch.cuda.graph
-    has its own, allocated from the graph's pool and cleared in the capture (2 us
+    has its own, allocated from the graph's pool and cleared in the capture (4 us
     a replay; a ws from kv_workspace, kept with the graph, saves them)."""
     dev = q.get_device()
     if _is_elsewhere(stream, dev):

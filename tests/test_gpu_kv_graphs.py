@@ -92,3 +92,43 @@ def test_capture_on_a_warm_stream_outlives_the_eager_workspace():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, R.kv_attend(cache, q, batch)) and all(bool((t == -1).all()) for t in junk)
+
+
+def test_graphs_that_share_a_workspace_clear_it_each():
+    """A workspace that an FFN call used last, passed to two captures: the second
+    is replayed alone, then both in turn, then eager calls of either kind."""
+    from activation_sparse_predictor_amd import binding as B
+    from synthetic import custom_config, make_layer, make_tokens
+    cfg = custom_config("relu", 256, 1000, 64, mean=0.2, number=120)
+    layer = R.to_device(make_layer(cfg), DEV)
+    x = make_tokens(cfg, 1).to(DEV)
+    fy, idx, cnt = R.decode(layer, x)
+    data = [case(*CASES[i], seed=80 + i) for i in (1, 0, 3)]
+    need = max([B.pi_workspace_size(B.PI_OP_DECODE, 1, cfg.d, cfg.r, cfg.ffn)]
+               + [B.pi_kv_workspace_size(len(b["ctx"]), q.shape[0], b["max_q"], q.shape[1], c["k"].shape[1], q.shape[2]) for c, b, q in data])
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+
+    def ffn():
+        y = torch.empty_like(fy)
+        B.check(B.pi_ffn_decode(B.PI_FFN_RELU, x, 1, cfg.d, cfg.ffn, layer["P1"], None, B.PI_ACT_RELU, layer["P2"], layer["b2"],
+                                cfg.r, 0.5, layer["W_up"], layer["b_up"], None, None, layer["W_down"], torch.empty_like(idx),
+                                torch.empty_like(cnt), y, 0, ws, ws.numel()), "pi_ffn_decode")
+        torch.cuda.synchronize()
+        return y
+
+    def same(i):
+        graphs[i][1].fill_(float("nan"))
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        return torch.equal(graphs[i][1], want[i])
+
+    want = [R.kv_attend(c, q, b) for c, b, q in data]
+    assert torch.equal(ffn(), fy)
+    graphs = [capture(*d, ws=ws) for d in data]
+    for i in (2, 1, 2, 0, 1, 0):
+        assert same(i), i
+    assert torch.equal(ffn(), fy)
+    for i, (c, b, q) in enumerate(data):
+        assert torch.equal(R.kv_attend(c, q, b, ws=ws), want[i])
+    assert all(same(i) for i in (1, 0, 2)) and torch.equal(ffn(), fy)
+    assert torch.equal(R.kv_attend(data[0][0], data[0][2], data[0][1], ws=ws), want[0])
