@@ -39,6 +39,9 @@ constexpr int pro_target(int kj) { return kj == 4 ? 256 : 512; }   // workgroups
 constexpr int kProMinTiles = 8;     // fewest tiles worth a workgroup of their own
 constexpr int kProSeg = 64;         // tiles whose granules are looked up at a time
 constexpr int kProRing = 2 * kProSeg;
+// Polls before the join gives up on the other pieces, which are done and only
+// have their results to write (some microseconds; this is tens of milliseconds).
+constexpr int kProWaitLimit = 1 << 16;
 
 // The waves' LDS writes are done and all of them are here.  Unlike
 // __syncthreads this does not wait for the loads of the tile after next.
@@ -55,7 +58,7 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     constexpr int kFrags = 16 * KJ;   // of a tile: 8 KJ of K, 8 KJ of V
     extern __shared__ u32x4 frags[];  // [2][kFrags][64]
     __shared__ Gran grans[kProRing * (kTile / kGran)];
-    __shared__ int s_last;
+    __shared__ int s_last, s_written;
     // (settled, so that what follows from them is not kept in registers from
     // unit to unit)
     const int lane = settle(lane_id()), wave = __builtin_amdgcn_readfirstlane(settle((int)threadIdx.x) / kWave);
@@ -295,16 +298,23 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
             if (tid == 0) fetch_add(ctr + 1, 1u);
             return;
         }
-        // The others are done and running: nothing that they wait for is held here.
+        // The others are done and running: nothing that they wait for is held
+        // here.  Should they not arrive all the same (counters that something
+        // else wrote), the rows become NaN and cannot pass as a result.
         if (tid == 0) {
-            while (ld_flag(ctr + 1) < (uint32_t)(w.splits - 1)) __builtin_amdgcn_s_sleep(1);
+            int polls = 0;
+            while ((int)ld_flag(ctr + 1) != w.splits - 1 && polls < kProWaitLimit) {
+                __builtin_amdgcn_s_sleep(1);
+                ++polls;
+            }
+            s_written = polls < kProWaitLimit;
             st_flag(ctr, 0u);
             st_flag(ctr + 1, 0u);
         }
         __syncthreads();
         float m[NT], sum[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) m[nt] = M[nt], sum[nt] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) m[nt] = M[nt], sum[nt] = s_written ? 0.f : __builtin_nanf("");
         for (int p = 0; p < w.splits; ++p) {
             if (p == w.split) continue;
 #pragma unroll

@@ -573,7 +573,8 @@ pi_status pi_kv_read(const pi_kv_cache* cache, const pi_kv_batch* batch,
  *
  * Work is split over the sequences' actual lengths, which the kernels read on
  * the device; the split, and with it the order of the sums, is a function of
- * those lengths and the sizes alone.  ws: pi_kv_workspace_size() bytes, under
+ * those lengths and the sizes alone.  Every internal wait is bounded: on overrun
+ * the rows concerned become NaN.  ws: pi_kv_workspace_size() bytes, under
  * the workspace rules above; graphs that share one may be replayed in any order,
  * one at a time.
  */

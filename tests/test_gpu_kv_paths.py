@@ -26,7 +26,7 @@ import torch
 
 from activation_sparse_predictor_amd import runtime as R
 from oracle import kv as O
-from tests.test_gpu_kv import DEV, host, host_batch, tables
+from tests.test_gpu_kv import DEV, filled, host, host_batch, queries, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,29 @@ def test_weights_are_not_rounded_once(fmt, window, heads, n_kv, d, new):
     tol = 2.0 ** -11 * np.abs(want) + 2.0 ** -16 * a + 2.0 ** -25
     worst = np.max(np.abs(y.cpu().numpy().astype(np.float64) - want) / tol)
     assert worst <= 1.0, f"{worst:.2f} times the bound"
+
+
+@pytest.mark.parametrize("heads,n_kv,d,new,split", [(8, 8, 64, 1100, True), (10, 5, 128, 2100, True), (4, 4, 256, 1600, True),
+                                                   (9, 9, 256, 1100, False)])
+def test_a_join_that_waits_in_vain_ends_in_nan(heads, n_kv, d, new, split):
+    """The prompt kernel's join waits for a count of pieces.  Set to one too few
+    from outside (which the workspace rules forbid), the bounded wait runs out:
+    the joined rows are NaN, the others (all, where the items fill the GPU by
+    themselves and none is split) as before, and the next call is right again."""
+    ctx = [4300]
+    assert to_prompt([new], heads, n_kv)
+    cache, rows = filled(ctx, n_kv, d, 64, "int8", seed=41)
+    q, batch = queries(new, heads, d), R.kv_batch([new], ctx, rows, DEV)
+    ws = R.kv_workspace(1, new, new, heads, n_kv, d, DEV)
+    lse = torch.empty(new, heads, device=DEV)
+    want = R.kv_attend(cache, q, batch, ws=ws)
+    torch.cuda.synchronize()
+    counters = ws[8192:8192 + 65536].view(torch.int32).view(1024, 16)
+    assert not torch.any(counters)
+    counters[:, 1] = -1
+    y = R.kv_attend(cache, q, batch, ws=ws, lse=lse)
+    torch.cuda.synchronize()
+    lost = torch.isnan(y).any(2)
+    assert bool(torch.any(lost)) == split and torch.equal(torch.isnan(y).all(2), lost) and torch.equal(torch.isnan(lse), lost)
+    assert torch.equal(y[~lost], want[~lost])
+    assert torch.equal(R.kv_attend(cache, q, batch, ws=ws), want)
