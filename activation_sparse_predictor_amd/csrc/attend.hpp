@@ -72,6 +72,14 @@ __device__ __forceinline__ int att_row_tiles(const AttArgs& A, const Seq& q, int
     return to < 0 ? 1 : to / kTile - first_tile + 1;
 }
 
+// Tiles of a piece, before items that run at once are fitted: `want`, but at
+// least min_tiles, and never above the 2^24 tiles of the longest context (2^30
+// tokens), so that the fitting and the divisions stay far below 2^31 (row ranges
+// that overlap, or a table that names pages again and again, can ask for more).
+__host__ __device__ constexpr int att_piece(float want, int min_tiles) {
+    return want < (float)min_tiles ? min_tiles : want < 16777216.f ? (int)want + 1 : 16777216;
+}
+
 // Splits the whole batch's tiles over about A.target workgroups: C tiles a
 // workgroup, the same for every sequence, from the lengths as they are on the
 // device.  Each item (sequence, row tile) becomes ceil(tiles / C) pieces, for
@@ -103,7 +111,7 @@ __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) 
     }
     const float room = (float)A.target / (float)A.c.n_kv;   // workgroups a head has
     const float want = all / room * 1.001f;                 // a little above: the slots rest on it
-    int C = want < A.min_tiles ? A.min_tiles : (int)want + 1;
+    int C = att_piece(want, A.min_tiles);
     if (b.n_seq <= kWave && items <= room) {
         // All items can run at once: the smallest C (to a sixteenth) whose rounded-up pieces still do.
         for (int i = 0; i < 24; ++i) {
