@@ -448,10 +448,11 @@ def kv_attend(cache: dict, q: torch.Tensor, batch: dict, y: Optional[torch.Tenso
               and lse.get_device() == dev, "lse must be n_tok x n_head floats")
     st = _raw_stream(dev)
     scale = d ** -0.5 if scale is None else float(scale)
+    window = min(max(int(window), -1), 2 ** 31 - 1)   # (ctypes would drop what lies above 32 bits)
     if ws is not None:
         _need(ws.get_device() == dev and ws.is_contiguous(), "ws must be contiguous and on q's device")
         size = ws.numel() * ws.element_size()
-        B.check(B.pi_kv_attend(c, b, q, qs, heads, scale, int(window), y, lse, ws, size, st), "pi_kv_attend")
+        B.check(B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, ws, size, st), "pi_kv_attend")
         return y
     if _capturing():
         # A graph's workspace is its alone: what other captures or eager calls on
@@ -461,16 +462,16 @@ def kv_attend(cache: dict, q: torch.Tensor, batch: dict, y: Optional[torch.Tenso
         size = B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, d)
         ws = torch.empty(size, dtype=_U8, device=q.device)
         ws[:B.PI_KV_WS_ZERO_BYTES].zero_()
-        B.check(B.pi_kv_attend(c, b, q, qs, heads, scale, int(window), y, lse, ws, size, st), "pi_kv_attend")
+        B.check(B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, ws, size, st), "pi_kv_attend")
         return y
     own = _KV_WS.get((dev, st))
     if own is None:
         own = _KV_WS[(dev, st)] = Workspace(q.device)
     size = 0 if own.buf is None else own.buf.numel()
-    status = B.pi_kv_attend(c, b, q, qs, heads, scale, int(window), y, lse, own.buf, size, st)
+    status = B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, own.buf, size, st)
     if status == B.PI_ERR_WORKSPACE:   # too small for these sizes: nothing was launched
         buf, size = own.get(B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, d))
-        status = B.pi_kv_attend(c, b, q, qs, heads, scale, int(window), y, lse, buf, size, st)
+        status = B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, buf, size, st)
     B.check(status, "pi_kv_attend")
     return y
 

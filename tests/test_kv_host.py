@@ -187,3 +187,12 @@ def test_a_workspace_that_is_passed_is_used_also_under_capture(pretend):
     ws = R.kv_workspace(1, 1, 1, 128, 2, 64, device="cpu")
     for capturing in (False, True):
         assert pretend(capturing=capturing, ws=ws)["at"] == ws.data_ptr()
+
+
+def test_windows_outside_the_c_type(pretend):
+    """A window beyond 32 bits is as wide as the type; a negative one stays negative (and is refused)."""
+    for window, want in ((0, 0), (5, 5), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1), (1 << 62, 2 ** 31 - 1),
+                         (-1, -1), (-(2 ** 32) + 5, -1)):
+        for capturing in (False, True):
+            assert pretend(window=window, capturing=capturing)["window"] == want
+        assert pretend(window=window, ws=R.kv_workspace(1, 1, 1, 128, 2, 64, device="cpu"))["window"] == want
