@@ -41,7 +41,7 @@ class Layer:
         self.w_qkv = rows((heads + 2 * n_kv) * self.d, cfg.d)
         self.w_o = rows(cfg.d, cfg.d)
         self.ffn = make_layer(cfg, device=device)
-        self.pages = -(-max_tokens // page)
+        self.page, self.pages = page, -(-max_tokens // page)
         self.cache = R.kv_cache(seqs * self.pages, n_kv, self.d, page, fmt, device)
         # a sequence's pages: here simply its share of the pool
         self.table = [list(range(s * self.pages, (s + 1) * self.pages)) for s in range(seqs)]
@@ -49,7 +49,10 @@ class Layer:
 
     def batch(self, new) -> dict:
         """The next new[s] tokens of each sequence."""
-        self.lengths = [x + n for x, n in zip(self.lengths, new)]
+        lengths = [x + n for x, n in zip(self.lengths, new)]
+        if max(lengths) > self.pages * self.page:   # the library would clamp the length and write over the newest tokens
+            raise ValueError(f"a sequence of {max(lengths)} tokens; its pages hold {self.pages * self.page}")
+        self.lengths = lengths
         return R.kv_batch(new, self.lengths, self.table, self.w_o.device)
 
     def attention(self, x: torch.Tensor, batch: dict) -> torch.Tensor:
