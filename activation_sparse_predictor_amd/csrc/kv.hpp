@@ -33,7 +33,6 @@ template <> struct Codes<0> {
         a = as_h2(__builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) - off;
         b = as_h2(__builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) - off;
     }
-    static __device__ __forceinline__ float value(uint32_t byte) { return (float)((int)(byte & 0xFFu) - 128); }
     // round(clamp(x, -127, 127)) of two numbers as two bytes (rintf: ties to even)
     static __device__ __forceinline__ uint32_t encode2(float x, float y) {
         const int a = (int)rintf(fminf(fmaxf(x, -kMax), kMax)) + 128;
@@ -49,9 +48,6 @@ template <> struct Codes<1> {
     static __device__ __forceinline__ void to_f16(uint32_t w, f16x2& a, f16x2& b) {
         a = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
         b = __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
-    }
-    static __device__ __forceinline__ float value(uint32_t byte) {
-        return (float)__builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(byte & 0xFFu, 1.0f, false)).x;
     }
     static __device__ __forceinline__ uint32_t encode2(float x, float y) {
         return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(fminf(fmaxf(x, -kMax), kMax), fminf(fmaxf(y, -kMax), kMax), 0,
