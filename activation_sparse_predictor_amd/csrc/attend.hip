@@ -6,7 +6,7 @@
 // K_j = ks code and V_j = vs code, one ks and vs a page and head.  Codes are
 // exact in fp16, so q . code runs on the matrix cores without rounding the
 // cache a second time; ks multiplies the fp32 score and vs the weight.  A vs
-// lies anywhere between 2^-31 and 2^9, so the running reference M follows the
+// lies anywhere between 2^-33 and 2^9.1, so the running reference M follows the
 // largest weight with its scale, max (x + log2 vs):
 //   w_j = 2^(x_j + log2 vs_j - M + 15.7),  l = sum w_j / vs_j,  y = sum w_j code_j / l.
 // M moves when a maximum is more than 0.25 above it, so w is at most 2^15.95,
@@ -39,7 +39,7 @@ namespace pi {
 
 constexpr float kLift = 15.7f, kSlack = 0.25f;   // of the references, above
 constexpr int kAttRows = 16;   // query rows of a workgroup
-constexpr int kMinTiles = 4;   // fewest tiles worth a workgroup of their own
+constexpr int kMinTiles = 4;   // tiles a piece of a whole context has at least
 // workgroups the work is split into: those that run at once, by the registers
 constexpr int single_target(int kj, int waves) { return kj == 4 || waves == 8 ? 256 : 512; }
 
@@ -269,8 +269,8 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     if (threadIdx.x == 0) s_last = fetch_add(ctr, 1u) == (uint32_t)(w.splits - 1);
     __syncthreads();
     if (!s_last) return;
-    // Each row's reference and sum over the pieces: sixteen lanes a row, a
-    // piece each.  The first outputs are already on their way meanwhile.
+    // Each row's reference and sum over the pieces: kAttThreads / ROWS lanes a
+    // row, a piece each.  The first outputs are already on their way meanwhile.
     auto join = [&](auto batch) __attribute__((always_inline)) {
         constexpr int kBatch = decltype(batch)::value;   // pieces loaded at a time
         constexpr int kRowLanes = kAttThreads / ROWS;
@@ -357,11 +357,16 @@ static_assert(kSyncBytes + (size_t)kAttSlots * kAttCtrStride * 4 == PI_KV_WS_ZER
 // Whether sequences of more rows than one item holds go to the prompt kernel.
 // Where the 16-row items of all heads are few, this kernel's split over the
 // context serves them better (one sequence, 64 rows of each of 8 kv heads on
-// 30000 tokens, 32 items: 35 us against 80; 512 tokens of 12 heads of 64, 384
-// items: 9.5 against 16).  With more, every item reads its keys again, and the
-// prompt kernel is faster (1024 rows of 8 kv heads on 8192 tokens, 512 items: 61
-// us against 93; 8 sequences of 56 heads on 2000 tokens: 64 against 70 with 20
-// rows each, 85 against 232 with 128).
+// 30000 tokens, 32 items: 35 us against 83; 4 sequences of 160 rows of 8 kv heads
+// on 2000 tokens, 320 items: 25 against 29; 512 tokens of 12 heads of 64, 384
+// items: 9.6 against 17).  With more, every item reads its keys again, and the
+// prompt kernel is faster (77 sequences of 71 rows of one kv head up to 8000
+// tokens, 385 items: 43 us against 60; 1024 rows of 8 kv heads on 8192 tokens, 512
+// items: 68 against 87; 8 sequences of 128 rows of 56 heads on 2000 tokens, 3584
+// items: 84 against 165).  The count does not see how few keys an item may have:
+// there it chooses wrongly (256 rows of 32 heads on as many tokens, 512 items:
+// 15.7 us against this kernel's 10.9; 8 sequences of 20 rows of 56 heads on 2000,
+// 896 items: 61 against 54).
 constexpr int kSingleItems = 384;
 static bool uses_prompt(const KvBatch& b, int group, int n_kv) {
     return (long long)b.max_q * group > kAttRows && att_most_row_tiles(b, group, kAttRows) * n_kv > kSingleItems;
@@ -395,11 +400,14 @@ static hipError_t launch_singles(AttArgs A, hipStream_t s) {
     const int kj = att_kj(A.c.d);
     const bool full = A.c.d == 64 * kj;
     // Where all items run at once, one eight-wave workgroup a CU each: half as
-    // many pieces to join (16 sequences of 4 x 8 rows, window 4097: 39 us
-    // against 44 with four waves; 131072 tokens: 34 against 35.5).  Where there
-    // are more, two four-wave workgroups a CU, one's start and end beside the
-    // other's loads (32 ragged sequences of 8 kv heads: 38 us against 48 with
-    // eight; 64 of 72 heads: 242 against 295).
+    // many pieces to join (16 sequences of 4 x 8 rows, window 4097: 39.7 us
+    // against 43.6 with four waves; 131072 tokens: 33 against 35; 8 sequences of
+    // 8 kv heads: 17.5 against 18.7; 32 of 4096 tokens each: 51 against 53).
+    // Where there are more, two four-wave workgroups a CU, one's start and end
+    // beside the other's loads (33 ragged sequences of 8 kv heads: 38 us against
+    // 48 with eight; 64: 68 against 71; 64 of 72 heads: 242 against 295).  With
+    // 16 to 32 ragged sequences of 8 kv heads eight waves lose 2 us (32: 39.6
+    // against 37.5): the pieces are then as long as the longest sequence.
     const int waves = kj < 4 && att_most_row_tiles(A.b, A.group, kAttRows) * A.c.n_kv <= 256 ? 8 : 4;
     A.target = single_target(kj, waves);
     A.min_tiles = kMinTiles;

@@ -36,7 +36,7 @@ struct AttArgs {
     long long q_stride;
     int n_head, group, window;
     int above, upto;         // this kernel's sequences: those with more rows than `above`, at most `upto`
-    int target, min_tiles;   // workgroups the work is split into, and the fewest tiles worth one
+    int target, min_tiles;   // workgroups the work is split into, and the least tiles of att_plan's C
     float scale2;            // scale * log2(e)
     h16* y;
     float* lse;
@@ -83,8 +83,10 @@ __host__ __device__ constexpr int att_piece(float want, int min_tiles) {
 // Splits the whole batch's tiles over about A.target workgroups: C tiles a
 // workgroup, the same for every sequence, from the lengths as they are on the
 // device.  Each item (sequence, row tile) becomes ceil(tiles / C) pieces, for
-// each head, that share its own tiles evenly; the last rows, which attend to
-// most, come first.  Every wave computes it for itself: a
+// each head, that share its own tiles evenly (`tiles` is the whole sequence's:
+// the early rows of a prompt, and rows under a short window, have fewer, and
+// their pieces may have one tile or none); the last rows, which attend to most,
+// come first.  Every wave computes it for itself: a
 // round of 64 sequences is one round of loads.  Fills in unit `item`, if there
 // is one, and returns how many there are (of each head).  With at most 2^24
 // rows and 2^10 sequences, whatever the lengths say, the sums stay below 2^31.

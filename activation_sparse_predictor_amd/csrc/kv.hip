@@ -18,6 +18,11 @@
 
 namespace pi {
 
+// The scale and the quotient are rounded to nearest in fp32, as the definition
+// has them.  A quotient that is a tie in exact arithmetic (fp16 values and
+// largest values share few bits, so there are some: 3 in 10^5 codes) falls to
+// the side that those two roundings leave it on, which another way of dividing
+// by QMAX, or 64 bits, need not share.
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 // Largest |x| of two fp16 pairs as bits: the order of the magnitudes' bits is
@@ -29,7 +34,7 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t x) {
 
 // x / s rounded to nearest, given inv = 1 / s rounded to nearest: one product
 // and one residual step (Markstein's division).  With |x| in fp16's range and
-// s = max|x| / QMAX at least 2^-32 nothing here is subnormal.
+// s = max|x| / QMAX at least 2^-24 / 448 > 2^-33 nothing here is subnormal.
 __device__ __forceinline__ float quotient(float x, float s, float inv) {
     const float q = x * inv;
     return fmaf(fmaf(-q, s, x), inv, q);

@@ -13,17 +13,17 @@
 // (vector work) run beside the other's products.  As in attend.hip the weights
 // enter as a leading and a following fp16 half (21 bits), so that which kernel a
 // call's sizes choose does not show in a row's precision.  Rounded to fp16 once
-// they cost a third fewer products (93-97 us against 112-115 below), but an
+// they cost a third fewer products (79-94 us against 97-113 below), but an
 // error of 2^-11 a weight, as large as the rounding of the output itself.
 //
-// Measured: 2048 tokens of 56 heads of 128 (60 GFLOP) in 112-115 us, 520-540
-// TFLOP/s; 509 tokens of 64 heads beside seven short sequences (65 GFLOP) in
-// 123, of which the other kernel's 17.  A large matrix product reaches 1.4
-// PFLOP/s, and the following halves are half as many products again.  What is
-// between: a tile's 96 products of a wave (1536 cycles) stand beside 250 vector
-// instructions (weights, codes to fp16; five cycles each, more beside another
-// wave's products) and 32 fragments from LDS.  LDS is a quarter busy, without
-// bank conflicts.
+// Measured: 2048 tokens of 56 heads of 128 (60 GFLOP) in 97-113 us, 530-620
+// TFLOP/s, by the card; 509 tokens of 64 heads beside seven short sequences (65
+// GFLOP) in 111-124, of which the other kernel's 16.  A large matrix product
+// reaches 1.4 PFLOP/s, and the following halves are half as many products again.
+// What is between: a tile's 96 products of a wave (1536 cycles, 36 % of the
+// kernel's) stand beside 250 vector instructions (weights, codes to fp16; five
+// cycles each, more beside another wave's products) and 32 fragments from LDS.
+// LDS is a fifth busy, without bank conflicts.
 #include "attend.hpp"
 
 namespace pi {
@@ -36,7 +36,7 @@ constexpr float kLift = 13.f, kSlack = 2.9f;
 constexpr int kProWaves = 4;
 constexpr int kProThreads = kProWaves * kWave;
 constexpr int pro_target(int kj) { return kj == 4 ? 256 : 512; }   // workgroups that run at once, by LDS
-constexpr int kProMinTiles = 8;     // fewest tiles worth a workgroup of their own
+constexpr int kProMinTiles = 8;     // tiles a piece of a whole context has at least
 constexpr int kProSeg = 64;         // tiles whose granules are looked up at a time
 constexpr int kProRing = 2 * kProSeg;
 // Polls before the join gives up on the other pieces, which are done and only
