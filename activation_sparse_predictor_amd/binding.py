@@ -43,6 +43,16 @@ PI_KV_FP8 = 1
 PI_KV_MAX_SEQ = 1024
 PI_KV_WS_ZERO_BYTES = 8192 + 65536   # of a workspace of pi_kv_attend alone, what has to be zero-filled once
 
+PI_ROPE_HALF = 0
+PI_ROPE_PAIRS = 1
+PI_ROPE_PLAIN = 0
+PI_ROPE_LINEAR = 1
+PI_ROPE_NTK = 2
+PI_ROPE_YARN = 3
+PI_VERIFY_MAX_VOCAB = 1 << 24
+
+ROPE_LAYOUTS = {"half": PI_ROPE_HALF, "pairs": PI_ROPE_PAIRS}
+ROPE_SCALINGS = {"none": PI_ROPE_PLAIN, "linear": PI_ROPE_LINEAR, "ntk": PI_ROPE_NTK, "yarn": PI_ROPE_YARN}
 KV_FMTS = {"int8": PI_KV_INT8, "fp8": PI_KV_FP8}
 KINDS = {"relu": PI_FFN_RELU, "reglu": PI_FFN_REGLU, "swiglu": PI_FFN_SWIGLU}
 ACTS = {"relu": PI_ACT_RELU, "none": PI_ACT_NONE}
@@ -64,6 +74,13 @@ class KvBatch(ctypes.Structure):
                 ("q_start", _P), ("ctx", _P), ("table", _P)]
 
 
+class Rope(ctypes.Structure):
+    """pi_rope: turns is a device address."""
+    _fields_ = [("layout", _I), ("rot", _I), ("gain", ctypes.c_float), ("turns", _P)]
+
+
+_D, _LL = ctypes.c_double, ctypes.c_int64
+_RP = ctypes.POINTER(Rope)
 _KC = ctypes.POINTER(KvCache)
 _KB = ctypes.POINTER(KvBatch)
 
@@ -90,6 +107,12 @@ _SIGNATURES = {
     "pi_kv_read": (_I, [_KC, _KB, _P, _P, _P]),
     "pi_kv_attend": (_I, [_KC, _KB, _P, ctypes.c_int64, _I, ctypes.c_float, _I, _P, _P, _P, _SZ, _P]),
     "pi_kv_workspace_size": (_I, [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "pi_rope_frequencies": (_I, [_I, _D, _I, _D, _D, _D, _D, _P, ctypes.POINTER(ctypes.c_float)]),
+    "pi_rope_turns": (_I, [_P, _I, _P]),
+    "pi_rotate": (_I, [_RP, _P, _I, _I, _I, _P, _LL, _P, _LL, _P]),
+    "pi_kv_append_rope": (_I, [_KC, _KB, _RP, _P, _I, _P, _LL, _P, _LL, _P, _LL, _I, _P, _LL, _P]),
+    "pi_verify": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _LL, _P, _LL, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "pi_verify_workspace_size": (_I, [_I, _I, _I, ctypes.POINTER(_SZ)]),
     "pi_profile": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
     "pi_reorder": (_I, [_P, _I, ctypes.c_double, _P, _P]),
     "pi_permute_rows": (_I, [_P, _P, _I, _I, _P, _P]),
@@ -251,6 +274,48 @@ def pi_kv_workspace_size(n_seq, n_tok, max_q, n_head, n_kv, d) -> int:
     out = _SZ(0)
     check(load().pi_kv_workspace_size(n_seq, n_tok, max_q, n_head, n_kv, d, ctypes.byref(out)),
           "pi_kv_workspace_size")
+    return out.value
+
+
+def pi_rope_frequencies(rot, base, scaling, factor, trained, slow, fast):
+    """Host-only: (frequencies as a float64 numpy array, gain)."""
+    import numpy as np
+    freqs, gain = np.empty(max(1, rot // 2), dtype=np.float64), ctypes.c_float(0)
+    check(load().pi_rope_frequencies(rot, base, scaling, factor, trained, slow, fast, freqs.ctypes.data, ctypes.byref(gain)),
+          "pi_rope_frequencies")
+    return freqs, gain.value
+
+
+def pi_rope_turns(freqs):
+    """Host-only: the turns of a float64 numpy array of frequencies, uint64."""
+    import numpy as np
+    freqs = np.ascontiguousarray(freqs, dtype=np.float64)
+    turns = np.empty(max(1, freqs.size), dtype=np.uint64)
+    check(load().pi_rope_turns(freqs.ctypes.data, freqs.size, turns.ctypes.data), "pi_rope_turns")
+    return turns
+
+
+def pi_rotate(rope, pos, n_tok, n_head, d, x, x_stride, y, y_stride, stream=None) -> int:
+    """rope: Rope (or None, which the library rejects)."""
+    return load().pi_rotate(rope, _ptr(pos), n_tok, n_head, d, _ptr(x), x_stride, _ptr(y), y_stride, _stream(stream))
+
+
+def pi_kv_append_rope(cache, batch, rope, rows, n_src, k, k_stride, v, v_stride, q, q_stride, n_head, q_out, out_stride,
+                      stream=None) -> int:
+    return load().pi_kv_append_rope(cache, batch, rope, _ptr(rows), n_src, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(q), q_stride,
+                                    n_head, _ptr(q_out), out_stride, _stream(stream))
+
+
+def pi_verify(n_seq, n_tok, vocab, q_start, ctx, tokens, parent, p, p_stride, q, q_stride, u, u_next, rows, start, new_ctx, next_,
+              ws, ws_bytes, stream=None) -> int:
+    return load().pi_verify(n_seq, n_tok, vocab, _ptr(q_start), _ptr(ctx), _ptr(tokens), _ptr(parent), _ptr(p), p_stride, _ptr(q),
+                            q_stride, _ptr(u), _ptr(u_next), _ptr(rows), _ptr(start), _ptr(new_ctx), _ptr(next_), _ptr(ws), ws_bytes,
+                            _stream(stream))
+
+
+def pi_verify_workspace_size(n_seq, n_tok, vocab) -> int:
+    out = _SZ(0)
+    check(load().pi_verify_workspace_size(n_seq, n_tok, vocab, ctypes.byref(out)), "pi_verify_workspace_size")
     return out.value
 
 

@@ -281,6 +281,38 @@ pi_status check_kv(const pi_kv_cache* c, const pi_kv_batch* b, pi::KvCache* kc, 
     return PI_OK;
 }
 
+pi_status check_verify_sizes(int n_seq, int n_tok, int vocab) {
+    PI_TRY(check_kv_counts(n_seq, n_tok, 1));
+    PI_REQUIRE(vocab >= 1 && vocab <= PI_VERIFY_MAX_VOCAB, PI_ERR_INVALID_ARG, "vocab=%d outside [1, %d]", vocab,
+               PI_VERIFY_MAX_VOCAB);
+    return PI_OK;
+}
+
+// A rotary plan for heads of d, checked and turned into the kernels' own.
+pi_status check_rope(const pi_rope* r, int d, pi::Rope* out) {
+    PI_REQUIRE(r != nullptr, PI_ERR_INVALID_ARG, "rope is NULL");
+    PI_REQUIRE(r->layout == PI_ROPE_HALF || r->layout == PI_ROPE_PAIRS, PI_ERR_INVALID_ARG, "layout=%d unknown", r->layout);
+    PI_REQUIRE(r->rot >= 2 && r->rot <= d && r->rot % 2 == 0, PI_ERR_INVALID_ARG, "rot=%d is not an even number in [2, d=%d]",
+               r->rot, d);
+    PI_REQUIRE(r->gain >= 0x1p-10f && r->gain <= 0x1p10f, PI_ERR_INVALID_ARG, "gain=%g outside [2^-10, 2^10]", (double)r->gain);
+    PI_REQUIRE(r->turns != nullptr, PI_ERR_INVALID_ARG, "turns is NULL");
+    PI_REQUIRE(aligned(r->turns, 8), PI_ERR_UNSUPPORTED, "turns is not 8-byte aligned");
+    *out = pi::Rope{r->layout, r->rot, r->gain, r->turns};
+    return PI_OK;
+}
+
+// Rows that a rotation reads and writes: in place, or apart.
+pi_status check_rotated(const pi_half* x, int64_t x_stride, const pi_half* y, int64_t y_stride, int64_t rows, int64_t row) {
+    if (x == y) {
+        PI_REQUIRE(x_stride == y_stride, PI_ERR_INVALID_ARG, "in place with strides %lld and %lld", (long long)x_stride,
+                   (long long)y_stride);
+        return PI_OK;
+    }
+    PI_REQUIRE(x + (rows - 1) * x_stride + row <= y || y + (rows - 1) * y_stride + row <= x, PI_ERR_INVALID_ARG,
+               "input and output overlap without being the same");
+    return PI_OK;
+}
+
 // The calls proper, on a checked workspace: hdr is its synchronisation header,
 // data the call's data area; clear: zero the tagged words first (single-token
 // paths only).
@@ -844,6 +876,139 @@ pi_status pi_kv_workspace_size(int n_seq, int n_tok, int max_q, int n_head, int 
     PI_TRY(check_kv_rows(n_tok, n_head, n_kv));
     PI_TRY(check_kv_d(d));
     *bytes = kv_ws_bytes(n_seq, n_tok, max_q, n_head, n_kv, d);
+    return ok();
+}
+
+pi_status pi_rope_frequencies(int rot, double base, int scaling, double factor, double trained, double slow, double fast,
+                              double* freqs, float* gain) {
+    PI_REQUIRE(freqs && gain, PI_ERR_INVALID_ARG, "NULL pointer argument");
+    PI_REQUIRE(rot >= 2 && rot % 2 == 0, PI_ERR_INVALID_ARG, "rot=%d is not an even positive number", rot);
+    PI_REQUIRE(std::isfinite(base) && base > 1.0, PI_ERR_INVALID_ARG, "base=%g must be above 1", base);
+    PI_REQUIRE(scaling >= PI_ROPE_PLAIN && scaling <= PI_ROPE_YARN, PI_ERR_INVALID_ARG, "scaling=%d unknown", scaling);
+    PI_REQUIRE(scaling == PI_ROPE_PLAIN || (std::isfinite(factor) && factor >= 1.0), PI_ERR_INVALID_ARG,
+               "factor=%g must be at least 1", factor);
+    if (scaling == PI_ROPE_YARN) {
+        PI_REQUIRE(std::isfinite(trained) && trained >= 1.0, PI_ERR_INVALID_ARG, "trained=%g must be at least 1", trained);
+        PI_REQUIRE(std::isfinite(fast) && slow >= 0.0 && slow < fast, PI_ERR_INVALID_ARG, "slow=%g and fast=%g: not 0 <= slow < fast",
+                   slow, fast);
+    }
+    const double tau = 6.283185307179586476925287;
+    if (scaling == PI_ROPE_NTK && rot > 2) base *= std::pow(factor, rot / (rot - 2.0));
+    for (int m = 0; m < rot / 2; ++m) {
+        double f = std::pow(base, -2.0 * m / rot);
+        if (scaling == PI_ROPE_LINEAR) f /= factor;
+        if (scaling == PI_ROPE_YARN) {
+            const double c = std::min(1.0, std::max(0.0, (trained * f / tau - slow) / (fast - slow)));
+            f = (1.0 - c) * f / factor + c * f;
+        }
+        freqs[m] = f;
+    }
+    *gain = scaling == PI_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    return ok();
+}
+
+pi_status pi_rope_turns(const double* freqs, int n, uint64_t* turns) {
+    PI_REQUIRE(freqs && turns, PI_ERR_INVALID_ARG, "NULL pointer argument");
+    PI_REQUIRE(n >= 1, PI_ERR_INVALID_ARG, "n=%d must be positive", n);
+    for (int m = 0; m < n; ++m)
+        PI_REQUIRE(freqs[m] >= 0.0 && freqs[m] <= 0x1p20, PI_ERR_INVALID_ARG, "frequency %d is %g, not in [0, 2^20]", m, freqs[m]);
+    for (int m = 0; m < n; ++m) {
+        const long double t = (long double)freqs[m] / 6.283185307179586476925286766559L, part = t - floorl(t);
+        const long double v = roundl(part * 0x1p64L);
+        turns[m] = v >= 0x1p64L ? 0 : (uint64_t)v;
+    }
+    return ok();
+}
+
+pi_status pi_rotate(const pi_rope* rope, const int32_t* pos, int n_tok, int n_head, int d, const pi_half* x, int64_t x_stride,
+                    pi_half* y, int64_t y_stride, void* stream) {
+    PI_REQUIRE(d >= 1, PI_ERR_INVALID_ARG, "d=%d must be positive", d);
+    PI_REQUIRE(d % 8 == 0 && d <= PI_KV_MAX_D, PI_ERR_UNSUPPORTED, "d=%d is not a multiple of 8 up to %d", d, PI_KV_MAX_D);
+    pi::Rope r;
+    PI_TRY(check_rope(rope, d, &r));
+    PI_REQUIRE(n_tok >= 1 && n_tok <= PI_KV_MAX_TOKENS, PI_ERR_INVALID_ARG, "n_tok=%d outside [1, %d]", n_tok, PI_KV_MAX_TOKENS);
+    PI_REQUIRE(n_head >= 1 && n_head <= 2 * PI_KV_MAX_HEADS, PI_ERR_INVALID_ARG, "n_head=%d outside [1, %d]", n_head,
+               2 * PI_KV_MAX_HEADS);
+    PI_TRY(check_word(pos, "pos", true));
+    PI_TRY(check_half(x, "x", true));
+    PI_TRY(check_half(y, "y", true));
+    PI_TRY(check_stride(x_stride, (int64_t)n_head * d, "x_stride"));
+    PI_TRY(check_stride(y_stride, (int64_t)n_head * d, "y_stride"));
+    PI_TRY(check_rotated(x, x_stride, y, y_stride, n_tok, (int64_t)n_head * d));
+    hipError_t e = pi::launch_rotate(r, pos, n_tok, reinterpret_cast<const pi::h16*>(x), x_stride, n_head, d,
+                                     reinterpret_cast<pi::h16*>(y), y_stride, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "pi_rotate");
+    return ok();
+}
+
+pi_status pi_kv_append_rope(const pi_kv_cache* cache, const pi_kv_batch* batch, const pi_rope* rope, const int32_t* rows,
+                            int n_src, const pi_half* k, int64_t k_stride, const pi_half* v, int64_t v_stride,
+                            const pi_half* q, int64_t q_stride, int n_head, pi_half* q_out, int64_t out_stride, void* stream) {
+    pi::KvCache c;
+    pi::KvBatch b;
+    pi::Rope r{};
+    PI_TRY(check_kv(cache, batch, &c, &b));
+    if (rope) PI_TRY(check_rope(rope, c.d, &r));
+    PI_TRY(check_word(rows, "rows", false));
+    PI_REQUIRE(n_src >= (rows ? 1 : b.n_tok) && n_src <= PI_KV_MAX_TOKENS, PI_ERR_INVALID_ARG, "n_src=%d outside [%d, %d]", n_src,
+               rows ? 1 : b.n_tok, PI_KV_MAX_TOKENS);
+    PI_TRY(check_half(k, "k", true));
+    PI_TRY(check_half(v, "v", true));
+    PI_TRY(check_stride(k_stride, (int64_t)c.n_kv * c.d, "k_stride"));
+    PI_TRY(check_stride(v_stride, (int64_t)c.n_kv * c.d, "v_stride"));
+    if (q) {
+        PI_REQUIRE(rope != nullptr, PI_ERR_INVALID_ARG, "q without rope");
+        PI_REQUIRE(rows == nullptr, PI_ERR_INVALID_ARG, "q together with rows");
+        PI_TRY(check_heads(n_head, c.n_kv));
+        PI_TRY(check_half(q, "q", true));
+        PI_TRY(check_half(q_out, "q_out", true));
+        PI_TRY(check_stride(q_stride, (int64_t)n_head * c.d, "q_stride"));
+        PI_TRY(check_stride(out_stride, (int64_t)n_head * c.d, "out_stride"));
+        PI_TRY(check_rotated(q, q_stride, q_out, out_stride, b.n_tok, (int64_t)n_head * c.d));
+    }
+    hipError_t e = pi::launch_kv_append_rope(
+        c, b, rope ? &r : nullptr, rows, n_src, reinterpret_cast<const pi::h16*>(k), k_stride, reinterpret_cast<const pi::h16*>(v),
+        v_stride, reinterpret_cast<const pi::h16*>(q), q_stride, n_head, reinterpret_cast<pi::h16*>(q_out), out_stride,
+        static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "pi_kv_append_rope");
+    return ok();
+}
+
+pi_status pi_verify(int n_seq, int n_tok, int vocab, const int32_t* q_start, const int32_t* ctx, const int32_t* tokens,
+                    const int32_t* parent, const float* p, int64_t p_stride, const float* q, int64_t q_stride, const float* u,
+                    const float* u_next, int32_t* rows, int32_t* start, int32_t* new_ctx, int32_t* next, void* ws, size_t ws_bytes,
+                    void* stream) {
+    PI_TRY(check_verify_sizes(n_seq, n_tok, vocab));
+    PI_TRY(check_word(q_start, "q_start", true));
+    PI_TRY(check_word(ctx, "ctx", true));
+    PI_TRY(check_word(tokens, "tokens", true));
+    PI_TRY(check_word(parent, "parent", true));
+    PI_TRY(check_word(p, "p", true));
+    PI_TRY(check_word(q, "q", false));
+    PI_TRY(check_word(u, "u", true));
+    PI_TRY(check_word(u_next, "u_next", true));
+    PI_TRY(check_word(rows, "rows", true));
+    PI_TRY(check_word(start, "start", true));
+    PI_TRY(check_word(new_ctx, "new_ctx", true));
+    PI_TRY(check_word(next, "next", true));
+    const int64_t far = (int64_t)1 << 40;
+    PI_REQUIRE(p_stride >= vocab && p_stride <= far, PI_ERR_INVALID_ARG, "p_stride=%lld is below vocab=%d or out of range",
+               (long long)p_stride, vocab);
+    PI_REQUIRE(!q || (q_stride >= vocab && q_stride <= far), PI_ERR_INVALID_ARG, "q_stride=%lld is below vocab=%d or out of range",
+               (long long)q_stride, vocab);
+    PI_TRY(check_ws(ws, ws_bytes, pi::verify_bytes(n_seq, n_tok, vocab), "pi_verify"));
+    ws_forget(ws);
+    pi::VerifyArgs A{n_seq, n_tok, vocab, q_start, ctx, tokens, parent, p, q, p_stride, q_stride, u, u_next, rows, start, new_ctx,
+                     next, 0, 0};
+    hipError_t e = pi::launch_verify(A, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "pi_verify");
+    return ok();
+}
+
+pi_status pi_verify_workspace_size(int n_seq, int n_tok, int vocab, size_t* bytes) {
+    PI_REQUIRE(bytes != nullptr, PI_ERR_INVALID_ARG, "bytes is NULL");
+    PI_TRY(check_verify_sizes(n_seq, n_tok, vocab));
+    *bytes = pi::verify_bytes(n_seq, n_tok, vocab);
     return ok();
 }
 

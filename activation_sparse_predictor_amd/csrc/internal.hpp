@@ -303,6 +303,22 @@ struct KvBatch {
     const int32_t *q_start, *ctx, *table;
 };
 
+// rotary positions (pi_rope with device-side types)
+struct Rope {
+    int layout, rot;
+    float gain;
+    const uint64_t* turns;
+};
+
+// rope.hip
+hipError_t launch_rotate(const Rope& R, const int32_t* pos, int n_tok, const h16* x, long long x_stride, int n_head, int d,
+                         h16* y, long long y_stride, hipStream_t s);
+
+// append.hip: k and v hold n_src rows, the batch's row i is rows[i] (rows NULL: i); rope NULL: nothing is turned; q NULL: no queries
+hipError_t launch_kv_append_rope(const KvCache& c, const KvBatch& b, const Rope* rope, const int32_t* rows, int n_src, const h16* k,
+                                 long long k_stride, const h16* v, long long v_stride, const h16* q, long long q_stride,
+                                 int n_head, h16* q_out, long long out_stride, hipStream_t s);
+
 // kv.hip
 hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const h16* k, long long k_stride, const h16* v,
                             long long v_stride, hipStream_t s);
@@ -313,6 +329,19 @@ size_t kv_attend_bytes(int n_seq, int n_tok, int max_q, int n_head, int n_kv, in
 size_t kv_attend_zero_bytes();   // at the data area's start: counters, all zero between calls
 hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
                             float scale, int window, h16* y, float* lse, char* data, hipStream_t s);
+
+// verify.hip
+struct VerifyArgs {
+    int n_seq, n_tok, vocab;
+    const int32_t *q_start, *ctx, *tokens, *parent;
+    const float *p, *q;   // q NULL: drafts without probabilities
+    long long p_stride, q_stride;
+    const float *u, *u_next;
+    int32_t *rows, *start, *new_ctx, *next;
+    int slice, slices;    // set by launch_verify
+};
+size_t verify_bytes(int n_seq, int n_tok, int vocab);
+hipError_t launch_verify(VerifyArgs A, char* ws, hipStream_t s);
 
 // profile.hip
 hipError_t launch_profile(const h16* X, int n, int d, int ffn, const h16* W, const float* b,

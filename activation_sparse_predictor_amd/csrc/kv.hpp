@@ -1,5 +1,5 @@
-// Device helpers of the 8-bit paged cache (kv.hip, attend.hip): code formats,
-// byte order, and where a call's tokens lie.
+// Device helpers of the 8-bit paged cache (kv.hip, append.hip, attend.hip): code
+// formats, byte order, rounding, and where a call's tokens lie.
 #pragma once
 
 #include "common.hpp"
@@ -60,6 +60,102 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
     return Codes<FMT>::encode2(a, b) | (Codes<FMT>::encode2(c, d) << 16);
 }
 
+// The scale and the quotient are rounded to nearest in fp32, as the definition
+// has them.  A quotient that is a tie in exact arithmetic (fp16 values and
+// largest values share few bits, so there are some: 3 in 10^5 codes) falls to
+// the side that those two roundings leave it on, which another way of dividing
+// by QMAX, or 64 bits, need not share.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+// Largest |x| of two fp16 pairs as bits: the order of the magnitudes' bits is
+// that of the numbers, with infinity and then NaN above all of them.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t x) {
+    const u16x2 a = __builtin_bit_cast(u16x2, m), b = __builtin_bit_cast(u16x2, x & 0x7FFF7FFFu);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
+}
+
+// x / s rounded to nearest, given inv = 1 / s rounded to nearest: one product
+// and one residual step (Markstein's division).  With |x| in fp16's range and
+// s = max|x| / QMAX at least 2^-24 / 448 > 2^-33 nothing here is subnormal.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+    const float q = x * inv;
+    return fmaf(fmaf(-q, s, x), inv, q);
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4_f16(uint32_t lo, uint32_t hi, float s, float inv) {
+    const f16x2 a = as_h2(lo), b = as_h2(hi);
+    return encode4<FMT>(quotient((float)a.x, s, inv), quotient((float)a.y, s, inv), quotient((float)b.x, s, inv),
+                        quotient((float)b.y, s, inv));
+}
+
+// Four codes rounded again after the scale grew by 1 / r.
+template <int FMT>
+__device__ __forceinline__ uint32_t requant4(uint32_t w, float r) {
+    f16x2 a, b;
+    Codes<FMT>::to_f16(w, a, b);
+    return encode4<FMT>((float)a.x * r, (float)a.y * r, (float)b.x * r, (float)b.y * r);
+}
+
+// The codes of a block's V tokens [a, e), from the values x of MAXT tasks a thread
+// (two dimensions of a granule's 16 tokens, a token's in one word), scale s and inv =
+// 1 / s (zero: all codes are 0), the older codes times r if the scale grew.
+template <int FMT, int kThreads, int MAXT>
+__device__ __forceinline__ void store_v(uint8_t* dst, const uint32_t (&x)[MAXT][16], int tid, int dp, int a, int e, float s, float inv,
+                                        float r, bool zero, bool grew) {
+#pragma unroll
+    for (int i = 0; i < MAXT; ++i) {
+        const int u = tid + i * kThreads;
+        const int g = u / dp * kGran;
+        if (g >= e || (g + kGran <= a && !grew)) continue;
+        u32x4* at = reinterpret_cast<u32x4*>(dst + (size_t)u * 32);
+        // the granule's new codes for both dimensions, [a, e) of them to be used
+        u32x4 n[2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t lo4 = Codes<FMT>::kZero4, hi4 = lo4;
+            if (!zero && g + 4 * j + 3 >= a && g + 4 * j < e) {
+                const uint32_t p = x[i][4 * j], y = x[i][4 * j + 1], z = x[i][4 * j + 2], w = x[i][4 * j + 3];
+                lo4 = encode4_f16<FMT>((p & 0xFFFFu) | (y << 16), (z & 0xFFFFu) | (w << 16), s, inv);
+                hi4 = encode4_f16<FMT>((p >> 16) | (y & 0xFFFF0000u), (z >> 16) | (w & 0xFFFF0000u), s, inv);
+            }
+            n[0][j] = lo4;
+            n[1][j] = hi4;
+        }
+        if (g >= a && g + kGran <= e) {
+            at[0] = n[0];
+            at[1] = n[1];
+        } else if (!grew) {   // single bytes, without waiting for what lies between them
+            uint8_t* b = reinterpret_cast<uint8_t*>(at);
+#pragma unroll
+            for (int t = 0; t < kGran; ++t) {
+                if (g + t < a || g + t >= e) continue;
+                b[t] = (uint8_t)(n[0][t / 4] >> (t % 4 * 8));
+                b[kGran + t] = (uint8_t)(n[1][t / 4] >> (t % 4 * 8));
+            }
+        } else {   // the older codes rounded again, and what lies behind the new ones kept
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const u32x4 o = at[k];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = g + 4 * j;
+                    const uint32_t again = t < a ? requant4<FMT>(o[j], r) : 0u;
+                    uint32_t keep = 0u;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t by = 0xFFu << (8 * y);
+                        keep |= (t + y < a ? again : t + y < e ? n[k][j] : o[j]) & by;
+                    }
+                    n[k][j] = keep;
+                }
+            }
+            at[0] = n[0];
+            at[1] = n[1];
+        }
+    }
+}
+
 // A sequence of the batch, with everything read from the device clamped so
 // that no row and no table entry outside the arrays can follow from it.
 struct Seq {
@@ -116,6 +212,17 @@ __device__ __forceinline__ Seq find_seq(const KvBatch& b, int item, int& inside,
     }
     inside = 0;
     return none;
+}
+
+// Upper bound of the blocks of `page` tokens that the batch's rows lie in:
+// n rows touch at most (n + page - 2) / page + 1 of them, and at most n.
+inline long long touched(const KvBatch& b, int page) {
+    long long n = b.n_tok;
+    const long long each = (long long)b.n_seq * ((b.max_q + page - 2) / page + 1);
+    const long long all = (long long)b.n_tok / page + 2LL * b.n_seq;
+    if (each < n) n = each;
+    if (all < n) n = all;
+    return n;
 }
 
 }  // namespace pi

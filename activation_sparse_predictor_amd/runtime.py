@@ -476,6 +476,129 @@ def kv_attend(cache: dict, q: torch.Tensor, batch: dict, y: Optional[torch.Tenso
     return y
 
 
+# ---- rotary positions.  A plan is a dict: layout ("half" or "pairs"), rot, gain
+# and turns (device, rot / 2 int64: the bits of the C ABI's uint64).
+
+
+def rope(rot: int, base: float = 10000.0, layout: str = "half", scaling: str = "none", factor: float = 1.0,
+         trained: float = 4096.0, slow: float = 1.0, fast: float = 32.0, freqs=None, gain: Optional[float] = None,
+         device="cuda") -> dict:
+    """A rotary plan for the first rot dimensions of a head: pi_rope_frequencies'
+    (scaling "none", "linear", "ntk" or "yarn"), or the caller's own freqs
+    (rot / 2 radians a position) and gain."""
+    import numpy as np
+    _need(layout in B.ROPE_LAYOUTS and scaling in B.ROPE_SCALINGS, "layout is 'half' or 'pairs', scaling 'none', 'linear', 'ntk' or 'yarn'")
+    if freqs is None:
+        freqs, own = B.pi_rope_frequencies(int(rot), float(base), B.ROPE_SCALINGS[scaling], float(factor), float(trained),
+                                           float(slow), float(fast))
+        gain = own if gain is None else gain
+    freqs = np.asarray(freqs, dtype=np.float64)
+    _need(freqs.shape == (rot // 2,), "freqs must be rot / 2 numbers")
+    turns = torch.from_numpy(B.pi_rope_turns(freqs).view(np.int64)).to(device)
+    return {"layout": layout, "rot": int(rot), "gain": 1.0 if gain is None else float(gain), "turns": turns}
+
+
+def _rope_args(plan: dict, device: int):
+    turns, layout, rot = plan["turns"], B.ROPE_LAYOUTS.get(plan["layout"]), plan["rot"]
+    if not (layout is not None and turns.dtype is torch.int64 and turns.shape == (rot // 2,) and turns.is_contiguous()
+            and turns.get_device() == device):
+        raise ValueError("a rotary plan is layout ('half' or 'pairs'), rot, gain and turns (rot / 2 int64), on the tensors' device")
+    return B.Rope(layout, rot, plan["gain"], turns.data_ptr())
+
+
+def rotate(x: torch.Tensor, pos: torch.Tensor, plan: dict, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pi_rotate: x (n_tok x n_head x d fp16, tokens any multiple of 8 elements
+    apart) turned by the positions pos (n_tok int32), into out (x itself: in place)."""
+    dev = x.get_device()
+    if _is_elsewhere(stream, dev):
+        return _elsewhere(stream, x.device, (x, pos, out, plan["turns"]), lambda: rotate(x, pos, plan, out))
+    _need(x.dim() == 3, "x must be fp16, n_tok x heads x d")
+    n, heads, d = x.shape
+    xs = _kv_rows(x, n, heads, d, "x")
+    _need(pos.dtype is _I32 and pos.shape == (n,) and pos.is_contiguous() and pos.get_device() == dev,
+          "pos must be n_tok int32 on x's device")
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ys = heads * d
+    else:
+        ys = _kv_rows(out, n, heads, d, "out")
+        _need(out.get_device() == dev, "out must be on x's device")
+    B.check(B.pi_rotate(_rope_args(plan, dev), pos, n, heads, d, x, xs, out, ys, _raw_stream(dev)), "pi_rotate")
+    return out
+
+
+def kv_append_rope(cache: dict, k: torch.Tensor, v: torch.Tensor, batch: dict, rope: Optional[dict] = None,
+                   q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                   rows: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """pi_kv_append_rope: kv_append with k turned by its cache positions (rope: a
+    plan) on the way, and q (n_tok x n_head x d) by the same into q_out (q itself:
+    in place), which is returned.  rows (n_tok int32): the batch's row i is row
+    rows[i] of k and v, as verify gives them."""
+    dev = k.get_device()
+    if _is_elsewhere(stream, dev):
+        return _elsewhere(stream, k.device, (k, v, q, q_out, rows, rope["turns"] if rope else None, *cache.values(), *batch.values()),
+                          lambda: kv_append_rope(cache, k, v, batch, rope, q, q_out, rows))
+    c, b = _kv_args(cache, batch, dev)
+    n_src = b.n_tok
+    if rows is not None:
+        _need(rows.dtype is _I32 and rows.shape == (b.n_tok,) and rows.is_contiguous() and rows.get_device() == dev,
+              "rows must be n_tok int32 on k's device")
+        n_src = k.shape[0]
+    ks = _kv_rows(k, n_src, c.n_kv, c.d, "k")
+    vs = _kv_rows(v, n_src, c.n_kv, c.d, "v")
+    _need(v.get_device() == dev, "k and v must be on one device")
+    plan = None if rope is None else _rope_args(rope, dev)
+    qs = os_ = heads = 0
+    if q is not None:
+        qs = _kv_rows(q, b.n_tok, None, c.d, "q")
+        heads = q.shape[1]
+        _need(q.get_device() == dev, "q must be on k's device")
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            os_ = heads * c.d
+        else:
+            os_ = _kv_rows(q_out, b.n_tok, heads, c.d, "q_out")
+            _need(q_out.get_device() == dev, "q_out must be on k's device")
+    else:
+        _need(q_out is None, "q_out without q")
+    B.check(B.pi_kv_append_rope(c, b, plan, rows, n_src, k, ks, v, vs, q, qs, heads, q_out, os_, _raw_stream(dev)),
+            "pi_kv_append_rope")
+    return q_out
+
+
+def verify(batch: dict, tokens: torch.Tensor, parent: torch.Tensor, p: torch.Tensor, u: torch.Tensor, u_next: torch.Tensor,
+           q: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """pi_verify: which drafted tokens stay.  batch: q_start, ctx and n_tok of the
+    rows; tokens and parent (n_tok int32); p and q (n_tok x vocab float32, rows
+    any number of elements apart; q None: fixed proposals); u (n_tok float32) and
+    u_next (n_seq).  Returns rows (n_tok int32, -1 behind the last), q_start, ctx
+    and next: {**batch, **verify(...)} is the batch of the tokens that stay, whose
+    rows kv_append_rope takes."""
+    start, ctx, n_tok = batch["q_start"], batch["ctx"], batch["n_tok"]
+    dev = p.get_device()
+    if _is_elsewhere(stream, dev):
+        return _elsewhere(stream, p.device, (start, ctx, tokens, parent, p, u, u_next, q),
+                          lambda: verify(batch, tokens, parent, p, u, u_next, q))
+    n_seq = ctx.shape[0] if ctx.dim() == 1 else -1
+    words, floats = (start, ctx, tokens, parent), (p, u, u_next) if q is None else (p, u, u_next, q)
+    if not (all(t.dtype is _I32 and t.is_contiguous() and t.get_device() == dev for t in words)
+            and all(t.dtype is _F32 and t.get_device() == dev for t in floats)
+            and start.shape == (n_seq + 1,) and tokens.shape == parent.shape == u.shape == (n_tok,) and u_next.shape == (n_seq,)
+            and u.is_contiguous() and u_next.is_contiguous() and p.dim() == 2 and p.shape[0] == n_tok
+            and (p.stride(1) == 1 or p.shape[1] == 1) and (q is None or (q.shape == p.shape and (q.stride(1) == 1 or q.shape[1] == 1)))):
+        raise ValueError("q_start (n_seq + 1), ctx (n_seq), tokens and parent (n_tok) are int32, u (n_tok), u_next (n_seq), p and q "
+                         "(n_tok x vocab, rows of neighbours) float32; all on one device")
+    vocab = p.shape[1]
+    rows, new_start, new_ctx, after = torch.empty(n_tok + 3 * n_seq + 1, dtype=_I32, device=p.device).split(
+        [n_tok, n_seq + 1, n_seq, n_seq])
+    size = B.pi_verify_workspace_size(n_seq, n_tok, vocab)
+    ws = torch.empty(size, dtype=_U8, device=p.device)
+    B.check(B.pi_verify(n_seq, n_tok, vocab, start, ctx, tokens, parent, p, p.stride(0) if n_tok > 1 else vocab, q,
+                        0 if q is None else q.stride(0) if n_tok > 1 else vocab, u, u_next, rows, new_start, new_ctx, after, ws, size,
+                        _raw_stream(dev)), "pi_verify")
+    return {"rows": rows, "q_start": new_start, "ctx": new_ctx, "next": after}
+
+
 def profile(X: torch.Tensor, W_fire: torch.Tensor, b_fire: Optional[torch.Tensor],
             counts: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     n, d = X.shape

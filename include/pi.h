@@ -585,6 +585,151 @@ pi_status pi_kv_attend(const pi_kv_cache* cache, const pi_kv_batch* batch,
 /* Workspace bytes of pi_kv_attend for these sizes. */
 pi_status pi_kv_workspace_size(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d, size_t* bytes);
 
+/*
+ * ---- Rotary positions ---------------------------------------------------------
+ *
+ * A head's pair of dimensions (a, b) at position p becomes
+ *   gain (a cos t - b sin t),  gain (b cos t + a sin t),  t = p f_m
+ * for pair m of rot / 2, f_m its frequency in radians a position; dimensions from
+ * rot on stay as they are.  The plan holds the frequencies as parts of a turn,
+ *   turns[m] = f_m / (2 pi) mod 1, in units of 2^-64,
+ * so that p * turns[m] mod 2^64 is the angle itself, exact at any position.
+ */
+typedef enum pi_rope_layout {
+    PI_ROPE_HALF = 0,    /* pair m: dimensions m and m + rot / 2 */
+    PI_ROPE_PAIRS = 1    /* pair m: dimensions 2 m and 2 m + 1 */
+} pi_rope_layout;
+
+typedef enum pi_rope_scaling {
+    PI_ROPE_PLAIN = 0,   /* f_m = base^(-2 m / rot) */
+    PI_ROPE_LINEAR = 1,  /* f_m / factor: positions as if they were factor times closer */
+    PI_ROPE_NTK = 2,     /* base times factor^(rot / (rot - 2)) (rot = 2: base): the slowest pair is stretched by factor, the fastest kept */
+    PI_ROPE_YARN = 3     /* each pair between its own and the linear frequency, by its turns n over
+                            the trained length: own from n = fast on, linear up to n = slow,
+                            in between (1 - c) f / factor + c f with c = (n - slow) / (fast - slow);
+                            gain = 0.1 ln(factor) + 1 */
+} pi_rope_scaling;
+
+typedef struct pi_rope {    /* read by the host during the call */
+    int layout;             /* pi_rope_layout */
+    int rot;                /* dimensions that are turned: even, 2 .. d */
+    float gain;             /* of the turned dimensions, in [2^-10, 2^10] */
+    const uint64_t* turns;  /* device: rot / 2 */
+} pi_rope;
+
+/*
+ * pi_rope_frequencies -- HOST-ONLY frequencies (host, rot / 2 doubles) and gain (host).
+ * trained (tokens), slow and fast (turns, usually 1 and 32) are PI_ROPE_YARN's; the
+ * others ignore them.  factor is ignored by PI_ROPE_PLAIN.
+ * Errors: INVALID_ARG for NULL pointers, an odd or non-positive rot, base not finite or
+ * not above 1, an unknown scaling, factor below 1, trained < 1, or not 0 <= slow < fast.
+ *
+ * pi_rope_turns -- HOST-ONLY: turns[m] (host) from n frequencies (host), rounded to
+ * nearest.  Errors: INVALID_ARG for NULL pointers, n < 1, a frequency that is negative, not finite or above 2^20.
+ */
+pi_status pi_rope_frequencies(int rot, double base, int scaling, double factor, double trained, double slow, double fast,
+                              double* freqs, float* gain);
+pi_status pi_rope_turns(const double* freqs, int n, uint64_t* turns);
+
+/*
+ * pi_rotate -- rotary positions of rows.
+ *
+ * x: n_tok rows of n_head heads of d (heads contiguous, tokens x_stride elements
+ * apart); row i is at position pos[i] (device; any int32, negative ones turn
+ * back).  y likewise, y_stride apart: x itself (y = x, same stride) or memory
+ * outside the span from x's first element to its last; in place, dimensions
+ * from rot on are not touched.  Products and sums are fp32, each result is
+ * rounded to fp16 once.
+ *
+ * Errors: INVALID_ARG for NULL pointers, an unknown layout, rot odd or outside
+ * [2, d], a gain outside its range, n_tok outside [1, PI_KV_MAX_TOKENS],
+ * n_head outside [1, 2 PI_KV_MAX_HEADS] (queries and keys of one projection can
+ * be turned in one call), strides below a row, y = x with another stride;
+ * UNSUPPORTED for d not a multiple of 8 up to PI_KV_MAX_D, strides not
+ * multiples of 8, misalignment (fp16 16 bytes, pos 4, turns 8).
+ */
+pi_status pi_rotate(const pi_rope* rope, const int32_t* pos, int n_tok, int n_head, int d,
+                    const pi_half* x, int64_t x_stride, pi_half* y, int64_t y_stride, void* stream);
+
+/*
+ * pi_kv_append_rope -- pi_kv_append with the position rotation on the way.
+ *
+ * As pi_kv_append (its rules for blocks, scales, codes and values that are not
+ * finite), with three additions:
+ *  - rope (may be NULL: none): keys are turned by their cache position before they are
+ *    quantised.  They stay in fp32 in between: a code is what the rotation in
+ *    fp32 gives, without a rounding to fp16.
+ *  - rows (device, may be NULL): row i of the batch is row rows[i] of k and v,
+ *    which hold n_src rows; an entry outside [0, n_src) counts as a value that is not
+ *    finite.  NULL: row i itself (n_src >= n_tok).  Entries past the
+ *    batch's last row (q_start[n_seq]) are not read: pi_verify's results go in as they are.
+ *  - q (may be NULL): n_tok rows of n_head heads of d, q_stride apart, turned by
+ *    the positions of the batch's rows, as pi_rotate does, into q_out
+ *    (out_stride apart; q itself with q's stride, or memory outside its span,
+ *    and not k or v).  Rows that belong to no sequence are left as they were.
+ *    Needs rope, and rows NULL.
+ * One launch.
+ *
+ * Errors: as pi_kv_append and pi_rotate; INVALID_ARG for n_src below 1 (or
+ * below n_tok without rows) or above PI_KV_MAX_TOKENS, q without q_out or rope
+ * or with rows, n_head not a multiple of n_kv.
+ */
+pi_status pi_kv_append_rope(const pi_kv_cache* cache, const pi_kv_batch* batch, const pi_rope* rope,
+                            const int32_t* rows, int n_src, const pi_half* k, int64_t k_stride,
+                            const pi_half* v, int64_t v_stride, const pi_half* q, int64_t q_stride, int n_head,
+                            pi_half* q_out, int64_t out_stride, void* stream);
+
+/*
+ * ---- Drafted tokens -----------------------------------------------------------
+ *
+ * A step of speculative decoding: each sequence brings n rows, the newest known
+ * token (whose key and value are not in the cache yet) and drafted ones below it,
+ * a chain or a tree; the model runs on all of them at once (pi_rotate,
+ * pi_kv_attend_tree, the FFN); pi_verify decides which stay; pi_kv_append_rope
+ * writes those, by pi_verify's lists.  The cache never holds a token that is
+ * taken back: a block's scale only grows, so such a token would have cost its
+ * neighbours precision for good.
+ *
+ * pi_verify -- which drafted tokens stay, and the token after them.
+ *
+ * Sequence s has rows q_start[s] .. q_start[s + 1] - 1 of tokens, parent, u, p and q
+ * (q_start[0] = 0, ascending, the last n_tok).  Its row 0 stays.  Row j >= 1 is a drafted
+ * token, tokens[j], below row parent[j] < j (counted from the sequence's
+ * first; one that is not in [0, j) is nobody's child).  p: the target's
+ * distribution after each row (fp32, vocab elements, rows p_stride apart); q
+ * likewise the draft's, from which the row's children were drawn one after
+ * the other; NULL: the drafts are fixed proposals, q is 1 at the child's own
+ * token and 0 elsewhere.  From row 0 on, with P = p of the row:
+ *   the row's children in order: child j with token x stays if u[j] q(x) < P(x),
+ *   and the walk goes on from it; otherwise P becomes max(P - q, 0) over its sum
+ *   and the next child is tried; when none is left,
+ *   next[s] = the smallest x with P(0) + .. + P(x) > u_next[s] (P(0) + .. + P(vocab - 1)).
+ * Tokens and what follows them are then distributed as if drawn from p alone
+ * (u, u_next: uniform in [0, 1)).  If nothing is left of P (all 0), the
+ * row's own p decides; if its sum is 0, infinite or NaN, next[s] = -1.  A
+ * token outside [0, vocab) has probability 0.  Rows of p and q are taken to sum to 1.
+ * p that is 1 at one token and 0 elsewhere is greedy decoding.
+ * Sums and differences are in 64 bits, in an order that depends on the sizes alone.
+ *
+ * Outputs (device): rows (n_tok): the rows that stay, sequence after sequence,
+ * each row 0 first and downward, -1 behind the last; start (n_seq + 1): where each
+ * sequence's begin; new_ctx (n_seq): ctx[s] plus their number; next.  With the page table, start and
+ * new_ctx are the batch for pi_kv_append_rope, and rows its list.  A sequence
+ * without rows: none, ctx[s], next -1.
+ * ws: pi_verify_workspace_size() bytes, 256-byte aligned; it need not be zeroed.
+ *
+ * Errors: INVALID_ARG for NULL pointers, n_seq outside [1, PI_KV_MAX_SEQ], n_tok
+ * outside [1, PI_KV_MAX_TOKENS], vocab outside [1, PI_VERIFY_MAX_VOCAB], strides below vocab;
+ * UNSUPPORTED for misalignment (4 bytes); WORKSPACE.
+ */
+#define PI_VERIFY_MAX_VOCAB (1 << 24)
+pi_status pi_verify(int n_seq, int n_tok, int vocab, const int32_t* q_start, const int32_t* ctx,
+                    const int32_t* tokens, const int32_t* parent, const float* p, int64_t p_stride,
+                    const float* q, int64_t q_stride, const float* u, const float* u_next,
+                    int32_t* rows, int32_t* start, int32_t* new_ctx, int32_t* next,
+                    void* ws, size_t ws_bytes, void* stream);
+pi_status pi_verify_workspace_size(int n_seq, int n_tok, int vocab, size_t* bytes);
+
 /* Workspace bytes that `op` needs for these sizes (op is a pi_op). */
 pi_status pi_workspace_size(int op, int B, int d, int r, int ffn, size_t* bytes);
 
