@@ -50,6 +50,7 @@ PI_ROPE_LINEAR = 1
 PI_ROPE_NTK = 2
 PI_ROPE_YARN = 3
 PI_VERIFY_MAX_VOCAB = 1 << 24
+PI_KV_MAX_TREE = 256
 
 ROPE_LAYOUTS = {"half": PI_ROPE_HALF, "pairs": PI_ROPE_PAIRS}
 ROPE_SCALINGS = {"none": PI_ROPE_PLAIN, "linear": PI_ROPE_LINEAR, "ntk": PI_ROPE_NTK, "yarn": PI_ROPE_YARN}
@@ -111,6 +112,7 @@ _SIGNATURES = {
     "pi_rope_turns": (_I, [_P, _I, _P]),
     "pi_rotate": (_I, [_RP, _P, _I, _I, _I, _P, _LL, _P, _LL, _P]),
     "pi_kv_append_rope": (_I, [_KC, _KB, _RP, _P, _I, _P, _LL, _P, _LL, _P, _LL, _I, _P, _LL, _P]),
+    "pi_kv_attend_tree": (_I, [_KC, _KB, _P, _LL, _I, _P, _LL, _P, _LL, _P, _I, _P, ctypes.c_float, _I, _P, _P, _P, _SZ, _P]),
     "pi_verify": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _LL, _P, _LL, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "pi_verify_workspace_size": (_I, [_I, _I, _I, ctypes.POINTER(_SZ)]),
     "pi_profile": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
@@ -304,6 +306,12 @@ def pi_kv_append_rope(cache, batch, rope, rows, n_src, k, k_stride, v, v_stride,
                       stream=None) -> int:
     return load().pi_kv_append_rope(cache, batch, rope, _ptr(rows), n_src, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(q), q_stride,
                                     n_head, _ptr(q_out), out_stride, _stream(stream))
+
+
+def pi_kv_attend_tree(cache, batch, q, q_stride, n_head, k, k_stride, v, v_stride, mask, words, pos, scale, window, y, lse, ws,
+                      ws_bytes, stream=None) -> int:
+    return load().pi_kv_attend_tree(cache, batch, _ptr(q), q_stride, n_head, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(mask), words,
+                                    _ptr(pos), scale, window, _ptr(y), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
 
 
 def pi_verify(n_seq, n_tok, vocab, q_start, ctx, tokens, parent, p, p_stride, q, q_stride, u, u_next, rows, start, new_ctx, next_,

@@ -281,6 +281,20 @@ pi_status check_kv(const pi_kv_cache* c, const pi_kv_batch* b, pi::KvCache* kc, 
     return PI_OK;
 }
 
+pi_status check_draft(const pi::KvDraft& t, const pi::KvCache& c, const pi::KvBatch& b, int window) {
+    PI_REQUIRE(t.words >= 1 && t.words <= PI_KV_MAX_TREE / 64, PI_ERR_INVALID_ARG, "words=%d outside [1, %d]", t.words,
+               PI_KV_MAX_TREE / 64);
+    PI_REQUIRE(b.max_q <= 64 * t.words, PI_ERR_INVALID_ARG, "max_q=%d above the mask's %d rows", b.max_q, 64 * t.words);
+    PI_TRY(check_half(reinterpret_cast<const pi_half*>(t.k), "k", true));
+    PI_TRY(check_half(reinterpret_cast<const pi_half*>(t.v), "v", true));
+    PI_TRY(check_stride(t.k_stride, (int64_t)c.n_kv * c.d, "k_stride"));
+    PI_TRY(check_stride(t.v_stride, (int64_t)c.n_kv * c.d, "v_stride"));
+    PI_REQUIRE(t.mask != nullptr, PI_ERR_INVALID_ARG, "mask is NULL");
+    PI_REQUIRE(aligned(t.mask, 8), PI_ERR_UNSUPPORTED, "mask is not 8-byte aligned");
+    PI_TRY(check_word(t.pos, "pos", window > 0));
+    return PI_OK;
+}
+
 pi_status check_verify_sizes(int n_seq, int n_tok, int vocab) {
     PI_TRY(check_kv_counts(n_seq, n_tok, 1));
     PI_REQUIRE(vocab >= 1 && vocab <= PI_VERIFY_MAX_VOCAB, PI_ERR_INVALID_ARG, "vocab=%d outside [1, %d]", vocab,
@@ -829,12 +843,17 @@ pi_status pi_kv_read(const pi_kv_cache* cache, const pi_kv_batch* batch, pi_half
     return ok();
 }
 
-pi_status pi_kv_attend(const pi_kv_cache* cache, const pi_kv_batch* batch, const pi_half* q, int64_t q_stride,
-                       int n_head, float scale, int window, pi_half* y, float* lse, void* ws, size_t ws_bytes,
-                       void* stream) {
+}  // extern "C"
+
+namespace {
+// pi_kv_attend and, with drafted rows, pi_kv_attend_tree
+pi_status run_attend(const pi_kv_cache* cache, const pi_kv_batch* batch, const pi_half* q, int64_t q_stride, int n_head,
+                     float scale, int window, pi_half* y, float* lse, const pi::KvDraft* draft, void* ws, size_t ws_bytes,
+                     void* stream, const char* name) {
     pi::KvCache c;
     pi::KvBatch b;
     PI_TRY(check_kv(cache, batch, &c, &b));
+    if (draft) PI_TRY(check_draft(*draft, c, b, window));
     PI_TRY(check_heads(n_head, c.n_kv));
     PI_TRY(check_kv_rows(b.n_tok, n_head, c.n_kv));
     PI_REQUIRE(std::isfinite(scale), PI_ERR_INVALID_ARG, "scale is not finite");
@@ -843,7 +862,7 @@ pi_status pi_kv_attend(const pi_kv_cache* cache, const pi_kv_batch* batch, const
     PI_TRY(check_stride(q_stride, (int64_t)n_head * c.d, "q_stride"));
     PI_TRY(check_half(y, "y", true));
     PI_TRY(check_word(lse, "lse", false));
-    PI_TRY(check_ws(ws, ws_bytes, kv_ws_bytes(b.n_seq, b.n_tok, b.max_q, n_head, c.n_kv, c.d), "pi_kv_attend"));
+    PI_TRY(check_ws(ws, ws_bytes, kv_ws_bytes(b.n_seq, b.n_tok, b.max_q, n_head, c.n_kv, c.d), name));
     hipStream_t s = static_cast<hipStream_t>(stream);
     char* data = static_cast<char*>(ws) + pi::kSyncBytes;
     // one key for every shape: the counters have one place, and each call leaves them zero
@@ -858,13 +877,31 @@ pi_status pi_kv_attend(const pi_kv_cache* cache, const pi_kv_batch* batch, const
     }
     if (e == hipSuccess)
         e = pi::launch_kv_attend(c, b, reinterpret_cast<const pi::h16*>(q), q_stride, n_head, scale, window,
-                                 reinterpret_cast<pi::h16*>(y), lse, data, s);
-    if (e != hipSuccess) return hip_fail(e, "pi_kv_attend");
+                                 reinterpret_cast<pi::h16*>(y), lse, data, draft, s);
+    if (e != hipSuccess) return hip_fail(e, name);
     // The next call, in another graph or in none, cannot rely on a captured
     // clear, nor on what the workspace held before the graph's replays.
     if (captured) ws_forget(ws);
     else ws_record(ws, key);
     return ok();
+}
+}  // namespace
+
+extern "C" {
+
+pi_status pi_kv_attend(const pi_kv_cache* cache, const pi_kv_batch* batch, const pi_half* q, int64_t q_stride,
+                       int n_head, float scale, int window, pi_half* y, float* lse, void* ws, size_t ws_bytes,
+                       void* stream) {
+    return run_attend(cache, batch, q, q_stride, n_head, scale, window, y, lse, nullptr, ws, ws_bytes, stream, "pi_kv_attend");
+}
+
+pi_status pi_kv_attend_tree(const pi_kv_cache* cache, const pi_kv_batch* batch, const pi_half* q, int64_t q_stride, int n_head,
+                            const pi_half* k, int64_t k_stride, const pi_half* v, int64_t v_stride, const uint64_t* mask,
+                            int words, const int32_t* pos, float scale, int window, pi_half* y, float* lse, void* ws,
+                            size_t ws_bytes, void* stream) {
+    const pi::KvDraft draft{reinterpret_cast<const pi::h16*>(k), reinterpret_cast<const pi::h16*>(v), k_stride, v_stride, mask,
+                            words, pos};
+    return run_attend(cache, batch, q, q_stride, n_head, scale, window, y, lse, &draft, ws, ws_bytes, stream, "pi_kv_attend_tree");
 }
 
 pi_status pi_kv_workspace_size(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d, size_t* bytes) {

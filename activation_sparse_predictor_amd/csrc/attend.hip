@@ -30,8 +30,6 @@
 // one sequence of 128 tokens.  The weights as a leading and a following fp16
 // half keep 22 bits where the products are free: the matrix cores are busy a
 // tenth of the time.
-#include <type_traits>
-
 #include "attend.hpp"
 #include "pi.h"
 
@@ -44,8 +42,9 @@ constexpr int kMinTiles = 4;   // tiles a piece of a whole context has at least
 constexpr int single_target(int kj, int waves) { return kj == 4 || waves == 8 ? 256 : 512; }
 
 // KJ: 64-dimension steps of a head; FULL: d is all of them; WAVES: of a workgroup.
-template <int FMT, int KJ, bool FULL, int WAVES>
-__device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) {
+template <int FMT, int KJ, bool FULL, int WAVES, class ARGS>
+__device__ __forceinline__ void attend_unit(const ARGS& A, const AttUnit& w) {
+    constexpr bool TREE = is_tree<ARGS>;
     constexpr int kAttWaves = WAVES, kAttThreads = WAVES * kWave, ROWS = kAttRows, DP = 64 * KJ, LD = DP + 4;
     extern __shared__ float lds[];   // while tiles are read: Gran [kSegGrans]; then the joins' arrays
     __shared__ int s_last;
@@ -80,8 +79,9 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     const int my_row = w.row_tile * ROWS + n16;
     const bool live = my_row < rows_all;
     const int my_tok = live ? my_row / group : 0, my_head = w.h * group + (live ? my_row - my_tok * group : 0);
-    const int pos = live ? first + my_tok : -1;
-    const int lo = A.window > 0 && pos - A.window + 1 > 0 ? pos - A.window + 1 : 0;
+    const int pos = !live ? -1 : TREE ? ctx - 1 : first + my_tok;   // the last cached token that the row attends to
+    int lo = A.window > 0 && pos - A.window + 1 > 0 ? pos - A.window + 1 : 0;
+    if constexpr (TREE) lo = live ? tree_from(A, ctx, w.q.row0 + my_tok) : 0;
     f16x8 qf[2 * KJ];
     {
         const h16* qr = A.q + (size_t)(w.q.row0 + my_tok) * A.q_stride + (size_t)my_head * d;
@@ -102,18 +102,55 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     const int row_a = w.row_tile * ROWS / group;
     int row_b = (w.row_tile * ROWS + ROWS - 1) / group;
     if (row_b >= w.q.n) row_b = w.q.n - 1;
-    const int free_to = first + row_a;                                                   // up to this one
-    const int free_from = A.window > 0 ? first + row_b - A.window + 1 : 0;               // from this one on
+    int free_to = first + row_a;                                                         // up to this one
+    int free_from = A.window > 0 ? first + row_b - A.window + 1 : 0;                     // from this one on
     // and outside these, none attends
-    const int any_to = first + row_b, any_from = A.window > 0 ? first + row_a - A.window + 1 : 0;
+    int any_to = first + row_b, any_from = A.window > 0 ? first + row_a - A.window + 1 : 0;
+    if constexpr (TREE) {
+        free_to = any_to = ctx - 1;
+        if (A.window > 0) free_from = __builtin_amdgcn_readfirstlane(max_lanes16(lo));
+        any_from = A.window > 0 ? ctx - A.window + 1 : 0;
+    }
 
     float M = kNone, l = 0.f;
     f32x4 O[4 * KJ];
 #pragma unroll
     for (int k = 0; k < 4 * KJ; ++k) O[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    for (int seg = w.t0; seg < w.t1; seg += kSegTiles) {
-        const int tiles = w.t1 - seg < kSegTiles ? w.t1 - seg : kSegTiles;
+    // Weights of a tile's scores S (times kx; -infinity where the row does not attend, which edge says may be) and their sum.
+    auto weigh = [&](f32x4 (&S)[4], bool edge, float kx, float lv, f16x8 (&ph)[2], f16x8 (&pl)[2]) __attribute__((always_inline)) {
+        float mx = S[0][0];
+#pragma unroll
+        for (int k = 1; k < 16; ++k) mx = fmaxf(mx, S[k / 4][k % 4]);
+        // a lane that attends to none of its keys adds nothing, whatever their page's scale is
+        const bool none = edge && mx == -__builtin_inff();
+        const float by = edge ? 1.f : kx;
+        mx = fmaf(mx, by, lv);
+        if (__ballot(mx > M + kSlack)) {
+            const float m = fmaxf(M, max_groups(mx)), f = exp2_fast(M - m);
+            l *= f;
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k) O[k] *= f;
+            M = m;
+        }
+        // the weights' leading and following halves: to 22 bits, at twice the output's products
+        const float c = none ? 0.f : lv - M + kLift, unscale = none ? 0.f : exp2_fast(-lv);
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float wt = exp2_fast(fmaf(S[k / 4][k % 4], by, c));
+            sum += wt;
+            const f16 hi = (f16)wt;
+            ph[k / 8][k % 8] = hi;
+            pl[k / 8][k % 8] = (f16)(wt - (float)hi);
+        }
+        l = fmaf(sum, unscale, l);
+    };
+
+    const int cached = (ctx + kTile - 1) / kTile;   // tiles before a drafted row's own
+    const int t1 = !TREE || w.t1 < cached ? w.t1 : cached > w.t0 ? cached : w.t0;
+    for (int seg = w.t0; seg < t1; seg += kSegTiles) {
+        const int tiles = t1 - seg < kSegTiles ? t1 - seg : kSegTiles;
         if (seg != w.t0) __syncthreads();   // the last segment's entries are no longer read
         att_lookup(A, w, d, seg * (kTile / kGran), tiles * (kTile / kGran), threadIdx.x, kAttThreads, grans);
         __syncthreads();
@@ -151,33 +188,8 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
                     S[k / 4][k % 4] = k >= lo - key0 && k <= pos - key0 ? x : -__builtin_inff();
                 }
             }
-            float mx = S[0][0];
-#pragma unroll
-            for (int k = 1; k < 16; ++k) mx = fmaxf(mx, S[k / 4][k % 4]);
-            // a lane that attends to none of its keys adds nothing, whatever their page's scale is
-            const bool none = edge && mx == -__builtin_inff();
-            const float by = edge ? 1.f : kx;
-            mx = fmaf(mx, by, lv);
-            if (__ballot(mx > M + kSlack)) {
-                const float m = fmaxf(M, max_groups(mx)), f = exp2_fast(M - m);
-                l *= f;
-#pragma unroll
-                for (int k = 0; k < 4 * KJ; ++k) O[k] *= f;
-                M = m;
-            }
-            // the weights' leading and following halves: to 22 bits, at twice the output's products
             f16x8 ph[2], pl[2];
-            const float c = none ? 0.f : lv - M + kLift, unscale = none ? 0.f : exp2_fast(-lv);
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float wt = exp2_fast(fmaf(S[k / 4][k % 4], by, c));
-                sum += wt;
-                const f16 hi = (f16)wt;
-                ph[k / 8][k % 8] = hi;
-                pl[k / 8][k % 8] = (f16)(wt - (float)hi);
-            }
-            l = fmaf(sum, unscale, l);
+            weigh(S, edge, kx, lv, ph, pl);
             if (FMT == 1 && (tile0 < any_from || tile0 + kTile - 1 > any_to)) {
 #pragma unroll
                 for (int k = 0; k < 4 * KJ; ++k)
@@ -193,6 +205,63 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
                 O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pl[1], O[k], 0, 0, 0);
             }
             if (next < tiles) load_v(e);
+        }
+    }
+
+    if constexpr (TREE) {
+        // The drafted rows: fp16 as they are, K and V of scale 1.  The piece's tiles
+        // go round the waves as the cached ones do, whose turn goes on here.
+        const int n = w.q.n, ahead = (w.t0 > cached ? w.t0 : cached) - w.t0;
+        for (int i = ahead + ((wave - ahead) & (kAttWaves - 1)); w.t0 + i < w.t1; i += kAttWaves) {
+            const int x = w.t0 + i - cached, tok0 = x * kTile;
+            const uint32_t mine = live ? (uint32_t)(tree_bits(A, w.q.row0 + my_tok, n, x) >> (kGran * g)) & 0xFFFFu : 0u;
+            f32x4 S[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int tok = tok0 + (n16 >> 2) * kGran + t * 4 + (n16 & 3);
+                const h16* p = A.tk + (size_t)(w.q.row0 + (tok < n ? tok : n - 1)) * A.tk_stride + (size_t)w.h * d + g * 16;
+                S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) {
+                    u32x4 a = {0u, 0u, 0u, 0u}, e = a;
+                    if (FULL || j * 4 + g < dc) {
+                        a = ld16(p + j * 64);
+                        e = ld16(p + j * 64 + 8);
+                    }
+                    S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), qf[2 * j], S[t], 0, 0, 0);
+                    S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, e), qf[2 * j + 1], S[t], 0, 0, 0);
+                }
+            }
+            const float kx = fabsf(A.scale2);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) S[k / 4][k % 4] = mine >> k & 1u ? S[k / 4][k % 4] * kx : -__builtin_inff();
+            f16x8 ph[2], pl[2];
+            weigh(S, true, kx, 0.f, ph, pl);
+            const h16* vt[kGran];   // this lane's granule: its tokens' rows
+#pragma unroll
+            for (int t = 0; t < kGran; ++t) {
+                const int tok = tok0 + g * kGran + t;
+                vt[t] = A.tv + (size_t)(w.q.row0 + (tok < n ? tok : n - 1)) * A.tv_stride + (size_t)w.h * d + n16;
+            }
+            uint32_t bad = 0u;
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k) {
+                if (!FULL && k >= dc) continue;
+                f16x8 a, b;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) a[t] = vt[t][k * 16], b[t] = vt[8 + t][k * 16];
+                u32x4 v[2] = {__builtin_bit_cast(u32x4, a), __builtin_bit_cast(u32x4, b)};
+                drop_nonfinite(v, bad);
+                a = __builtin_bit_cast(f16x8, v[0]), b = __builtin_bit_cast(f16x8, v[1]);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[0], O[k], 0, 0, 0);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, ph[1], O[k], 0, 0, 0);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[0], O[k], 0, 0, 0);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pl[1], O[k], 0, 0, 0);
+            }
+            if (__ballot(bad != 0u)) {
+                bad = or_lanes16(bad);
+                if (bad & mine) l = __builtin_nanf("");
+            }
         }
     }
 
@@ -231,8 +300,9 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
     auto emit = [&](int r, int i, f32x4 o) {
         const int gr = w.row_tile * ROWS + r, tok = gr / group, head = w.h * group + gr - tok * group;
         const size_t to = (size_t)(w.q.row0 + tok) * A.n_head + head;
-        const bool empty = first + tok < 0;
         const float sum = done[ROWS + r];
+        bool empty = first + tok < 0;
+        if constexpr (TREE) empty = sum == 0.f && !tree_sees(A, w.q, tok);
         // no weight at all although there are keys: every score was -infinity
         const float f = sum == 0.f ? __builtin_nanf("") : 1.f / sum;
         typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
@@ -336,17 +406,17 @@ __device__ __forceinline__ void attend_unit(const AttArgs& A, const AttUnit& w) 
 
 // A workgroup takes units until there are none: whatever the lengths on the
 // device say, every piece of every item runs, and the counters end at zero.
-template <int FMT, int KJ, bool FULL, int WAVES>
-__global__ __launch_bounds__(WAVES * kWave, KJ == 4 ? 1 : 2) void k_attend(AttArgs A) {
+template <int FMT, int KJ, bool FULL, int WAVES, class ARGS>
+__global__ __launch_bounds__(WAVES * kWave, KJ == 4 ? 1 : 2) void k_attend(ARGS A) {
     AttUnit w;
     w.h = blockIdx.x;
-    const int units = att_plan<kAttRows>(A, blockIdx.y, w);
+    const int units = att_plan<kAttRows, ARGS>(A, blockIdx.y, w);
     for (int u = blockIdx.y; u < units;) {
-        attend_unit<FMT, KJ, FULL, WAVES>(A, w);
+        attend_unit<FMT, KJ, FULL, WAVES, ARGS>(A, w);
         u += gridDim.y;
         if (u < units) {
             __syncthreads();   // the next unit uses the same shared memory
-            att_plan<kAttRows>(A, u, w);
+            att_plan<kAttRows, ARGS>(A, u, w);
         }
     }
 }
@@ -379,24 +449,26 @@ size_t kv_attend_bytes(int n_seq, int n_tok, int max_q, int n_head, int n_kv, in
     return kv_attend_zero_bytes() + rows * (64 * kj + 2) * 4;
 }
 
-template <int FMT, int KJ, bool FULL, int WAVES>
-static hipError_t launch_single(const AttArgs& A, hipStream_t s) {
+template <int FMT, int KJ, bool FULL, int WAVES, class ARGS>
+static hipError_t launch_single(const ARGS& A, hipStream_t s) {
     constexpr size_t joins = ((size_t)WAVES * (64 * KJ + 4 + 2) + 2) * kAttRows * 4, looks = kSegGrans * sizeof(Gran);
     constexpr size_t shm = joins > looks ? joins : looks;
     if (shm > 65536) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<FMT, KJ, FULL, WAVES>),
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend<FMT, KJ, FULL, WAVES, ARGS>),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);
         if (e != hipSuccess) return e;
     }
     // heads side by side: the row tiles that read one head's pages run on one
     // XCD where the heads are a multiple of 8, and share its L2
-    hipLaunchKernelGGL((k_attend<FMT, KJ, FULL, WAVES>), dim3(A.c.n_kv, att_grid(A, kAttRows)), dim3(WAVES * kWave), shm,
-                       s, A);
+    int drafted = 0;
+    if constexpr (is_tree<ARGS>) drafted = A.words;
+    hipLaunchKernelGGL((k_attend<FMT, KJ, FULL, WAVES, ARGS>), dim3(A.c.n_kv, att_grid(A, kAttRows, drafted)), dim3(WAVES * kWave),
+                       shm, s, A);
     return hipGetLastError();
 }
 
-template <int FMT>
-static hipError_t launch_singles(AttArgs A, hipStream_t s) {
+template <int FMT, class ARGS>
+static hipError_t launch_singles(ARGS A, hipStream_t s) {
     const int kj = att_kj(A.c.d);
     const bool full = A.c.d == 64 * kj;
     // Where all items run at once, one eight-wave workgroup a CU each: half as
@@ -411,30 +483,37 @@ static hipError_t launch_singles(AttArgs A, hipStream_t s) {
     const int waves = kj < 4 && att_most_row_tiles(A.b, A.group, kAttRows) * A.c.n_kv <= 256 ? 8 : 4;
     A.target = single_target(kj, waves);
     A.min_tiles = kMinTiles;
-    if (kj == 4) return full ? launch_single<FMT, 4, true, 4>(A, s) : launch_single<FMT, 4, false, 4>(A, s);
-    if (kj == 2 && waves == 8) return full ? launch_single<FMT, 2, true, 8>(A, s) : launch_single<FMT, 2, false, 8>(A, s);
-    if (kj == 2) return full ? launch_single<FMT, 2, true, 4>(A, s) : launch_single<FMT, 2, false, 4>(A, s);
-    if (waves == 8) return full ? launch_single<FMT, 1, true, 8>(A, s) : launch_single<FMT, 1, false, 8>(A, s);
-    return full ? launch_single<FMT, 1, true, 4>(A, s) : launch_single<FMT, 1, false, 4>(A, s);
+    if (kj == 4) return full ? launch_single<FMT, 4, true, 4, ARGS>(A, s) : launch_single<FMT, 4, false, 4, ARGS>(A, s);
+    if (kj == 2 && waves == 8) return full ? launch_single<FMT, 2, true, 8, ARGS>(A, s) : launch_single<FMT, 2, false, 8, ARGS>(A, s);
+    if (kj == 2) return full ? launch_single<FMT, 2, true, 4, ARGS>(A, s) : launch_single<FMT, 2, false, 4, ARGS>(A, s);
+    if (waves == 8) return full ? launch_single<FMT, 1, true, 8, ARGS>(A, s) : launch_single<FMT, 1, false, 8, ARGS>(A, s);
+    return full ? launch_single<FMT, 1, true, 4, ARGS>(A, s) : launch_single<FMT, 1, false, 4, ARGS>(A, s);
 }
 
-hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
-                            float scale, int window, h16* y, float* lse, char* data, hipStream_t s) {
-    const int group = n_head / c.n_kv;
-    if (window > 0x3FFFFFFF) window = 0;   // above any length (and positions less it would pass 32 bits)
-    AttArgs A{c, b, q, q_stride, n_head, group, window, 0, 0x7FFFFFFF, 0, 0, scale * 1.4426950408889634f, y, lse,
-              reinterpret_cast<uint32_t*>(data), reinterpret_cast<float*>(data + kv_attend_zero_bytes())};
-    if (uses_prompt(b, group, c.n_kv)) {
+template <class ARGS>
+static hipError_t launch_attend(ARGS A, hipStream_t s) {
+    const KvBatch& b = A.b;
+    if (uses_prompt(b, A.group, A.c.n_kv)) {
         // rows of long and short sequences: each kernel takes its own (they
         // share the workspace, one after the other)
         A.upto = kAttRows;
-        AttArgs P = A;
+        ARGS P = A;
         P.above = kAttRows;
         P.upto = 0x7FFFFFFF;
         const hipError_t e = launch_attend_prompt(P, s);
         if (e != hipSuccess || b.n_tok == (long long)b.n_seq * b.max_q) return e;   // no short ones
     }
-    return c.fmt == 0 ? launch_singles<0>(A, s) : launch_singles<1>(A, s);
+    return A.c.fmt == 0 ? launch_singles<0>(A, s) : launch_singles<1>(A, s);
+}
+
+hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
+                            float scale, int window, h16* y, float* lse, char* data, const KvDraft* draft, hipStream_t s) {
+    const int group = n_head / c.n_kv;
+    if (!draft && window > 0x3FFFFFFF) window = 0;   // above any length (and positions less it would pass 32 bits)
+    const AttArgs A{c, b, q, q_stride, n_head, group, window, 0, 0x7FFFFFFF, 0, 0, scale * 1.4426950408889634f, y, lse,
+                    reinterpret_cast<uint32_t*>(data), reinterpret_cast<float*>(data + kv_attend_zero_bytes())};
+    if (!draft) return launch_attend(A, s);
+    return launch_attend(TreeArgs{A, draft->k, draft->v, draft->k_stride, draft->v_stride, draft->mask, draft->words, draft->pos}, s);
 }
 
 }  // namespace pi

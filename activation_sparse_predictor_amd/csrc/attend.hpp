@@ -3,6 +3,8 @@
 // against hundreds of rows.
 #pragma once
 
+#include <type_traits>
+
 #include "kv.hpp"
 
 namespace pi {
@@ -44,6 +46,72 @@ struct AttArgs {
     float* part;
 };
 
+// Attention of drafted tokens (pi_kv_attend_tree): every row sees the cached
+// tokens, all ctx of them or, under a window, those above its own position less
+// the window, and the drafted rows that its mask names.  The drafted rows are
+// further tiles of 64 keys behind the cached ones.
+struct TreeArgs : AttArgs {
+    const h16 *tk, *tv;            // drafted keys and values: n_tok rows
+    long long tk_stride, tv_stride;
+    const uint64_t* mask;          // n_tok x words
+    int words;
+    const int32_t* pos;            // n_tok; only read under a window
+};
+constexpr int kMaxDrafted = 4;     // tiles of drafted rows (words)
+template <class ARGS> constexpr bool is_tree = std::is_same_v<ARGS, TreeArgs>;
+
+// Cached positions below this one are outside a drafted row's window.
+__device__ __forceinline__ int tree_from(const TreeArgs& A, int ctx, int row) {
+    if (A.window <= 0) return 0;
+    const int p = A.pos[row];
+    const int from = (p > ctx ? p : ctx) - A.window + 1;
+    return from > 0 ? from : 0;
+}
+// The drafted rows of tile x that row `row` of a sequence of n rows attends to, as bits.
+__device__ __forceinline__ uint64_t tree_bits(const TreeArgs& A, int row, int n, int x) {
+    if (x >= A.words) return 0ull;
+    const uint64_t m = A.mask[(size_t)row * A.words + x];
+    const int have = n - x * kTile;
+    return have >= kTile ? m : have <= 0 ? 0ull : m & ((1ull << have) - 1);
+}
+// Whether a drafted row attends to anything.
+__device__ __forceinline__ bool tree_sees(const TreeArgs& A, const Seq& q, int tok) {
+    if (tree_from(A, q.ctx, q.row0 + tok) < q.ctx) return true;
+    for (int x = 0; x < A.words; ++x)
+        if (tree_bits(A, q.row0 + tok, q.n, x)) return true;
+    return false;
+}
+// A drafted token's value that is not finite would reach, times a weight of 0,
+// rows that do not attend to it.  It is taken as 0, and the token's bit goes
+// into `bad`, which makes the sums of the rows that do attend to it NaN.
+// v: a dimension's 16 tokens.
+__device__ __forceinline__ void drop_nonfinite(u32x4 (&v)[2], uint32_t& bad) {
+    uint32_t any = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) any |= ((v[i / 4][i % 4] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+    if (!__ballot(any != 0u)) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t x = v[i / 4][i % 4], top = ((x & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+        bad |= ((top >> 15 & 1u) | (top >> 30 & 2u)) << (2 * i);
+        v[i / 4][i % 4] = x & ~((top >> 15) * 0xFFFFu);
+    }
+}
+// Over the 16 lanes of one g: bits that any has, and the largest.
+__device__ __forceinline__ uint32_t or_lanes16(uint32_t v) {
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) v |= __shfl_xor(v, m, kWave);
+    return v;
+}
+__device__ __forceinline__ int max_lanes16(int v) {
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) {
+        const int o = __shfl_xor(v, m, kWave);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
 // What a workgroup works on: a row tile of a sequence, its keys' tiles
 // [t0, t1), head h; piece `split` of `splits`, whose first has slot `slot`.
 struct AttUnit {
@@ -52,18 +120,25 @@ struct AttUnit {
 };
 
 // First tile of a sequence that any of its rows attends to, and the tiles in all (at least one).
+template <bool TREE>
 __device__ __forceinline__ int att_first_tile(const Seq& q, int window) {
-    const int lo = q.ctx - q.n - window + 1;
+    const int lo = q.ctx - (TREE ? 0 : q.n) - window + 1;
     return window > 0 && lo > 0 ? lo / kTile : 0;
 }
+template <bool TREE>
 __device__ __forceinline__ int att_tiles(const Seq& q, int window) {
-    const int n = (q.ctx + kTile - 1) / kTile - att_first_tile(q, window);
+    const int n = (q.ctx + kTile - 1) / kTile - att_first_tile<TREE>(q, window);
+    if (TREE) return n + (q.n + kTile - 1) / kTile;
     return n > 0 ? n : 1;
 }
 
 // The tiles that rows [row_tile * ROWS, + ROWS) attend to: the first, and how many.
-template <int ROWS>
-__device__ __forceinline__ int att_row_tiles(const AttArgs& A, const Seq& q, int row_tile, int& first_tile) {
+template <int ROWS, class ARGS>
+__device__ __forceinline__ int att_row_tiles(const ARGS& A, const Seq& q, int row_tile, int& first_tile) {
+    if constexpr (is_tree<ARGS>) {
+        first_tile = att_first_tile<true>(q, A.window);
+        return att_tiles<true>(q, A.window);
+    }
     const int a = row_tile * ROWS / A.group;
     int b = (row_tile * ROWS + ROWS - 1) / A.group;
     b = b < q.n ? b : q.n - 1;
@@ -90,8 +165,9 @@ __host__ __device__ constexpr int att_piece(float want, int min_tiles) {
 // round of 64 sequences is one round of loads.  Fills in unit `item`, if there
 // is one, and returns how many there are (of each head).  With at most 2^24
 // rows and 2^10 sequences, whatever the lengths say, the sums stay below 2^31.
-template <int ROWS>
-__device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) {
+template <int ROWS, class ARGS>
+__device__ __forceinline__ int att_plan(const ARGS& A, int item, AttUnit& w) {
+    constexpr bool TREE = is_tree<ARGS>;
     const KvBatch& b = A.b;
     auto row_tiles = [&](const Seq& q) {
         const int rows = q.n * A.group;
@@ -106,7 +182,7 @@ __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) 
         if (s < b.n_seq) {
             q = kv_seq(b, s);
             rt = row_tiles(q);
-            tiles = att_tiles(q, A.window);
+            tiles = att_tiles<TREE>(q, A.window);
         }
         all += group_sum<64>((float)rt * (float)tiles);
         items += group_sum<64>((float)rt);
@@ -129,7 +205,7 @@ __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) 
             if (s < b.n_seq) {
                 q = kv_seq(b, s);
                 rt = row_tiles(q);
-                tiles = att_tiles(q, A.window);
+                tiles = att_tiles<TREE>(q, A.window);
             }
         }
         const int ns = (tiles + C - 1) / C;
@@ -151,7 +227,7 @@ __device__ __forceinline__ int att_plan(const AttArgs& A, int item, AttUnit& w) 
             w.slot = __builtin_amdgcn_readlane(slots_upto, l) - __builtin_amdgcn_readlane(held, l) +
                      behind * w.splits;   // the item's first slot
             int f;
-            const int T = att_row_tiles<ROWS>(A, w.q, w.row_tile, f);
+            const int T = att_row_tiles<ROWS, ARGS>(A, w.q, w.row_tile, f);
             const int each = T / w.splits, more = T - each * w.splits;
             w.t0 = f + w.split * each + (w.split < more ? w.split : more);
             w.t1 = w.t0 + each + (w.split < more ? 1 : 0);
@@ -237,9 +313,9 @@ inline long long att_most_row_tiles(const KvBatch& b, int group, int rows) {
     return each < all ? each : all;
 }
 // Units of one head that the plan can come to (more would be taken in turn).
-inline unsigned att_grid(const AttArgs& A, int rows) {
+inline unsigned att_grid(const AttArgs& A, int rows, int drafted_tiles = 0) {
     const long long items = att_most_row_tiles(A.b, A.group, rows);
-    const long long cap = ((long long)A.b.table_stride * A.c.page + kTile - 1) / kTile;
+    const long long cap = ((long long)A.b.table_stride * A.c.page + kTile - 1) / kTile + drafted_tiles;
     const long long most = items * ((cap + A.min_tiles - 1) / A.min_tiles);
     long long units = items + (A.target + A.c.n_kv - 1) / A.c.n_kv;
     if (units > most) units = most;
@@ -252,5 +328,6 @@ __host__ __device__ constexpr int att_kj(int d) { return d <= 64 ? 1 : d <= 128 
 // prompt.hip
 constexpr int prompt_rows(int kj) { return kj == 4 ? 64 : 128; }
 hipError_t launch_attend_prompt(AttArgs A, hipStream_t s);
+hipError_t launch_attend_prompt(TreeArgs A, hipStream_t s);
 
 }  // namespace pi

@@ -327,8 +327,16 @@ hipError_t launch_kv_read(const KvCache& c, const KvBatch& b, h16* k, h16* v, hi
 // attend.hip
 size_t kv_attend_bytes(int n_seq, int n_tok, int max_q, int n_head, int n_kv, int d);
 size_t kv_attend_zero_bytes();   // at the data area's start: counters, all zero between calls
-hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head,
-                            float scale, int window, h16* y, float* lse, char* data, hipStream_t s);
+struct KvDraft {   // pi_kv_attend_tree's drafted rows
+    const h16 *k, *v;
+    long long k_stride, v_stride;
+    const uint64_t* mask;
+    int words;
+    const int32_t* pos;
+};
+// draft NULL: pi_kv_attend
+hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, long long q_stride, int n_head, float scale,
+                            int window, h16* y, float* lse, char* data, const KvDraft* draft, hipStream_t s);
 
 // verify.hip
 struct VerifyArgs {

@@ -50,8 +50,9 @@ __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(
 // Two numbers as fp16, rounded towards zero.
 __device__ __forceinline__ f16x2 cut2(float a, float b) { return __builtin_bit_cast(f16x2, __builtin_amdgcn_cvt_pkrtz(a, b)); }
 
-template <int FMT, int KJ, bool FULL>
-__device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) {
+template <int FMT, int KJ, bool FULL, class ARGS>
+__device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
+    constexpr bool TREE = is_tree<ARGS>;
     static_assert(kProWaves == 4 && kProWaves % KJ == 0, "a thread's pieces");
     constexpr int NT = KJ == 4 ? 1 : 2, ROWS = kProWaves * 16 * NT, DP = 64 * KJ;
     static_assert(ROWS == prompt_rows(KJ), "rows of a workgroup");
@@ -59,6 +60,7 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     extern __shared__ u32x4 frags[];  // [2][kFrags][64]
     __shared__ Gran grans[kProRing * (kTile / kGran)];
     __shared__ int s_last, s_written;
+    __shared__ uint32_t s_bad[TREE ? kMaxDrafted : 1][kTile / kGran];   // drafted tokens whose values are not finite
     // (settled, so that what follows from them is not kept in registers from
     // unit to unit)
     const int lane = settle(lane_id()), wave = __builtin_amdgcn_readfirstlane(settle((int)threadIdx.x) / kWave);
@@ -66,6 +68,8 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     const int d = FULL ? DP : A.c.d, dc = d / 16, group = A.group;
     const int first = w.q.ctx - w.q.n, rows_all = w.q.n * group;
     const int n = w.t1 - w.t0;
+    // tiles of the piece that the cache holds; drafted rows are the others
+    const int cached = (w.q.ctx + kTile - 1) / kTile, nc = !TREE || w.t1 <= cached ? n : cached > w.t0 ? cached - w.t0 : 0;
 
     auto fill = [&](int x, int count) {   // tiles [x, x + count) of this unit, into their places of the ring
         att_lookup(A, w, d, (w.t0 + x) * (kTile / kGran), count * (kTile / kGran), threadIdx.x, kProThreads,
@@ -78,12 +82,18 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         return t < w.q.n ? t : w.q.n - 1;
     };
     const int row_w = w.row_tile * ROWS, row_v = row_w + wave * 16 * NT;
-    const int any_to = first + last_tok(row_w + ROWS - 1);
-    const int any_from = A.window > 0 ? first + row_w / group - A.window + 1 : 0;
+    int any_to = first + last_tok(row_w + ROWS - 1);
+    int any_from = A.window > 0 ? first + row_w / group - A.window + 1 : 0;
     const bool idle = row_v >= rows_all;
-    const int v_to = idle ? -1 : first + last_tok(row_v + 16 * NT - 1), v_free_to = first + row_v / group;
-    const int v_from = A.window > 0 ? first + row_v / group - A.window + 1 : 0;
-    const int v_free_from = A.window > 0 ? v_to - A.window + 1 : 0;
+    int v_to = idle ? -1 : first + last_tok(row_v + 16 * NT - 1), v_free_to = first + row_v / group;
+    int v_from = A.window > 0 ? first + row_v / group - A.window + 1 : 0;
+    int v_free_from = A.window > 0 ? v_to - A.window + 1 : 0;
+    if constexpr (TREE) {
+        any_to = v_free_to = w.q.ctx - 1;
+        v_to = idle ? -1 : w.q.ctx - 1;
+        any_from = v_from = A.window > 0 ? w.q.ctx - A.window + 1 : 0;
+        v_free_from = 0;
+    }
     int pos[NT], lo[NT];
     f16x8 qf[NT][2 * KJ];
     const uint32_t sign = A.scale2 < 0.f ? 0x80008000u : 0u;
@@ -92,8 +102,13 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         const int r = row_v + nt * 16 + n16;
         const bool live = r < rows_all;
         const int tok = live ? r / group : 0, head = w.h * group + (live ? r - tok * group : 0);
-        pos[nt] = live ? first + tok : -1;
+        pos[nt] = !live ? -1 : TREE ? w.q.ctx - 1 : first + tok;
         lo[nt] = A.window > 0 && pos[nt] - A.window + 1 > 0 ? pos[nt] - A.window + 1 : 0;
+        if constexpr (TREE) {
+            lo[nt] = live ? tree_from(A, w.q.ctx, w.q.row0 + tok) : 0;
+            const int most = A.window > 0 ? __builtin_amdgcn_readfirstlane(max_lanes16(lo[nt])) : 0;
+            v_free_from = most > v_free_from ? most : v_free_from;
+        }
         const h16* qr = A.q + (size_t)(w.q.row0 + tok) * A.q_stride + (size_t)head * d;
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
@@ -139,6 +154,46 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         to[(i * 2 * kProWaves + 1) * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(v.z, v.w));
     };
 
+    // Tile x, drafted: fp16 rows as they are, straight into the fragments' places.
+    auto stage_drafted = [&](int x) __attribute__((always_inline)) {
+        if constexpr (TREE) {
+            const int tile = w.t0 + x - cached, tok0 = tile * kTile, rows = w.q.n;
+            u32x4* to = frags + ((x & 1) * kFrags + 2 * wave) * 64 + lane;
+            auto row = [&](int tok) { return (size_t)(w.q.row0 + (tok < rows ? tok : rows - 1)); };
+            const u32x4 zero = {0u, 0u, 0u, 0u};
+            u32x4 kv[2 * KJ];
+#pragma unroll
+            for (int i = 0; i < KJ; ++i) {
+                const int t = wave / KJ + i * (kProWaves / KJ), ch = wave % KJ * 4 + g;
+                const h16* p = A.tk + row(tok0 + (n16 >> 2) * kGran + t * 4 + (n16 & 3)) * A.tk_stride + (size_t)w.h * d + ch * 16;
+                kv[2 * i] = kv[2 * i + 1] = zero;
+                if (FULL || ch < dc) kv[2 * i] = ld16(p), kv[2 * i + 1] = ld16(p + 8);
+            }
+            f16x8 v[2 * KJ];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const h16* p = A.tv + row(tok0 + g * kGran + t) * A.tv_stride + (size_t)w.h * d + wave * 16 + n16;
+                const h16* q = A.tv + row(tok0 + g * kGran + 8 + t) * A.tv_stride + (size_t)w.h * d + wave * 16 + n16;
+#pragma unroll
+                for (int i = 0; i < KJ; ++i) {
+                    v[2 * i][t] = v[2 * i + 1][t] = (f16)0.f;
+                    if (FULL || wave + 4 * i < dc) v[2 * i][t] = p[i * kProWaves * 16], v[2 * i + 1][t] = q[i * kProWaves * 16];
+                }
+            }
+            uint32_t bad = 0u;
+#pragma unroll
+            for (int i = 0; i < KJ; ++i) {
+                to[i * 2 * kProWaves * 64] = kv[2 * i];
+                to[(i * 2 * kProWaves + 1) * 64] = kv[2 * i + 1];
+                u32x4 f[2] = {__builtin_bit_cast(u32x4, v[2 * i]), __builtin_bit_cast(u32x4, v[2 * i + 1])};
+                drop_nonfinite(f, bad);
+                to[(KJ + i) * 2 * kProWaves * 64] = f[0];
+                to[((KJ + i) * 2 * kProWaves + 1) * 64] = f[1];
+            }
+            if (bad) atomicOr(&s_bad[tile & (kMaxDrafted - 1)][g], bad);
+        }
+    };
+
     const float minus = settle(-1.f);   // (a constant would turn the differences below into a conversion and a subtraction each)
     float M[NT], l[NT];
     f32x4 O[NT][4 * KJ];
@@ -151,12 +206,19 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     }
 
     if (n > 0) {
-        fill(0, n < kProSeg ? n : kProSeg);
+        if constexpr (TREE) {
+            if (threadIdx.x < kMaxDrafted * (kTile / kGran)) (&s_bad[0][0])[threadIdx.x] = 0u;
+        }
+        fill(0, nc < kProSeg ? nc : kProSeg);
         __syncthreads();
-        load(0);
+        if (!TREE || nc > 0) {
+            load(0);
 #pragma unroll
-        for (int i = 0; i < 2 * KJ; ++i) store(0, i);
-        if (n > 1) load(1);
+            for (int i = 0; i < 2 * KJ; ++i) store(0, i);
+        } else {
+            stage_drafted(0);
+        }
+        if (nc > 1) load(1);
         lds_barrier();
     }
     for (int x = 0; x < n; ++x) {
@@ -169,19 +231,34 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
             case 2: __builtin_amdgcn_s_setprio(1); break;
             default: __builtin_amdgcn_s_setprio(0);
         }
-        if (x % kProSeg == 0 && x + kProSeg < n) {   // the next segment, in the half of the ring that is done with
-            const int left = n - x - kProSeg;
+        if (x % kProSeg == 0 && x + kProSeg < nc) {   // the next segment, in the half of the ring that is done with
+            const int left = nc - x - kProSeg;
             fill(x + kProSeg, left < kProSeg ? left : kProSeg);
         }
-        if (x + 1 < n) {
+        if (x + 1 < nc) {
 #pragma unroll
             for (int i = 0; i < 2 * KJ; ++i) store(x + 1, i);
+        } else if (TREE && x + 1 < n) {
+            stage_drafted(x + 1);
         }
-        if (x + 2 < n) load(x + 2);
+        if (x + 2 < nc) load(x + 2);
         const int tile0 = (w.t0 + x) * kTile;
-        if (tile0 <= v_to && tile0 + kTile - 1 >= v_from) {
+        const bool drafted = TREE && x >= nc;
+        if (drafted ? !idle : tile0 <= v_to && tile0 + kTile - 1 >= v_from) {
             const Gran* gr = &grans[(x & (kProRing - 1)) * (kTile / kGran)];
-            const float kx = gr[g].kx, lv = gr[g].lv;
+            float kx = gr[g].kx, lv = gr[g].lv;
+            uint32_t mine[NT], broken = 0u;   // drafted tokens of granule g: those that the row attends to, and those whose values are not finite
+            if constexpr (TREE) {
+                if (drafted) {
+                    kx = fabsf(A.scale2), lv = 0.f;
+                    broken = s_bad[(w.t0 + x - cached) & (kMaxDrafted - 1)][g];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int r = row_v + nt * 16 + n16;
+                        mine[nt] = r < rows_all ? (uint32_t)(tree_bits(A, w.q.row0 + r / group, w.q.n, w.t0 + x - cached) >> (kGran * g)) & 0xFFFFu : 0u;
+                    }
+                }
+            }
             const u32x4* kf = frags + (x & 1) * kFrags * 64 + lane;
             // Fragments are read a group of products ahead (the compiler alone reads one and waits for it).
             f32x4 S[NT][4];
@@ -210,11 +287,17 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
             for (int k = 0; k < 4; ++k) va[0][k] = __builtin_bit_cast(f16x8, vf[k * 64]);
             __builtin_amdgcn_sched_barrier(0);
             const int key0 = tile0 + g * kGran;
-            const bool edge = tile0 < v_free_from || tile0 + kTile - 1 > v_free_to;
+            const bool edge = drafted || tile0 < v_free_from || tile0 + kTile - 1 > v_free_to;
             f16x8 ph[NT][2], pl[NT][2];   // the weights' leading and following halves
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                if (edge) {
+                if (drafted) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float v = S[nt][k / 4][k % 4] * kx;
+                        S[nt][k / 4][k % 4] = mine[nt] >> k & 1u ? v : -__builtin_inff();
+                    }
+                } else if (edge) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const float v = S[nt][k / 4][k % 4] * kx;
@@ -249,6 +332,7 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
                     pl[nt][k / 8][k % 8] = more.x, pl[nt][k / 8][k % 8 + 1] = more.y;
                 }
                 l[nt] = fmaf(sum, unscale, l[nt]);
+                if (drafted && (broken & mine[nt])) l[nt] = __builtin_nanf("");
             }
 #pragma unroll
             for (int k = 0; k < 2 * KJ; ++k) {   // two 16-dimension tiles at a time
@@ -374,7 +458,8 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
         if (row >= rows_all) continue;
         const int tok = row / group, head = w.h * group + row - tok * group;
         const size_t to = (size_t)(w.q.row0 + tok) * A.n_head + head;
-        const bool empty = first + tok < 0;
+        bool empty = first + tok < 0;
+        if constexpr (TREE) empty = l[nt] == 0.f && !tree_sees(A, w.q, tok);
         // no weight at all although there are keys: every score was -infinity
         const float f = l[nt] == 0.f ? __builtin_nanf("") : 1.f / l[nt];
 #pragma unroll
@@ -389,36 +474,39 @@ __device__ __forceinline__ void prompt_unit(const AttArgs& A, const AttUnit& w) 
     }
 }
 
-template <int FMT, int KJ, bool FULL>
-__global__ __launch_bounds__(kProThreads, 2) void k_attend_prompt(AttArgs A) {
+template <int FMT, int KJ, bool FULL, class ARGS>
+__global__ __launch_bounds__(kProThreads, 2) void k_attend_prompt(ARGS A) {
     constexpr int ROWS = prompt_rows(KJ);
     AttUnit w;
     w.h = blockIdx.x;
-    const int units = att_plan<ROWS>(A, blockIdx.y, w);
+    const int units = att_plan<ROWS, ARGS>(A, blockIdx.y, w);
     for (int u = blockIdx.y; u < units;) {
-        prompt_unit<FMT, KJ, FULL>(A, w);
+        prompt_unit<FMT, KJ, FULL, ARGS>(A, w);
         u += gridDim.y;
         if (u < units) {
             __syncthreads();   // the next unit uses the same shared memory
-            att_plan<ROWS>(A, u, w);
+            att_plan<ROWS, ARGS>(A, u, w);
         }
     }
 }
 
-hipError_t launch_attend_prompt(AttArgs A, hipStream_t s) {
+template <class ARGS>
+static hipError_t launch(ARGS A, hipStream_t s) {
     const int kj = att_kj(A.c.d);
     A.target = pro_target(kj);
     A.min_tiles = kProMinTiles;
-    const dim3 grid(A.c.n_kv, att_grid(A, prompt_rows(kj)));
+    int drafted = 0;
+    if constexpr (is_tree<ARGS>) drafted = A.words;
+    const dim3 grid(A.c.n_kv, att_grid(A, prompt_rows(kj), drafted));
     const size_t shm = (size_t)2 * 16 * kj * 1024;
     const bool full = A.c.d == 64 * kj;
     hipError_t e = hipSuccess;
 #define PI_PRO(F, K, U)                                                                                   \
     do {                                                                                                  \
         if (shm + 16384 > 65536)                                                                          \
-            e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_prompt<F, K, U>),             \
+            e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_attend_prompt<F, K, U, ARGS>),       \
                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);                \
-        if (e == hipSuccess) hipLaunchKernelGGL((k_attend_prompt<F, K, U>), grid, dim3(kProThreads), shm, s, A); \
+        if (e == hipSuccess) hipLaunchKernelGGL((k_attend_prompt<F, K, U, ARGS>), grid, dim3(kProThreads), shm, s, A); \
     } while (0)
 #define PI_PRO_D(F)                                                          \
     if (kj == 1) { if (full) PI_PRO(F, 1, true); else PI_PRO(F, 1, false); }  \
@@ -430,5 +518,7 @@ hipError_t launch_attend_prompt(AttArgs A, hipStream_t s) {
     if (e != hipSuccess) return e;
     return hipGetLastError();
 }
+hipError_t launch_attend_prompt(AttArgs A, hipStream_t s) { return launch(A, s); }
+hipError_t launch_attend_prompt(TreeArgs A, hipStream_t s) { return launch(A, s); }
 
 }  // namespace pi

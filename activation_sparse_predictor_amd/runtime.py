@@ -448,31 +448,97 @@ def kv_attend(cache: dict, q: torch.Tensor, batch: dict, y: Optional[torch.Tenso
               and lse.get_device() == dev, "lse must be n_tok x n_head floats")
     st = _raw_stream(dev)
     scale = d ** -0.5 if scale is None else float(scale)
-    window = min(max(int(window), -1), 2 ** 31 - 1)   # (ctypes would drop what lies above 32 bits)
+    window = _window(window)
+    _attend_with(lambda ws, size: B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, ws, size, st), b, heads, c.n_kv, d, q.device,
+                 st, ws, "pi_kv_attend")
+    return y
+
+
+def _window(window) -> int:
+    return min(max(int(window), -1), 2 ** 31 - 1)   # (ctypes would drop what lies above 32 bits)
+
+
+def _attend_with(call, b, heads: int, n_kv: int, d: int, device, st: int, ws: Optional[torch.Tensor], name: str) -> None:
+    """call(workspace, bytes) on the caller's workspace or on one of this module's."""
     if ws is not None:
-        _need(ws.get_device() == dev and ws.is_contiguous(), "ws must be contiguous and on q's device")
-        size = ws.numel() * ws.element_size()
-        B.check(B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, ws, size, st), "pi_kv_attend")
-        return y
+        _need(ws.device == device and ws.is_contiguous(), "ws must be contiguous and on q's device")
+        B.check(call(ws, ws.numel() * ws.element_size()), name)
+        return
     if _capturing():
         # A graph's workspace is its alone: what other captures or eager calls on
         # this stream do is not replayed with it, and a kept buffer may be
         # replaced by a larger one.  The capture's pool holds the memory as long
         # as the graph lives and gives it to later allocations of the capture.
-        size = B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, d)
-        ws = torch.empty(size, dtype=_U8, device=q.device)
+        size = B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, n_kv, d)
+        ws = torch.empty(size, dtype=_U8, device=device)
         ws[:B.PI_KV_WS_ZERO_BYTES].zero_()
-        B.check(B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, ws, size, st), "pi_kv_attend")
-        return y
-    own = _KV_WS.get((dev, st))
+        B.check(call(ws, size), name)
+        return
+    key = (device.index, st)
+    own = _KV_WS.get(key)
     if own is None:
-        own = _KV_WS[(dev, st)] = Workspace(q.device)
-    size = 0 if own.buf is None else own.buf.numel()
-    status = B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, own.buf, size, st)
+        own = _KV_WS[key] = Workspace(device)
+    status = call(own.buf, 0 if own.buf is None else own.buf.numel())
     if status == B.PI_ERR_WORKSPACE:   # too small for these sizes: nothing was launched
-        buf, size = own.get(B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, d))
-        status = B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, buf, size, st)
-    B.check(status, "pi_kv_attend")
+        status = call(*own.get(B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, n_kv, d)))
+    B.check(status, name)
+
+
+def kv_tree(parents, device="cuda") -> dict:
+    """From host lists, parents[s][j] the parent of row j of sequence s (-1: none; it
+    lies before j): mask (n_tok x words int64, the bits of the C ABI's uint64), each row
+    its ancestors and itself, parent and depth (n_tok int32)."""
+    most = max(len(seq) for seq in parents)
+    words = max(1, (most + 63) // 64)
+    masks, depths = [], []
+    for seq in parents:
+        mine, depth = [], []
+        for j, p in enumerate(seq):
+            _need(-1 <= p < j, "a parent lies before its children")
+            mine.append((mine[p] if p >= 0 else 0) | 1 << j)
+            depth.append(depth[p] + 1 if p >= 0 else 0)
+        masks += [[(m >> 64 * w & (1 << 64) - 1) - (m >> 64 * w + 63 & 1) * (1 << 64) for w in range(words)] for m in mine]
+        depths += depth
+    return {"mask": torch.tensor(masks, dtype=torch.int64, device=device),
+            "parent": torch.tensor([p for seq in parents for p in seq], dtype=_I32, device=device),
+            "depth": torch.tensor(depths, dtype=_I32, device=device)}
+
+
+def kv_attend_tree(cache: dict, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, batch: dict, mask: torch.Tensor,
+                   pos: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                   window: int = 0, lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """pi_kv_attend_tree: attention of drafted tokens, q (n_tok x n_head x d fp16),
+    over the cache, whose lengths the batch's ctx are, and over each other, k and
+    v (n_tok x n_kv x d fp16), as mask says (n_tok x words int64, kv_tree's).
+    pos (n_tok int32) is needed under a window.  scale, y, lse and ws as kv_attend's."""
+    dev = q.get_device()
+    if _is_elsewhere(stream, dev):
+        return _elsewhere(stream, q.device, (q, k, v, mask, pos, y, lse, ws, *cache.values(), *batch.values()),
+                          lambda: kv_attend_tree(cache, q, k, v, batch, mask, pos, y, scale, window, lse, ws))
+    c, b = _kv_args(cache, batch, dev)
+    d = c.d
+    qs = _kv_rows(q, b.n_tok, None, d, "q")
+    ks = _kv_rows(k, b.n_tok, c.n_kv, d, "k")
+    vs = _kv_rows(v, b.n_tok, c.n_kv, d, "v")
+    heads = q.shape[1]
+    if not (mask.dtype is torch.int64 and mask.dim() == 2 and mask.shape[0] == b.n_tok and mask.is_contiguous()
+            and k.get_device() == v.get_device() == mask.get_device() == dev
+            and (pos is None or (pos.dtype is _I32 and pos.shape == (b.n_tok,) and pos.is_contiguous() and pos.get_device() == dev))):
+        raise ValueError("mask is n_tok x words int64, pos n_tok int32; k, v, mask and pos on q's device")
+    if y is None:
+        y = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _kv_rows(y, b.n_tok, heads, d, "y", stride=False)
+        _need(y.get_device() == dev, "y must be on q's device")
+    if lse is not None:
+        _need(lse.shape == (b.n_tok, heads) and lse.dtype is _F32 and lse.is_contiguous()
+              and lse.get_device() == dev, "lse must be n_tok x n_head floats")
+    st = _raw_stream(dev)
+    scale = d ** -0.5 if scale is None else float(scale)
+    window = _window(window)
+    _attend_with(lambda ws, size: B.pi_kv_attend_tree(c, b, q, qs, heads, k, ks, v, vs, mask, mask.shape[1], pos, scale, window, y, lse,
+                                                      ws, size, st), b, heads, c.n_kv, d, q.device, st, ws, "pi_kv_attend_tree")
     return y
 
 

@@ -690,6 +690,35 @@ pi_status pi_kv_append_rope(const pi_kv_cache* cache, const pi_kv_batch* batch, 
  * taken back: a block's scale only grows, so such a token would have cost its
  * neighbours precision for good.
  *
+ * pi_kv_attend_tree -- attention of drafted tokens over the cache and each other.
+ *
+ * The batch's rows q_start[s] .. q_start[s + 1] - 1 are sequence s's drafted
+ * tokens; unlike in pi_kv_attend they are not part of the cache, and ctx[s]
+ * counts the cached tokens alone.  q, n_head, scale, y, lse, ws as there; k
+ * and v: n_tok rows of n_kv heads of d (heads contiguous, k_stride and v_stride apart),
+ * turned already where the model turns them.  Row i of a sequence attends to
+ *  - the cached tokens at positions j < ctx[s]; under a window (> 0) those with j >
+ *    max(pos[i], ctx[s]) - window, pos (device, n_tok) its position: ctx[s] plus its
+ *    depth.  Without a window pos may be NULL;
+ *  - the drafted tokens j < n whose bit j % 64 of word j / 64 of its mask is
+ *    set (device, n_tok x words 64-bit words; usually its ancestors and itself).
+ * Both together under one softmax, in pi_kv_attend's precision; a row that
+ * attends to nothing gets y = 0, lse = -infinity.  Drafted tokens that a row does
+ * not attend to may hold anything, NaN included; a drafted value that is not
+ * finite makes the whole heads that attend to its token NaN.  max_q is at most 64 words.
+ *
+ * Errors: as pi_kv_attend; INVALID_ARG for words outside [1, PI_KV_MAX_TREE /
+ * 64], max_q above 64 words, k, v or mask NULL, pos NULL under a window;
+ * UNSUPPORTED for misalignment (k, v 16 bytes, mask 8, pos 4).
+ */
+#define PI_KV_MAX_TREE 256
+pi_status pi_kv_attend_tree(const pi_kv_cache* cache, const pi_kv_batch* batch,
+                            const pi_half* q, int64_t q_stride, int n_head,
+                            const pi_half* k, int64_t k_stride, const pi_half* v, int64_t v_stride,
+                            const uint64_t* mask, int words, const int32_t* pos, float scale, int window,
+                            pi_half* y, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * pi_verify -- which drafted tokens stay, and the token after them.
  *
  * Sequence s has rows q_start[s] .. q_start[s + 1] - 1 of tokens, parent, u, p and q

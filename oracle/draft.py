@@ -128,7 +128,7 @@ def attend_tree(cache, batch, q, k, v, mask, scale, window=0, pos=None):
         else:
             ck = cv = np.zeros((0, n_kv, d))
         for row in range(start[s], start[s + 1]):
-            lo = min(c, max(0, int(pos[row]) - window + 1)) if window else 0
+            lo = min(c, max(0, max(int(pos[row]), c) - window + 1)) if window else 0
             take = [start[s] + j for j in bits(mask[row], start[s + 1] - start[s])]
             kk = np.concatenate([ck[lo:], k[take].astype(np.float64)]).transpose(1, 0, 2)
             vv = np.concatenate([cv[lo:], v[take].astype(np.float64)]).transpose(1, 0, 2)

@@ -115,6 +115,41 @@ def test_append_rope_refuses_what_append_refuses():
     assert B.pi_kv_append_rope(cache(), batch(), None, None, 3, A, 128, A, 128, A, 512, 8, FAR, 512, 0) == BAD
 
 
+def tree(c=None, b=None, **kw):
+    a = dict(q=A, q_stride=512, n_head=8, k=A, k_stride=128, v=A, v_stride=128, mask=A, words=1, pos=None, scale=0.1, window=0, y=A,
+             lse=None, ws=A, ws_bytes=1 << 40)
+    a.update(kw)
+    return B.pi_kv_attend_tree(c or cache(), b or batch(), *a.values(), 0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(y=None), BAD), (dict(mask=None), BAD), (dict(mask=A + 4), UNSUP),
+    (dict(words=0), BAD), (dict(words=5), BAD), (dict(window=3), BAD), (dict(window=3, pos=A + 2), UNSUP), (dict(pos=A + 2), UNSUP),
+    (dict(window=-1), BAD), (dict(k=A + 8), UNSUP), (dict(v=A + 2), UNSUP), (dict(k_stride=120), BAD), (dict(v_stride=132), UNSUP),
+    (dict(n_head=7), BAD), (dict(n_head=0), BAD), (dict(scale=NAN), BAD), (dict(q_stride=504), BAD), (dict(q=A + 2), UNSUP),
+    (dict(y=A + 8), UNSUP), (dict(lse=A + 2), UNSUP), (dict(ws=None), WS), (dict(ws_bytes=100), WS), (dict(ws=A + 16), UNSUP)])
+def test_tree_refused(kw, code):
+    assert tree(**kw) == code and B.last_error() != ""
+
+
+def test_tree_refuses_more_rows_than_the_mask_has():
+    big = batch(n_tok=500, max_q=65)
+    assert tree(b=big) == BAD and tree(b=big, words=2, ws=None) == WS
+    assert tree(b=batch(n_tok=500, max_q=257), words=4) == BAD
+    assert tree(c=cache(fmt=2)) == BAD and tree(b=batch(n_seq=0)) == BAD
+
+
+def test_trees_from_lists():
+    t = R.kv_tree([[-1, 0, 0, 2], [-1], [-1] + list(range(69))], device="cpu")
+    assert t["mask"].shape == (75, 2) and t["parent"].tolist()[:6] == [-1, 0, 0, 2, -1, -1] and t["depth"].tolist()[:6] == [0, 1, 1, 2, 0, 0]
+    assert t["mask"][:5, 0].tolist() == [1, 3, 5, 13, 1] and t["mask"][:5, 1].tolist() == [0] * 5
+    assert t["mask"][5 + 63].tolist() == [-1, 0] and t["mask"][5 + 69].tolist() == [-1, 63] and t["depth"][-1] == 69
+    assert R.kv_tree([[-1], [], [-1, 0]], device="cpu")["mask"].tolist() == [[1], [1], [3]]
+    for bad in ([[0]], [[-1, 1]], [[-1, -2]]):
+        with pytest.raises(ValueError):
+            R.kv_tree(bad, device="cpu")
+
+
 def decide(**kw):
     a = dict(n_seq=2, n_tok=5, vocab=100, q_start=A, ctx=A, tokens=A, parent=A, p=A, p_stride=100, q=A, q_stride=100, u=A, u_next=A,
              rows=A, start=A, new_ctx=A, next=A, ws=A, ws_bytes=1 << 30)
@@ -147,20 +182,29 @@ def test_runtime_refuses_what_it_cannot_pass_on(monkeypatch):
     b = R.kv_batch([1, 2], [5, 6], [[0], [1]], device="cpu")
     x, pos, turns = torch.zeros(3, 2, 64).half(), torch.zeros(3, dtype=torch.int32), R.rope(64, device="cpu")
     i, f, p = torch.zeros(3, dtype=torch.int32), torch.zeros(3), torch.zeros(3, 10)
-    for call in (lambda: R.rotate(x, pos, turns), lambda: R.kv_append_rope(c, x, x, b, turns, q=x), lambda: R.verify(b, i, i, p, f, f[:2])):
+    for call in (lambda: R.rotate(x, pos, turns), lambda: R.kv_append_rope(c, x, x, b, turns, q=x), lambda: R.verify(b, i, i, p, f, f[:2]),
+                 lambda: R.kv_attend_tree(c, x, x, x, b, torch.ones(3, 1, dtype=torch.int64))):
         with pytest.raises(ValueError):   # the host is no place for them
             call()
     monkeypatch.setattr(R, "_is_elsewhere", lambda stream, dev: False)
     monkeypatch.setattr(R, "_raw_stream", lambda dev: 0)
     done = []
-    for name in ("pi_rotate", "pi_kv_append_rope", "pi_verify"):
+    for name in ("pi_rotate", "pi_kv_append_rope", "pi_verify", "pi_kv_attend_tree"):
         monkeypatch.setattr(B, name, lambda *a, **k: done.append(a) or B.PI_OK)
     R.rotate(x, pos, turns)
     R.kv_append_rope(c, x, x, b, turns, q=x)
     R.kv_append_rope(c, torch.zeros(9, 2, 64).half(), torch.zeros(9, 2, 64).half(), b, rows=i)
     R.verify(b, i, i, p, f, f[:2], q=torch.zeros(3, 20)[:, :10])
-    assert len(done) == 4
+    m, ws = torch.ones(3, 1, dtype=torch.int64), torch.zeros(1 << 10, dtype=torch.uint8)
+    q = torch.zeros(3, 4, 64).half()
+    R.kv_attend_tree(c, q, x, x, b, m, pos, window=2 ** 40, ws=ws)
+    assert len(done) == 5 and done[-1][13] == 2 ** 31 - 1
     refused = [
+        lambda: R.kv_attend_tree(c, q, x, x, b, m.int(), ws=ws), lambda: R.kv_attend_tree(c, q, x, x, b, m[:2], ws=ws),
+        lambda: R.kv_attend_tree(c, q, x, x, b, m[:, 0], ws=ws), lambda: R.kv_attend_tree(c, q, x[:2], x, b, m, ws=ws),
+        lambda: R.kv_attend_tree(c, q, x, q, b, m, ws=ws), lambda: R.kv_attend_tree(c, q.float(), x, x, b, m, ws=ws),
+        lambda: R.kv_attend_tree(c, q, x, x, b, m, pos.long(), ws=ws), lambda: R.kv_attend_tree(c, q, x, x, b, m, y=x, ws=ws),
+        lambda: R.kv_attend_tree(c, q, x, x, b, m, lse=torch.zeros(3, 3), ws=ws),
         lambda: R.rotate(x.float(), pos, turns), lambda: R.rotate(x[0], pos, turns), lambda: R.rotate(x, pos.long(), turns),
         lambda: R.rotate(x, pos[:2], turns), lambda: R.rotate(x, pos, {**turns, "layout": "other"}),
         lambda: R.rotate(x, pos, {**turns, "rot": 32}), lambda: R.rotate(x, pos, {**turns, "turns": turns["turns"].int()}),
@@ -174,4 +218,4 @@ def test_runtime_refuses_what_it_cannot_pass_on(monkeypatch):
     for call in refused:
         with pytest.raises(ValueError):
             call()
-    assert len(done) == 4
+    assert len(done) == 5
