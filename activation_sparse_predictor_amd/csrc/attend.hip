@@ -69,7 +69,12 @@ __device__ __forceinline__ void attend_unit(const ARGS& A, const AttUnit& w) {
             for (int j = 0; j < KJ; ++j) kc[t][j] = ld16_stream(p + t * 4 * d + (FULL ? j * 256 : ko[j]));
     };
     auto load_v = [&](const Gran& e) {
-        const uint8_t* p = gran_at(A.c.v, e) + n16 * 16;
+        const uint8_t* p = gran_at(A.c.v, e) + n16 * (TREE ? 32 : 16);
+        if constexpr (TREE) {   // output tile k: every other dimension of 32, as the drafted rows' pairs come
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k) vc[k] = ld16_stream(p + k % 2 * 16 + (FULL || k / 2 * 32 + 2 * n16 < d ? k / 2 * 512 : -32 * n16));
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < 4 * KJ; ++k) vc[k] = ld16_stream(p + (FULL || k < dc ? k : dc - 1) * 256);
     };
@@ -147,14 +152,86 @@ __device__ __forceinline__ void attend_unit(const ARGS& A, const AttUnit& w) {
         l = fmaf(sum, unscale, l);
     };
 
-    const int cached = (ctx + kTile - 1) / kTile;   // tiles before a drafted row's own
-    const int t1 = !TREE || w.t1 < cached ? w.t1 : cached > w.t0 ? cached : w.t0;
-    for (int seg = w.t0; seg < t1; seg += kSegTiles) {
-        const int tiles = t1 - seg < kSegTiles ? t1 - seg : kSegTiles;
-        if (seg != w.t0) __syncthreads();   // the last segment's entries are no longer read
+    int c0 = w.t0, c1 = w.t1, turn = 0;   // cached tiles, and the wave that has the first of them
+    auto look_up = [&](int seg) __attribute__((always_inline)) {
+        const int tiles = c1 - seg < kSegTiles ? c1 - seg : kSegTiles;
         att_lookup(A, w, d, seg * (kTile / kGran), tiles * (kTile / kGran), threadIdx.x, kAttThreads, grans);
         __syncthreads();
-        int i = wave;   // this wave's tile in the segment
+    };
+    if constexpr (TREE) {
+        // The drafted rows: fp16 as they are, K and V of scale 1.  A piece's tiles go
+        // round the waves, the drafted ones first, at most one of them a wave; its
+        // rows are under way while the first granules are looked up.
+        const TreeTiles tt = tree_tiles(A, w);
+        c0 = tt.from, c1 = tt.to, turn = tt.drafted & (kAttWaves - 1);
+        const bool has = wave < tt.drafted;
+        const int n = w.q.n, tok0 = (w.t0 + wave) * kTile;
+        auto row = [&](int tok) { return (size_t)(w.q.row0 + (tok < n ? tok : n - 1)); };
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+        u32x4 dk[4][2 * KJ];
+        uint32_t dv[2 * KJ][kGran], bits = 0u;   // dimensions 2 n16 and the next of 32, of the lane's 16 tokens; those that the row attends to
+        auto load_values = [&](int j0, int j1) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kGran; ++i) {
+                const h16* p = A.tv + row(tok0 + g * kGran + i) * A.tv_stride + (size_t)w.h * d + 2 * n16;
+#pragma unroll
+                for (int j = j0; j < j1; ++j) dv[j][i] = FULL || j * 32 + 2 * n16 < d ? *reinterpret_cast<const uint32_t*>(p + j * 32) : 0u;
+            }
+        };
+        constexpr int kEarly = KJ == 4 ? 0 : 2 * KJ;   // value loads that fit the registers beside the keys'
+        if (has) {
+            if (live) bits = (uint32_t)(tree_bits(A, w.q.row0 + my_tok, n, w.t0 + wave) >> (kGran * g)) & 0xFFFFu;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const h16* p = A.tk + row(tok0 + (n16 >> 2) * kGran + t * 4 + (n16 & 3)) * A.tk_stride + (size_t)w.h * d + g * 16;
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) {
+                    dk[t][2 * j] = dk[t][2 * j + 1] = zero;
+                    if (FULL || j * 4 + g < dc) dk[t][2 * j] = ld16(p + j * 64), dk[t][2 * j + 1] = ld16(p + j * 64 + 8);
+                }
+            }
+            load_values(0, kEarly);
+        }
+        if (c0 < c1) look_up(c0);
+        if (has) {
+            const float kx = fabsf(A.scale2);
+            f32x4 S[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < 2 * KJ; ++j) S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, dk[t][j]), qf[j], S[t], 0, 0, 0);
+            }
+            load_values(kEarly, 2 * KJ);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) S[k / 4][k % 4] = bits >> k & 1u ? S[k / 4][k % 4] * kx : -__builtin_inff();
+            f16x8 ph[2], pl[2];
+            weigh(S, true, kx, 0.f, ph, pl);
+            uint32_t bad = 0u;
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; ++k) {
+                u32x4 v[2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)   // the even or the odd dimension of two tokens
+                    v[i / 4][i % 4] = __builtin_amdgcn_perm(dv[k / 2][2 * i + 1], dv[k / 2][2 * i], k % 2 ? 0x07060302u : 0x05040100u);
+                drop_nonfinite(v, bad);
+                const f16x8 a = __builtin_bit_cast(f16x8, v[0]), b = __builtin_bit_cast(f16x8, v[1]);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[0], O[k], 0, 0, 0);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, ph[1], O[k], 0, 0, 0);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[0], O[k], 0, 0, 0);
+                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pl[1], O[k], 0, 0, 0);
+            }
+            if (__ballot(bad != 0u)) {
+                bad = or_lanes16(bad);
+                if (bad & bits) l = __builtin_nanf("");
+            }
+        }
+    }
+    for (int seg = c0; seg < c1; seg += kSegTiles) {
+        const int tiles = c1 - seg < kSegTiles ? c1 - seg : kSegTiles;
+        if (seg != c0) __syncthreads();   // the last segment's entries are no longer read
+        if (!TREE || seg != c0) look_up(seg);
+        int i = TREE ? (wave - turn) & (kAttWaves - 1) : wave;   // this wave's tile in the segment
         Gran e;         // of the lane's V granule
         if (i < tiles) {
             load_k(grans[i * 4 + (n16 >> 2)]);
@@ -208,63 +285,6 @@ __device__ __forceinline__ void attend_unit(const ARGS& A, const AttUnit& w) {
         }
     }
 
-    if constexpr (TREE) {
-        // The drafted rows: fp16 as they are, K and V of scale 1.  The piece's tiles
-        // go round the waves as the cached ones do, whose turn goes on here.
-        const int n = w.q.n, ahead = (w.t0 > cached ? w.t0 : cached) - w.t0;
-        for (int i = ahead + ((wave - ahead) & (kAttWaves - 1)); w.t0 + i < w.t1; i += kAttWaves) {
-            const int x = w.t0 + i - cached, tok0 = x * kTile;
-            const uint32_t mine = live ? (uint32_t)(tree_bits(A, w.q.row0 + my_tok, n, x) >> (kGran * g)) & 0xFFFFu : 0u;
-            f32x4 S[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int tok = tok0 + (n16 >> 2) * kGran + t * 4 + (n16 & 3);
-                const h16* p = A.tk + (size_t)(w.q.row0 + (tok < n ? tok : n - 1)) * A.tk_stride + (size_t)w.h * d + g * 16;
-                S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < KJ; ++j) {
-                    u32x4 a = {0u, 0u, 0u, 0u}, e = a;
-                    if (FULL || j * 4 + g < dc) {
-                        a = ld16(p + j * 64);
-                        e = ld16(p + j * 64 + 8);
-                    }
-                    S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), qf[2 * j], S[t], 0, 0, 0);
-                    S[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, e), qf[2 * j + 1], S[t], 0, 0, 0);
-                }
-            }
-            const float kx = fabsf(A.scale2);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) S[k / 4][k % 4] = mine >> k & 1u ? S[k / 4][k % 4] * kx : -__builtin_inff();
-            f16x8 ph[2], pl[2];
-            weigh(S, true, kx, 0.f, ph, pl);
-            const h16* vt[kGran];   // this lane's granule: its tokens' rows
-#pragma unroll
-            for (int t = 0; t < kGran; ++t) {
-                const int tok = tok0 + g * kGran + t;
-                vt[t] = A.tv + (size_t)(w.q.row0 + (tok < n ? tok : n - 1)) * A.tv_stride + (size_t)w.h * d + n16;
-            }
-            uint32_t bad = 0u;
-#pragma unroll
-            for (int k = 0; k < 4 * KJ; ++k) {
-                if (!FULL && k >= dc) continue;
-                f16x8 a, b;
-#pragma unroll
-                for (int t = 0; t < 8; ++t) a[t] = vt[t][k * 16], b[t] = vt[8 + t][k * 16];
-                u32x4 v[2] = {__builtin_bit_cast(u32x4, a), __builtin_bit_cast(u32x4, b)};
-                drop_nonfinite(v, bad);
-                a = __builtin_bit_cast(f16x8, v[0]), b = __builtin_bit_cast(f16x8, v[1]);
-                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ph[0], O[k], 0, 0, 0);
-                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, ph[1], O[k], 0, 0, 0);
-                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[0], O[k], 0, 0, 0);
-                O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pl[1], O[k], 0, 0, 0);
-            }
-            if (__ballot(bad != 0u)) {
-                bad = or_lanes16(bad);
-                if (bad & mine) l = __builtin_nanf("");
-            }
-        }
-    }
-
     // Join the waves that had tiles: references first, then every wave brings
     // its sums to the common one and the workgroup adds them up.
     const int mine_n = w.t1 - w.t0, parts = mine_n < 1 ? 1 : mine_n < kAttWaves ? mine_n : kAttWaves;
@@ -284,8 +304,17 @@ __device__ __forceinline__ void attend_unit(const ARGS& A, const AttUnit& w) {
         for (int p = 0; p < parts; ++p) Mr = fmaxf(Mr, stat[p * 2 * ROWS + n16]);
         const float f = exp2_fast(M - Mr);
 #pragma unroll
-        for (int k = 0; k < 4 * KJ; ++k)
-            *reinterpret_cast<f32x4*>(&outs[(wave * ROWS + n16) * LD + k * 16 + g * 4]) = O[k] * f;
+        for (int k = 0; k < 4 * KJ; ++k) {
+            if constexpr (TREE) {   // (tiles k and k + 1: eight neighbours)
+                if (k % 2 == 0) {
+                    float* to = &outs[(wave * ROWS + n16) * LD + k * 16 + g * 8];
+                    *reinterpret_cast<f32x4*>(to) = f32x4{O[k][0], O[k + 1][0], O[k][1], O[k + 1][1]} * f;
+                    *reinterpret_cast<f32x4*>(to + 4) = f32x4{O[k][2], O[k + 1][2], O[k][3], O[k + 1][3]} * f;
+                }
+            } else {
+                *reinterpret_cast<f32x4*>(&outs[(wave * ROWS + n16) * LD + k * 16 + g * 4]) = O[k] * f;
+            }
+        }
         if (wave == 0 && g == 0) {
             float sum = 0.f;
             for (int p = 0; p < parts; ++p)
@@ -494,6 +523,11 @@ template <class ARGS>
 static hipError_t launch_attend(ARGS A, hipStream_t s) {
     const KvBatch& b = A.b;
     if (uses_prompt(b, A.group, A.c.n_kv)) {
+        // Drafted rows: where most sequences have about as many as the largest, a
+        // workgroup's waves without rows cost less than a second launch that finds
+        // little or nothing to do (16 ragged trees of 6 to 16: 79 us against 88).  One tree of
+        // 64 beside 31 single rows: 60 us in two launches, 78 in one; 8 beside 56: 72 and 76.
+        if (is_tree<ARGS> && 2LL * b.n_tok >= (long long)b.n_seq * b.max_q) return launch_attend_prompt(A, s);
         // rows of long and short sequences: each kernel takes its own (they
         // share the workspace, one after the other)
         A.upto = kAttRows;

@@ -49,7 +49,8 @@ struct AttArgs {
 // Attention of drafted tokens (pi_kv_attend_tree): every row sees the cached
 // tokens, all ctx of them or, under a window, those above its own position less
 // the window, and the drafted rows that its mask names.  The drafted rows are
-// further tiles of 64 keys behind the cached ones.
+// further tiles of 64 keys, before the cached ones: their loads are under way
+// while the cached granules are looked up.
 struct TreeArgs : AttArgs {
     const h16 *tk, *tv;            // drafted keys and values: n_tok rows
     long long tk_stride, tv_stride;
@@ -74,6 +75,7 @@ __device__ __forceinline__ uint64_t tree_bits(const TreeArgs& A, int row, int n,
     const int have = n - x * kTile;
     return have >= kTile ? m : have <= 0 ? 0ull : m & ((1ull << have) - 1);
 }
+__device__ __forceinline__ uint64_t tree_bits(const AttArgs&, int, int, int) { return 0ull; }   // no drafted rows
 // Whether a drafted row attends to anything.
 __device__ __forceinline__ bool tree_sees(const TreeArgs& A, const Seq& q, int tok) {
     if (tree_from(A, q.ctx, q.row0 + tok) < q.ctx) return true;
@@ -125,10 +127,14 @@ __device__ __forceinline__ int att_first_tile(const Seq& q, int window) {
     const int lo = q.ctx - (TREE ? 0 : q.n) - window + 1;
     return window > 0 && lo > 0 ? lo / kTile : 0;
 }
-template <bool TREE>
-__device__ __forceinline__ int att_tiles(const Seq& q, int window) {
-    const int n = (q.ctx + kTile - 1) / kTile - att_first_tile<TREE>(q, window);
-    if (TREE) return n + (q.n + kTile - 1) / kTile;
+__device__ __forceinline__ int tree_drafted(const TreeArgs& A, const Seq& q) {   // at most the mask's, whatever the lengths say
+    const int n = (q.n + kTile - 1) / kTile;
+    return n < A.words ? n : A.words;
+}
+template <class ARGS>
+__device__ __forceinline__ int att_tiles(const ARGS& A, const Seq& q) {
+    const int n = (q.ctx + kTile - 1) / kTile - att_first_tile<is_tree<ARGS>>(q, A.window);
+    if constexpr (is_tree<ARGS>) return n + tree_drafted(A, q);
     return n > 0 ? n : 1;
 }
 
@@ -136,8 +142,8 @@ __device__ __forceinline__ int att_tiles(const Seq& q, int window) {
 template <int ROWS, class ARGS>
 __device__ __forceinline__ int att_row_tiles(const ARGS& A, const Seq& q, int row_tile, int& first_tile) {
     if constexpr (is_tree<ARGS>) {
-        first_tile = att_first_tile<true>(q, A.window);
-        return att_tiles<true>(q, A.window);
+        first_tile = 0;   // of its drafted and cached tiles together
+        return att_tiles(A, q);
     }
     const int a = row_tile * ROWS / A.group;
     int b = (row_tile * ROWS + ROWS - 1) / A.group;
@@ -145,6 +151,16 @@ __device__ __forceinline__ int att_row_tiles(const ARGS& A, const Seq& q, int ro
     const int from = A.window > 0 ? q.ctx - q.n + a - A.window + 1 : 0, to = q.ctx - q.n + b;
     first_tile = from > 0 ? from / kTile : 0;
     return to < 0 ? 1 : to / kTile - first_tile + 1;
+}
+
+// A unit's tiles as its drafted ones, [w.t0, + drafted), and its cached ones, [from, to).
+struct TreeTiles {
+    int drafted, from, to;
+};
+__device__ __forceinline__ TreeTiles tree_tiles(const TreeArgs& A, const AttUnit& w) {
+    const int nt = tree_drafted(A, w.q), f = att_first_tile<true>(w.q, A.window) - nt;
+    const int a = w.t0 > nt ? w.t0 : nt, b = w.t1 > nt ? w.t1 : nt, d = (w.t1 < nt ? w.t1 : nt) - w.t0;
+    return TreeTiles{d > 0 ? d : 0, f + a, f + b};
 }
 
 // Tiles of a piece, before items that run at once are fitted: `want`, but at
@@ -167,7 +183,6 @@ __host__ __device__ constexpr int att_piece(float want, int min_tiles) {
 // rows and 2^10 sequences, whatever the lengths say, the sums stay below 2^31.
 template <int ROWS, class ARGS>
 __device__ __forceinline__ int att_plan(const ARGS& A, int item, AttUnit& w) {
-    constexpr bool TREE = is_tree<ARGS>;
     const KvBatch& b = A.b;
     auto row_tiles = [&](const Seq& q) {
         const int rows = q.n * A.group;
@@ -182,7 +197,7 @@ __device__ __forceinline__ int att_plan(const ARGS& A, int item, AttUnit& w) {
         if (s < b.n_seq) {
             q = kv_seq(b, s);
             rt = row_tiles(q);
-            tiles = att_tiles<TREE>(q, A.window);
+            tiles = att_tiles(A, q);
         }
         all += group_sum<64>((float)rt * (float)tiles);
         items += group_sum<64>((float)rt);
@@ -205,7 +220,7 @@ __device__ __forceinline__ int att_plan(const ARGS& A, int item, AttUnit& w) {
             if (s < b.n_seq) {
                 q = kv_seq(b, s);
                 rt = row_tiles(q);
-                tiles = att_tiles<TREE>(q, A.window);
+                tiles = att_tiles(A, q);
             }
         }
         const int ns = (tiles + C - 1) / C;

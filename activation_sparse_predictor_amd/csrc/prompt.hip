@@ -68,11 +68,15 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
     const int d = FULL ? DP : A.c.d, dc = d / 16, group = A.group;
     const int first = w.q.ctx - w.q.n, rows_all = w.q.n * group;
     const int n = w.t1 - w.t0;
-    // tiles of the piece that the cache holds; drafted rows are the others
-    const int cached = (w.q.ctx + kTile - 1) / kTile, nc = !TREE || w.t1 <= cached ? n : cached > w.t0 ? cached - w.t0 : 0;
+    // the unit's first tiles are drafted rows, nd of them; tile x >= nd is the cache's tile c0 + x
+    int nd = 0, c0 = w.t0;
+    if constexpr (TREE) {
+        const TreeTiles t = tree_tiles(A, w);
+        nd = t.drafted, c0 = t.from - nd;
+    }
 
     auto fill = [&](int x, int count) {   // tiles [x, x + count) of this unit, into their places of the ring
-        att_lookup(A, w, d, (w.t0 + x) * (kTile / kGran), count * (kTile / kGran), threadIdx.x, kProThreads,
+        att_lookup(A, w, d, (c0 + x) * (kTile / kGran), count * (kTile / kGran), threadIdx.x, kProThreads,
                    &grans[(x & (kProRing - 1)) * (kTile / kGran)]);
     };
 
@@ -81,7 +85,16 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
         const int t = r / group;
         return t < w.q.n ? t : w.q.n - 1;
     };
-    const int row_w = w.row_tile * ROWS, row_v = row_w + wave * 16 * NT;
+    const int row_w = w.row_tile * ROWS, row_v = row_w + wave * 16 * (TREE ? 1 : NT);
+    // A wave's operand nt has rows [row_of(nt), + 16).  Drafted rows are often fewer
+    // than a workgroup's 128: they fill the waves' first operands before any
+    // second one, and the second ones from the other end in every other unit, so that
+    // a SIMD's waves do not all have two.
+    auto row_of = [&](int nt) {
+        if (!TREE) return row_v + nt * 16;
+        return nt == 0 ? row_v : row_w + (kProWaves + (wave ^ ((w.q.s ^ w.row_tile) & 1 ? kProWaves - 1 : 0))) * 16;
+    };
+    const int operands = TREE && NT == 2 && row_of(NT - 1) >= rows_all ? 1 : NT;
     int any_to = first + last_tok(row_w + ROWS - 1);
     int any_from = A.window > 0 ? first + row_w / group - A.window + 1 : 0;
     const bool idle = row_v >= rows_all;
@@ -99,7 +112,7 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
     const uint32_t sign = A.scale2 < 0.f ? 0x80008000u : 0u;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int r = row_v + nt * 16 + n16;
+        const int r = row_of(nt) + n16;
         const bool live = r < rows_all;
         const int tok = live ? r / group : 0, head = w.h * group + (live ? r - tok * group : 0);
         pos[nt] = !live ? -1 : TREE ? w.q.ctx - 1 : first + tok;
@@ -142,7 +155,7 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
         }
     };
     auto store = [&](int x, int i) __attribute__((always_inline)) {   // piece i
-        const int tile0 = (w.t0 + x) * kTile, key0 = tile0 + g * kGran;
+        const int tile0 = (c0 + x) * kTile, key0 = tile0 + g * kGran;
         u32x4* to = frags + ((x & 1) * kFrags + 2 * wave) * 64 + lane;
         u32x4 v = st[i];
         if (FMT == 1 && i >= KJ && (tile0 < any_from || tile0 + kTile - 1 > any_to)) {   // slots that no row here attends to may hold NaN
@@ -154,43 +167,59 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
         to[(i * 2 * kProWaves + 1) * 64] = __builtin_bit_cast(u32x4, codes8<FMT>(v.z, v.w));
     };
 
-    // Tile x, drafted: fp16 rows as they are, straight into the fragments' places.
-    auto stage_drafted = [&](int x) __attribute__((always_inline)) {
+    // Drafted tile x: fp16 rows as they are, into the fragments' places.  Keys as
+    // above; of the values, two neighbouring dimensions of a granule's tokens a thread.
+    constexpr int kDraftV = TREE ? (KJ + 1) / 2 : 1;   // (one head dimension in 64: half of the threads)
+    u32x4 dk[TREE ? 2 * KJ : 1];
+    uint32_t dv[kDraftV][kGran];
+    auto load_drafted = [&](int x) __attribute__((always_inline)) {
         if constexpr (TREE) {
-            const int tile = w.t0 + x - cached, tok0 = tile * kTile, rows = w.q.n;
-            u32x4* to = frags + ((x & 1) * kFrags + 2 * wave) * 64 + lane;
+            const int tok0 = (w.t0 + x) * kTile, rows = w.q.n;
             auto row = [&](int tok) { return (size_t)(w.q.row0 + (tok < rows ? tok : rows - 1)); };
             const u32x4 zero = {0u, 0u, 0u, 0u};
-            u32x4 kv[2 * KJ];
 #pragma unroll
             for (int i = 0; i < KJ; ++i) {
                 const int t = wave / KJ + i * (kProWaves / KJ), ch = wave % KJ * 4 + g;
                 const h16* p = A.tk + row(tok0 + (n16 >> 2) * kGran + t * 4 + (n16 & 3)) * A.tk_stride + (size_t)w.h * d + ch * 16;
-                kv[2 * i] = kv[2 * i + 1] = zero;
-                if (FULL || ch < dc) kv[2 * i] = ld16(p), kv[2 * i + 1] = ld16(p + 8);
+                dk[2 * i] = dk[2 * i + 1] = zero;
+                if (FULL || ch < dc) dk[2 * i] = ld16(p), dk[2 * i + 1] = ld16(p + 8);
             }
-            f16x8 v[2 * KJ];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const h16* p = A.tv + row(tok0 + g * kGran + t) * A.tv_stride + (size_t)w.h * d + wave * 16 + n16;
-                const h16* q = A.tv + row(tok0 + g * kGran + 8 + t) * A.tv_stride + (size_t)w.h * d + wave * 16 + n16;
+            for (int t = 0; t < kGran; ++t) {
+                const h16* p = A.tv + row(tok0 + g * kGran + t) * A.tv_stride + (size_t)w.h * d;
 #pragma unroll
-                for (int i = 0; i < KJ; ++i) {
-                    v[2 * i][t] = v[2 * i + 1][t] = (f16)0.f;
-                    if (FULL || wave + 4 * i < dc) v[2 * i][t] = p[i * kProWaves * 16], v[2 * i + 1][t] = q[i * kProWaves * 16];
+                for (int i = 0; i < kDraftV; ++i) {
+                    const int dim = (wave + 4 * i) * 32 + 2 * n16;
+                    dv[i][t] = (FULL && KJ > 1) || dim < d ? *reinterpret_cast<const uint32_t*>(p + dim) : 0u;
                 }
+            }
+        }
+    };
+    auto store_drafted = [&](int x) __attribute__((always_inline)) {
+        if constexpr (TREE) {
+            u32x4* const tile = frags + (x & 1) * kFrags * 64;
+#pragma unroll
+            for (int i = 0; i < KJ; ++i) {
+                tile[(2 * (wave + 4 * i)) * 64 + lane] = dk[2 * i];
+                tile[(2 * (wave + 4 * i) + 1) * 64 + lane] = dk[2 * i + 1];
             }
             uint32_t bad = 0u;
 #pragma unroll
-            for (int i = 0; i < KJ; ++i) {
-                to[i * 2 * kProWaves * 64] = kv[2 * i];
-                to[(i * 2 * kProWaves + 1) * 64] = kv[2 * i + 1];
-                u32x4 f[2] = {__builtin_bit_cast(u32x4, v[2 * i]), __builtin_bit_cast(u32x4, v[2 * i + 1])};
-                drop_nonfinite(f, bad);
-                to[(KJ + i) * 2 * kProWaves * 64] = f[0];
-                to[((KJ + i) * 2 * kProWaves + 1) * 64] = f[1];
+            for (int i = 0; i < kDraftV; ++i) {
+                if ((wave + 4 * i) * 32 >= DP) continue;
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {   // dimension (wave + 4 i) 32 + 2 n16 + o: fragment pair, and lane in it
+                    u32x4 v[2];
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        v[t / 4][t % 4] = __builtin_amdgcn_perm(dv[i][2 * t + 1], dv[i][2 * t], o ? 0x07060302u : 0x05040100u);
+                    drop_nonfinite(v, bad);
+                    u32x4* to = tile + (8 * KJ + 2 * ((wave + 4 * i) * 2 + (n16 >> 3))) * 64 + g * 16 + (2 * n16 + o) % 16;
+                    to[0] = v[0];
+                    to[64] = v[1];
+                }
             }
-            if (bad) atomicOr(&s_bad[tile & (kMaxDrafted - 1)][g], bad);
+            if (bad) atomicOr(&s_bad[(w.t0 + x) & (kMaxDrafted - 1)][g], bad);
         }
     };
 
@@ -205,63 +234,26 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
         for (int k = 0; k < 4 * KJ; ++k) O[nt][k] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    if (n > 0) {
-        if constexpr (TREE) {
-            if (threadIdx.x < kMaxDrafted * (kTile / kGran)) (&s_bad[0][0])[threadIdx.x] = 0u;
-        }
-        fill(0, nc < kProSeg ? nc : kProSeg);
-        __syncthreads();
-        if (!TREE || nc > 0) {
-            load(0);
-#pragma unroll
-            for (int i = 0; i < 2 * KJ; ++i) store(0, i);
-        } else {
-            stage_drafted(0);
-        }
-        if (nc > 1) load(1);
-        lds_barrier();
-    }
-    for (int x = 0; x < n; ++x) {
-        // Of the two workgroups of a CU the younger one's waves get what the
-        // older one's leave.  A priority that falls every second tile, and starts
-        // again, keeps the two abreast, so that they end together.
-        switch (x / 2 & 3) {
-            case 0: __builtin_amdgcn_s_setprio(3); break;
-            case 1: __builtin_amdgcn_s_setprio(2); break;
-            case 2: __builtin_amdgcn_s_setprio(1); break;
-            default: __builtin_amdgcn_s_setprio(0);
-        }
-        if (x % kProSeg == 0 && x + kProSeg < nc) {   // the next segment, in the half of the ring that is done with
-            const int left = nc - x - kProSeg;
-            fill(x + kProSeg, left < kProSeg ? left : kProSeg);
-        }
-        if (x + 1 < nc) {
-#pragma unroll
-            for (int i = 0; i < 2 * KJ; ++i) store(x + 1, i);
-        } else if (TREE && x + 1 < n) {
-            stage_drafted(x + 1);
-        }
-        if (x + 2 < nc) load(x + 2);
-        const int tile0 = (w.t0 + x) * kTile;
-        const bool drafted = TREE && x >= nc;
+    // Tile x against this wave's first LIVE operands, those that have rows.
+    auto compute = [&](auto live, auto of_drafted, int x) __attribute__((always_inline)) {
+        constexpr int LIVE = decltype(live)::value;
+        constexpr bool drafted = decltype(of_drafted)::value;
+        const int tile0 = (c0 + x) * kTile;
         if (drafted ? !idle : tile0 <= v_to && tile0 + kTile - 1 >= v_from) {
             const Gran* gr = &grans[(x & (kProRing - 1)) * (kTile / kGran)];
-            float kx = gr[g].kx, lv = gr[g].lv;
-            uint32_t mine[NT], broken = 0u;   // drafted tokens of granule g: those that the row attends to, and those whose values are not finite
-            if constexpr (TREE) {
-                if (drafted) {
-                    kx = fabsf(A.scale2), lv = 0.f;
-                    broken = s_bad[(w.t0 + x - cached) & (kMaxDrafted - 1)][g];
+            const float kx = drafted ? fabsf(A.scale2) : gr[g].kx, lv = drafted ? 0.f : gr[g].lv;
+            uint32_t mine[LIVE], broken = 0u;   // drafted tokens of granule g: those that the row attends to, and those whose values are not finite
+            if constexpr (drafted) {
+                broken = s_bad[(w.t0 + x) & (kMaxDrafted - 1)][g];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int r = row_v + nt * 16 + n16;
-                        mine[nt] = r < rows_all ? (uint32_t)(tree_bits(A, w.q.row0 + r / group, w.q.n, w.t0 + x - cached) >> (kGran * g)) & 0xFFFFu : 0u;
-                    }
+                for (int nt = 0; nt < LIVE; ++nt) {
+                    const int r = row_of(nt) + n16;
+                    mine[nt] = r < rows_all ? (uint32_t)(tree_bits(A, w.q.row0 + r / group, w.q.n, w.t0 + x) >> (kGran * g)) & 0xFFFFu : 0u;
                 }
             }
             const u32x4* kf = frags + (x & 1) * kFrags * 64 + lane;
             // Fragments are read a group of products ahead (the compiler alone reads one and waits for it).
-            f32x4 S[NT][4];
+            f32x4 S[LIVE][4];
             f16x8 ka[2][2 * KJ];
 #pragma unroll
             for (int k = 0; k < 2 * KJ; ++k) ka[0][k] = __builtin_bit_cast(f16x8, kf[k * 64]);
@@ -273,11 +265,11 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) S[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int nt = 0; nt < LIVE; ++nt) S[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < 2 * KJ; ++k)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < LIVE; ++nt)
                         S[nt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ka[t % 2][k], qf[nt][k], S[nt][t], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -288,10 +280,10 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
             __builtin_amdgcn_sched_barrier(0);
             const int key0 = tile0 + g * kGran;
             const bool edge = drafted || tile0 < v_free_from || tile0 + kTile - 1 > v_free_to;
-            f16x8 ph[NT][2], pl[NT][2];   // the weights' leading and following halves
+            f16x8 ph[LIVE][2], pl[LIVE][2];   // the weights' leading and following halves
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (drafted) {
+            for (int nt = 0; nt < LIVE; ++nt) {
+                if constexpr (drafted) {
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         const float v = S[nt][k / 4][k % 4] * kx;
@@ -344,7 +336,7 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
+                    for (int nt = 0; nt < LIVE; ++nt) {
                         f32x4& o = O[nt][2 * k + i / 2];
                         o = __builtin_amdgcn_mfma_f32_16x16x32_f16(va[k % 2][i], ph[nt][i % 2], o, 0, 0, 0);
                         o = __builtin_amdgcn_mfma_f32_16x16x32_f16(va[k % 2][i], pl[nt][i % 2], o, 0, 0, 0);
@@ -352,6 +344,57 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+    };
+    auto compute_rows = [&](auto of_drafted, int x) __attribute__((always_inline)) {
+        if (TREE && NT == 2 && operands == 1) compute(std::integral_constant<int, 1>{}, of_drafted, x);
+        else compute(std::integral_constant<int, NT>{}, of_drafted, x);
+    };
+
+    if constexpr (TREE) {
+        if (nd > 0) {
+            if (threadIdx.x < kMaxDrafted * (kTile / kGran)) (&s_bad[0][0])[threadIdx.x] = 0u;
+        }
+    }
+    if (n > 0) {
+        fill(nd, (n < kProSeg ? n : kProSeg) - nd);
+        __syncthreads();
+        if constexpr (TREE) {
+#pragma unroll 1
+            for (int x = 0; x < nd; ++x) {
+                load_drafted(x);
+                store_drafted(x);
+                lds_barrier();
+                compute_rows(std::true_type{}, x);
+            }
+        }
+        if (n > nd) {
+            load(nd);
+#pragma unroll
+            for (int i = 0; i < 2 * KJ; ++i) store(nd, i);
+        }
+        if (n > nd + 1) load(nd + 1);
+        lds_barrier();
+    }
+    for (int x = nd; x < n; ++x) {
+        // Of the two workgroups of a CU the younger one's waves get what the
+        // older one's leave.  A priority that falls every second tile, and starts
+        // again, keeps the two abreast, so that they end together.
+        switch (x / 2 & 3) {
+            case 0: __builtin_amdgcn_s_setprio(3); break;
+            case 1: __builtin_amdgcn_s_setprio(2); break;
+            case 2: __builtin_amdgcn_s_setprio(1); break;
+            default: __builtin_amdgcn_s_setprio(0);
+        }
+        if (TREE ? x == nd || x % kProSeg == 0 : x % kProSeg == 0) {   // the next segment, in the half of the ring that is done with
+            const int next = TREE ? x / kProSeg * kProSeg + kProSeg : x + kProSeg, left = n - next;
+            if (left > 0) fill(next, left < kProSeg ? left : kProSeg);
+        }
+        if (x + 1 < n) {
+#pragma unroll
+            for (int i = 0; i < 2 * KJ; ++i) store(x + 1, i);
+        }
+        if (x + 2 < n) load(x + 2);
+        compute_rows(std::false_type{}, x);
         lds_barrier();
     }
 
@@ -454,7 +497,7 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
     typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const int row = row_w + wave * 16 * NT + nt * 16 + n16e;
+        const int row = row_of(nt) + n16e;
         if (row >= rows_all) continue;
         const int tok = row / group, head = w.h * group + row - tok * group;
         const size_t to = (size_t)(w.q.row0 + tok) * A.n_head + head;
@@ -475,7 +518,7 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
 }
 
 template <int FMT, int KJ, bool FULL, class ARGS>
-__global__ __launch_bounds__(kProThreads, 2) void k_attend_prompt(ARGS A) {
+__global__ __launch_bounds__(kProThreads, is_tree<ARGS> && KJ == 1 ? 3 : 2) void k_attend_prompt(ARGS A) {
     constexpr int ROWS = prompt_rows(KJ);
     AttUnit w;
     w.h = blockIdx.x;

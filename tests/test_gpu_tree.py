@@ -206,6 +206,25 @@ def test_rows_of_no_sequence_are_left_and_broken_ranges_stay_inside():
     assert torch.equal(y[5:], y0[5:])
 
 
+@pytest.mark.parametrize("heads,n_kv", [(4, 2), (64, 16)])
+def test_more_rows_than_the_mask_has_stay_inside(heads, n_kv):
+    """Row ranges on the device that exceed max_q and the mask: those rows are unspecified, others are not touched."""
+    n, d = 400, 64
+    cache, rows = filled([5000, 33], n_kv, d, 16, "int8", seed=21)
+    q, (k, v) = queries(n, heads, d), drafted(n, n_kv, d)
+    batch = R.kv_batch([64, 3], [5000, 33], rows, DEV)
+    batch.update(n_tok=n, max_q=64, q_start=torch.tensor([0, 397, 400], dtype=torch.int32, device=DEV))
+    mask = torch.full((n, 1), 7, dtype=torch.int64, device=DEV)
+    y = torch.full((n + 8, heads, d), 5.0, dtype=torch.float16, device=DEV)
+    R.kv_attend_tree(cache, q, k, v, batch, mask, y=y[:n])
+    torch.cuda.synchronize()
+    assert torch.all(y[n:] == 5.0)
+    # (the split of the work, and with it the order of the sums, is the whole batch's: within the bound, not bit for bit)
+    want, _, a = O.attend_tree(host(cache), {"q_start": [0, 3], "ctx": [33], "table": [rows[1]]},
+                               *(t[397:].cpu().numpy() for t in (q, k, v)), np.full((3, 1), 7, np.uint64), d ** -0.5)
+    assert np.all(np.abs(y[397:400].cpu().numpy() - want) <= 2.0 ** -11 * np.abs(want) + 1.25 * 2.0 ** -10 * a + 2.0 ** -25)
+
+
 def test_a_page_that_does_not_exist_is_its_readers():
     cache, batch, mask, pos, q, k, v = case([5, 3], [40, 33], 4, 2, 64, 16, "int8", seed=16)
     y0 = R.kv_attend_tree(cache, q, k, v, batch, mask)
