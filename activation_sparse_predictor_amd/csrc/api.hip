@@ -1036,7 +1036,7 @@ pi_status pi_verify(int n_seq, int n_tok, int vocab, const int32_t* q_start, con
     PI_TRY(check_ws(ws, ws_bytes, pi::verify_bytes(n_seq, n_tok, vocab), "pi_verify"));
     ws_forget(ws);
     pi::VerifyArgs A{n_seq, n_tok, vocab, q_start, ctx, tokens, parent, p, q, p_stride, q_stride, u, u_next, rows, start, new_ctx,
-                     next, 0, 0};
+                     next, 0, 0, 0};
     hipError_t e = pi::launch_verify(A, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(e, "pi_verify");
     return ok();

@@ -346,7 +346,7 @@ struct VerifyArgs {
     long long p_stride, q_stride;
     const float *u, *u_next;
     int32_t *rows, *start, *new_ctx, *next;
-    int slice, slices;    // set by launch_verify
+    int slice, slices, each;   // set by launch_verify: elements of a slice, slices, and those of a workgroup
 };
 size_t verify_bytes(int n_seq, int n_tok, int vocab);
 hipError_t launch_verify(VerifyArgs A, char* ws, hipStream_t s);

@@ -645,23 +645,27 @@ def verify(batch: dict, tokens: torch.Tensor, parent: torch.Tensor, p: torch.Ten
     if _is_elsewhere(stream, dev):
         return _elsewhere(stream, p.device, (start, ctx, tokens, parent, p, u, u_next, q),
                           lambda: verify(batch, tokens, parent, p, u, u_next, q))
-    n_seq = ctx.shape[0] if ctx.dim() == 1 else -1
-    words, floats = (start, ctx, tokens, parent), (p, u, u_next) if q is None else (p, u, u_next, q)
-    if not (all(t.dtype is _I32 and t.is_contiguous() and t.get_device() == dev for t in words)
-            and all(t.dtype is _F32 and t.get_device() == dev for t in floats)
-            and start.shape == (n_seq + 1,) and tokens.shape == parent.shape == u.shape == (n_tok,) and u_next.shape == (n_seq,)
-            and u.is_contiguous() and u_next.is_contiguous() and p.dim() == 2 and p.shape[0] == n_tok
-            and (p.stride(1) == 1 or p.shape[1] == 1) and (q is None or (q.shape == p.shape and (q.stride(1) == 1 or q.shape[1] == 1)))):
+    seqs, shape = ctx.shape, p.shape
+    # one expression: this runs before every step of a serving loop
+    if not (len(seqs) == 1 and len(shape) == 2 and shape[0] == n_tok and start.shape == (seqs[0] + 1,) and u_next.shape == seqs
+            and tokens.shape == parent.shape == u.shape == (n_tok,)
+            and start.dtype is _I32 and ctx.dtype is _I32 and tokens.dtype is _I32 and parent.dtype is _I32
+            and p.dtype is _F32 and u.dtype is _F32 and u_next.dtype is _F32
+            and start.is_contiguous() and ctx.is_contiguous() and tokens.is_contiguous() and parent.is_contiguous()
+            and u.is_contiguous() and u_next.is_contiguous() and (p.stride(1) == 1 or shape[1] == 1)
+            and start.get_device() == ctx.get_device() == tokens.get_device() == parent.get_device() == u.get_device()
+            == u_next.get_device() == dev
+            and (q is None or (q.shape == shape and q.dtype is _F32 and (q.stride(1) == 1 or shape[1] == 1) and q.get_device() == dev))):
         raise ValueError("q_start (n_seq + 1), ctx (n_seq), tokens and parent (n_tok) are int32, u (n_tok), u_next (n_seq), p and q "
                          "(n_tok x vocab, rows of neighbours) float32; all on one device")
-    vocab = p.shape[1]
-    rows, new_start, new_ctx, after = torch.empty(n_tok + 3 * n_seq + 1, dtype=_I32, device=p.device).split(
-        [n_tok, n_seq + 1, n_seq, n_seq])
+    n_seq, vocab = seqs[0], shape[1]
     size = B.pi_verify_workspace_size(n_seq, n_tok, vocab)
-    ws = torch.empty(size, dtype=_U8, device=p.device)
+    head = -(-size // 256) * 64   # the workspace, in words, before the outputs: one allocation
+    ws, rows, new_start, new_ctx, after = torch.empty(head + n_tok + 3 * n_seq + 1, dtype=_I32, device=p.device).split(
+        [head, n_tok, n_seq + 1, n_seq, n_seq])
     B.check(B.pi_verify(n_seq, n_tok, vocab, start, ctx, tokens, parent, p, p.stride(0) if n_tok > 1 else vocab, q,
-                        0 if q is None else q.stride(0) if n_tok > 1 else vocab, u, u_next, rows, new_start, new_ctx, after, ws, size,
-                        _raw_stream(dev)), "pi_verify")
+                        0 if q is None else q.stride(0) if n_tok > 1 else vocab, u, u_next, rows, new_start, new_ctx, after, ws,
+                        size, _raw_stream(dev)), "pi_verify")
     return {"rows": rows, "q_start": new_start, "ctx": new_ctx, "next": after}
 
 
