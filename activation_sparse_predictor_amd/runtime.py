@@ -8,6 +8,7 @@ W_down, b_up, b_gate, P1, b1, P2, b2) plus kind, tau and sizes.
 
 from __future__ import annotations
 
+import functools
 from typing import Dict, Optional, Tuple
 
 import torch
@@ -632,6 +633,10 @@ def kv_append_rope(cache: dict, k: torch.Tensor, v: torch.Tensor, batch: dict, r
     return q_out
 
 
+_VERIFY_WS: Dict[Tuple[int, int], torch.Tensor] = {}
+_verify_bytes = functools.lru_cache(maxsize=256)(B.pi_verify_workspace_size)
+
+
 def verify(batch: dict, tokens: torch.Tensor, parent: torch.Tensor, p: torch.Tensor, u: torch.Tensor, u_next: torch.Tensor,
            q: Optional[torch.Tensor] = None, stream=None) -> dict:
     """pi_verify: which drafted tokens stay.  batch: q_start, ctx and n_tok of the
@@ -659,13 +664,19 @@ def verify(batch: dict, tokens: torch.Tensor, parent: torch.Tensor, p: torch.Ten
         raise ValueError("q_start (n_seq + 1), ctx (n_seq), tokens and parent (n_tok) are int32, u (n_tok), u_next (n_seq), p and q "
                          "(n_tok x vocab, rows of neighbours) float32; all on one device")
     n_seq, vocab = seqs[0], shape[1]
-    size = B.pi_verify_workspace_size(n_seq, n_tok, vocab)
-    head = -(-size // 256) * 64   # the workspace, in words, before the outputs: one allocation
-    ws, rows, new_start, new_ctx, after = torch.empty(head + n_tok + 3 * n_seq + 1, dtype=_I32, device=p.device).split(
-        [head, n_tok, n_seq + 1, n_seq, n_seq])
+    on, st = p.device, _raw_stream(dev)
+    rows, new_start = torch.empty(n_tok, dtype=_I32, device=on), torch.empty(n_seq + 1, dtype=_I32, device=on)
+    new_ctx, after = torch.empty(n_seq, dtype=_I32, device=on), torch.empty(n_seq, dtype=_I32, device=on)
+    size = _verify_bytes(n_seq, n_tok, vocab)
+    if _capturing():   # the graph's own, from its pool
+        ws = torch.empty(size, dtype=_U8, device=on)
+    else:              # a stream's calls share one: it holds nothing between them
+        ws = _VERIFY_WS.get((dev, st))
+        if ws is None or ws.numel() < size:
+            ws = _VERIFY_WS[(dev, st)] = torch.empty(size, dtype=_U8, device=on)
     B.check(B.pi_verify(n_seq, n_tok, vocab, start, ctx, tokens, parent, p, p.stride(0) if n_tok > 1 else vocab, q,
                         0 if q is None else q.stride(0) if n_tok > 1 else vocab, u, u_next, rows, new_start, new_ctx, after, ws,
-                        size, _raw_stream(dev)), "pi_verify")
+                        size, st), "pi_verify")
     return {"rows": rows, "q_start": new_start, "ctx": new_ctx, "next": after}
 
 

@@ -188,6 +188,7 @@ def test_runtime_refuses_what_it_cannot_pass_on(monkeypatch):
             call()
     monkeypatch.setattr(R, "_is_elsewhere", lambda stream, dev: False)
     monkeypatch.setattr(R, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(R, "_capturing", lambda: False)
     done = []
     for name in ("pi_rotate", "pi_kv_append_rope", "pi_verify", "pi_kv_attend_tree"):
         monkeypatch.setattr(B, name, lambda *a, **k: done.append(a) or B.PI_OK)
