@@ -489,10 +489,10 @@ static hipError_t launch_single(const ARGS& A, hipStream_t s) {
     }
     // heads side by side: the row tiles that read one head's pages run on one
     // XCD where the heads are a multiple of 8, and share its L2
-    int drafted = 0;
-    if constexpr (is_tree<ARGS>) drafted = A.words;
-    hipLaunchKernelGGL((k_attend<FMT, KJ, FULL, WAVES, ARGS>), dim3(A.c.n_kv, att_grid(A, kAttRows, drafted)), dim3(WAVES * kWave),
-                       shm, s, A);
+    unsigned units;
+    if constexpr (is_tree<ARGS>) units = att_grid(A, kAttRows, A.words, A.at_once);
+    else units = att_grid(A, kAttRows);
+    hipLaunchKernelGGL((k_attend<FMT, KJ, FULL, WAVES, ARGS>), dim3(A.c.n_kv, units), dim3(WAVES * kWave), shm, s, A);
     return hipGetLastError();
 }
 
@@ -512,6 +512,7 @@ static hipError_t launch_singles(ARGS A, hipStream_t s) {
     const int waves = kj < 4 && att_most_row_tiles(A.b, A.group, kAttRows) * A.c.n_kv <= 256 ? 8 : 4;
     A.target = single_target(kj, waves);
     A.min_tiles = kMinTiles;
+    if constexpr (is_tree<ARGS>) A.at_once = A.target;
     if (kj == 4) return full ? launch_single<FMT, 4, true, 4, ARGS>(A, s) : launch_single<FMT, 4, false, 4, ARGS>(A, s);
     if (kj == 2 && waves == 8) return full ? launch_single<FMT, 2, true, 8, ARGS>(A, s) : launch_single<FMT, 2, false, 8, ARGS>(A, s);
     if (kj == 2) return full ? launch_single<FMT, 2, true, 4, ARGS>(A, s) : launch_single<FMT, 2, false, 4, ARGS>(A, s);
@@ -547,7 +548,7 @@ hipError_t launch_kv_attend(const KvCache& c, const KvBatch& b, const h16* q, lo
     const AttArgs A{c, b, q, q_stride, n_head, group, window, 0, 0x7FFFFFFF, 0, 0, scale * 1.4426950408889634f, y, lse,
                     reinterpret_cast<uint32_t*>(data), reinterpret_cast<float*>(data + kv_attend_zero_bytes())};
     if (!draft) return launch_attend(A, s);
-    return launch_attend(TreeArgs{A, draft->k, draft->v, draft->k_stride, draft->v_stride, draft->mask, draft->words, draft->pos}, s);
+    return launch_attend(TreeArgs{A, draft->k, draft->v, draft->k_stride, draft->v_stride, draft->mask, draft->words, draft->pos, 0}, s);
 }
 
 }  // namespace pi

@@ -57,6 +57,7 @@ struct TreeArgs : AttArgs {
     const uint64_t* mask;          // n_tok x words
     int words;
     const int32_t* pos;            // n_tok; only read under a window
+    int at_once;                   // workgroups that the chip holds (target: the bound that the slots rest on)
 };
 constexpr int kMaxDrafted = 4;     // tiles of drafted rows (words)
 template <class ARGS> constexpr bool is_tree = std::is_same_v<ARGS, TreeArgs>;
@@ -205,12 +206,32 @@ __device__ __forceinline__ int att_plan(const ARGS& A, int item, AttUnit& w) {
     const float room = (float)A.target / (float)A.c.n_kv;   // workgroups a head has
     const float want = all / room * 1.001f;                 // a little above: the slots rest on it
     int C = att_piece(want, A.min_tiles);
-    if (b.n_seq <= kWave && items <= room) {
-        // All items can run at once: the smallest C (to a sixteenth) whose rounded-up pieces still do.
+    // the smallest C from `from` on (to a sixteenth) whose rounded-up pieces are at most `most`
+    auto fit = [&](int from, float most) {
+        int c = from;
         for (int i = 0; i < 24; ++i) {
-            if (group_sum<64>((float)(rt * ((tiles + C - 1) / C))) <= room) break;
-            C += C / 16 + 1;
+            if (group_sum<64>((float)(rt * ((tiles + c - 1) / c))) <= most) break;
+            c += c / 16 + 1;
         }
+        return c;
+    };
+    if constexpr (is_tree<ARGS>) {
+        const float once = (float)A.at_once / (float)A.c.n_kv;
+        if (b.n_seq <= kWave && items <= once) {
+            const float wish = all / once * 1.001f;
+            C = fit(att_piece(wish, A.min_tiles), once);
+            // Items alike in length do not divide into just any number of workgroups:
+            // where one turn of pieces would leave many idle, two turns of shorter ones
+            // (each with its start and join, about eight tiles' time) may end earlier.
+            const float slots = (float)kAttSlots / (float)A.c.n_kv, twice = 2.f * once < slots ? 2.f * once : slots;
+            if ((float)C > 1.5f * wish && C > 32) {
+                const int c = fit(att_piece(0.5f * wish, A.min_tiles), twice);
+                if (2 * (c + 8) < C + 8) C = c;
+            }
+        }
+    } else if (b.n_seq <= kWave && items <= room) {
+        // All items can run at once.
+        C = fit(C, room);
     }
     int before = 0, slots = 0;
     for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
@@ -328,11 +349,12 @@ inline long long att_most_row_tiles(const KvBatch& b, int group, int rows) {
     return each < all ? each : all;
 }
 // Units of one head that the plan can come to (more would be taken in turn).
-inline unsigned att_grid(const AttArgs& A, int rows, int drafted_tiles = 0) {
+inline unsigned att_grid(const AttArgs& A, int rows, int drafted_tiles = 0, int at_once = 0) {
     const long long items = att_most_row_tiles(A.b, A.group, rows);
     const long long cap = ((long long)A.b.table_stride * A.c.page + kTile - 1) / kTile + drafted_tiles;
     const long long most = items * ((cap + A.min_tiles - 1) / A.min_tiles);
-    long long units = items + (A.target + A.c.n_kv - 1) / A.c.n_kv;
+    const int most_units = 2 * at_once > A.target ? 2 * at_once : A.target;
+    long long units = items + (most_units + A.c.n_kv - 1) / A.c.n_kv;
     if (units > most) units = most;
     return (unsigned)(units < 65535 ? units : 65535);
 }

@@ -538,9 +538,14 @@ static hipError_t launch(ARGS A, hipStream_t s) {
     const int kj = att_kj(A.c.d);
     A.target = pro_target(kj);
     A.min_tiles = kProMinTiles;
-    int drafted = 0;
-    if constexpr (is_tree<ARGS>) drafted = A.words;
-    const dim3 grid(A.c.n_kv, att_grid(A, prompt_rows(kj), drafted));
+    unsigned units;
+    if constexpr (is_tree<ARGS>) {
+        A.at_once = kj == 1 ? 768 : A.target;   // (three of a head of up to 64 dimensions fit a CU)
+        units = att_grid(A, prompt_rows(kj), A.words, A.at_once);
+    } else {
+        units = att_grid(A, prompt_rows(kj));
+    }
+    const dim3 grid(A.c.n_kv, units);
     const size_t shm = (size_t)2 * 16 * kj * 1024;
     const bool full = A.c.d == 64 * kj;
     hipError_t e = hipSuccess;
