@@ -88,11 +88,10 @@ __device__ __forceinline__ void prompt_unit(const ARGS& A, const AttUnit& w) {
     const int row_w = w.row_tile * ROWS, row_v = row_w + wave * 16 * (TREE ? 1 : NT);
     // A wave's operand nt has rows [row_of(nt), + 16).  Drafted rows are often fewer
     // than a workgroup's 128: they fill the waves' first operands before any
-    // second one, and the second ones from the other end in every other unit, so that
-    // a SIMD's waves do not all have two.
+    // second one, so that no wave has two while another has none.
     auto row_of = [&](int nt) {
         if (!TREE) return row_v + nt * 16;
-        return nt == 0 ? row_v : row_w + (kProWaves + (wave ^ ((w.q.s ^ w.row_tile) & 1 ? kProWaves - 1 : 0))) * 16;
+        return nt == 0 ? row_v : row_w + (kProWaves + wave) * 16;
     };
     const int operands = TREE && NT == 2 && row_of(NT - 1) >= rows_all ? 1 : NT;
     int any_to = first + last_tok(row_w + ROWS - 1);
