@@ -11,6 +11,8 @@
 // under 2^-23 of one: a 2^11th of the rounding of an fp16 result.
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "internal.hpp"
 
@@ -29,16 +31,20 @@ __device__ __forceinline__ void rope_cos_sin(int pos, uint64_t turns, float gain
 
 // From so many units on, four heads share a thread's angles; below, the threads
 // would be too few to fill the chip.
-constexpr long long kRopeShareFrom = 1 << 19;
+constexpr long long kRopeShareFrom = 1 << 18;
 
 constexpr int kRopePairs = 1;   // of pi_rope_layout; 0: half
 
-// A thread's share of a head: eight dimensions of the pairs layout; of the half
-// layout two runs of eight, rot / 2 apart, or eight that are not turned; where
-// those runs would not start at 16 bytes, one pair.
+// A thread's share of a head: 16 dimensions of the pairs layout (eight where rot or
+// d does not divide into 16); of the half layout two runs of eight, rot / 2 apart, or
+// eight that are not turned; where rot does not divide into these, one pair.
+__host__ __device__ inline int rope_dims(const Rope& R, int d) {   // of a unit that is turned
+    if (R.rot % 16 == 0 && (R.layout != kRopePairs || d % 16 == 0)) return 16;
+    return R.rot % 8 == 0 && R.layout == kRopePairs ? 8 : 2;
+}
 __host__ __device__ inline int rope_units(const Rope& R, int d) {
-    if (R.layout == kRopePairs) return d / 8;
-    return R.rot % 16 == 0 ? R.rot / 16 + (d - R.rot) / 8 : d / 2;
+    const int dims = rope_dims(R, d);
+    return R.layout != kRopePairs && dims == 16 ? R.rot / 16 + (d - R.rot) / 8 : d / dims;
 }
 
 // Unit `slot % units` of heads slot / units, + groups, + 2 groups, ... (up to HPT of
@@ -52,10 +58,12 @@ __device__ __forceinline__ void rotate_heads(const Rope& R, int d, int n_head, i
         p = (f16)fmaf(fa, c, -(fb * s));   // one rounding to fp16, the result's
         q = (f16)fmaf(fb, c, fa * s);
     };
-    if (R.layout != kRopePairs && R.rot % 16 != 0) {
+    const int dims = rope_dims(R, d);
+    if (dims == 2) {
         const bool turned = u < half;
         if (!turned && x == y) return;
-        const int i = turned ? u : R.rot + 2 * (u - half), j = turned ? u + half : i + 1;
+        const int i = !turned ? R.rot + 2 * (u - half) : R.layout == kRopePairs ? 2 * u : u;
+        const int j = turned && R.layout != kRopePairs ? u + half : i + 1;
         f16 a[HPT], b[HPT];
 #pragma unroll
         for (int k = 0; k < HPT; ++k) {
@@ -74,59 +82,64 @@ __device__ __forceinline__ void rotate_heads(const Rope& R, int d, int n_head, i
         }
         return;
     }
-    const bool pairs = R.layout == kRopePairs, two = !pairs && u < R.rot / 16;
-    const int at = pairs || two ? 8 * u : R.rot + (u - R.rot / 16) * 8;
-    const bool turned = two || (pairs && at < R.rot);
-    if (!turned && x == y) return;
-    u32x4 a[HPT], b[HPT];
-#pragma unroll
-    for (int k = 0; k < HPT; ++k) {
-        const int h = g + k * groups;
-        if (h >= n_head) continue;
-        a[k] = ld16(x + (size_t)h * d + at);
-        if (two) b[k] = ld16(x + (size_t)h * d + at + half);
-    }
-    if (two) {
-        float c[8], s[8];
-#pragma unroll
-        for (int m = 0; m < 8; ++m) rope_cos_sin(pos, R.turns[at + m], R.gain, c[m], s[m]);
+    // VECS vectors of eight dimensions a head, the second `behind` dimensions after the
+    // first; rotate: turns them, by the angles from pair m0 on.
+    auto run = [&](auto vecs, int at, int behind, bool turned, int m0, auto rotate) __attribute__((always_inline)) {
+        constexpr int VECS = decltype(vecs)::value;
+        u32x4 v[HPT][VECS];
 #pragma unroll
         for (int k = 0; k < HPT; ++k) {
             const int h = g + k * groups;
             if (h >= n_head) continue;
-            u32x4 p, q;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const f16x2 v = as_h2(a[k][m]), w = as_h2(b[k][m]);
-                f16 e0, e1, f0, f1;
-                turn(v.x, w.x, c[2 * m], s[2 * m], e0, f0);
-                turn(v.y, w.y, c[2 * m + 1], s[2 * m + 1], e1, f1);
-                p[m] = __builtin_bit_cast(uint32_t, f16x2{e0, e1});
-                q[m] = __builtin_bit_cast(uint32_t, f16x2{f0, f1});
-            }
-            *reinterpret_cast<u32x4*>(y + (size_t)h * d + at) = p;
-            *reinterpret_cast<u32x4*>(y + (size_t)h * d + at + half) = q;
+            for (int i = 0; i < VECS; ++i) v[k][i] = ld16(x + (size_t)h * d + at + i * behind);
         }
+        float c[4 * VECS], s[4 * VECS];
+        if (turned) {
+#pragma unroll
+            for (int m = 0; m < 4 * VECS; ++m) rope_cos_sin(pos, R.turns[m0 + m], R.gain, c[m], s[m]);
+        }
+#pragma unroll
+        for (int k = 0; k < HPT; ++k) {
+            const int h = g + k * groups;
+            if (h >= n_head) continue;
+            if (turned) rotate(v[k], c, s);
+#pragma unroll
+            for (int i = 0; i < VECS; ++i) *reinterpret_cast<u32x4*>(y + (size_t)h * d + at + i * behind) = v[k][i];
+        }
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    if (R.layout == kRopePairs) {
+        const int at = dims * u;
+        if (at >= R.rot && x == y) return;
+        auto neighbours = [&](auto& v, auto& c, auto& s) __attribute__((always_inline)) {
+#pragma unroll
+            for (int m = 0; m < (int)(sizeof(c) / sizeof(c[0])); ++m) {
+                const f16x2 w = as_h2(v[m / 4][m % 4]);
+                f16 p, q;
+                turn(w.x, w.y, c[m], s[m], p, q);
+                v[m / 4][m % 4] = __builtin_bit_cast(uint32_t, f16x2{p, q});
+            }
+        };
+        if (dims == 16) run(Two{}, at, 8, at < R.rot, at / 2, neighbours);
+        else run(One{}, at, 0, at < R.rot, at / 2, neighbours);
         return;
     }
-    float c[4], s[4];
+    if (u < R.rot / 16) {
+        run(Two{}, 8 * u, half, true, 8 * u, [&](auto& v, auto& c, auto& s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-        if (turned && at / 2 + m < half) rope_cos_sin(pos, R.turns[at / 2 + m], R.gain, c[m], s[m]);
-#pragma unroll
-    for (int k = 0; k < HPT; ++k) {
-        const int h = g + k * groups;
-        if (h >= n_head) continue;
-        u32x4 p = a[k];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            if (!turned || at / 2 + m >= half) continue;
-            const f16x2 v = as_h2(a[k][m]);
-            f16 e, f;
-            turn(v.x, v.y, c[m], s[m], e, f);
-            p[m] = __builtin_bit_cast(uint32_t, f16x2{e, f});
-        }
-        *reinterpret_cast<u32x4*>(y + (size_t)h * d + at) = p;
+            for (int m = 0; m < 4; ++m) {
+                const f16x2 a = as_h2(v[0][m]), b = as_h2(v[1][m]);
+                f16 e0, e1, f0, f1;
+                turn(a.x, b.x, c[2 * m], s[2 * m], e0, f0);
+                turn(a.y, b.y, c[2 * m + 1], s[2 * m + 1], e1, f1);
+                v[0][m] = __builtin_bit_cast(uint32_t, f16x2{e0, e1});
+                v[1][m] = __builtin_bit_cast(uint32_t, f16x2{f0, f1});
+            }
+        });
+    } else if (x != y) {
+        run(One{}, R.rot + (u - R.rot / 16) * 8, 0, false, 0, [](auto&, auto&, auto&) {});
     }
 }
 

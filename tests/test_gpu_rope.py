@@ -88,6 +88,22 @@ def test_rotate_many_rows(layout, heads, d, rot):
     assert torch.equal(few, got[:2])
 
 
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("heads,d,rot", [(18, 80, 20), (30, 128, 64), (33, 40, 40), (7, 128, 120)])
+def test_rotate_many_rows_either_layout(layout, heads, d, rot):
+    """Shared angles at every width of a thread's share: 16 dimensions, eight, one pair; in place too."""
+    n = (1 << 18) // (heads * (d // 16)) + 5
+    rng = np.random.default_rng(d + rot)
+    x = rows(rng, n, heads, d, heads * d + 8)
+    pos = rng.integers(-(1 << 30), 1 << 30, n).astype(np.int32)
+    plan = R.rope(rot, layout=layout, device=DEV)
+    freqs, gain = O.frequencies(rot)
+    kept, at = x.cpu().numpy(), torch.from_numpy(pos).to(DEV)
+    got = R.rotate(x, at, plan)
+    near(got.cpu().numpy(), O.rotate(kept, pos, freqs, layout, gain), kept, rot, layout, gain)
+    assert torch.equal(R.rotate(x, at, plan, out=x), got)
+
+
 def test_far_positions_are_exact():
     """Angles of whole eighths of a turn at positions up to the type's ends."""
     freqs = 2 * np.pi * np.array([0.25, 0.125, 0.5, 0.375])
