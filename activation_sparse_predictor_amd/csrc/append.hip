@@ -6,6 +6,13 @@
 // rotation adds no rounding of its own; the batch's row i may be any row of k and
 // v (a list on the device: the drafted tokens that were accepted); and the
 // queries' heads are turned by further workgroups of the same launch.
+//
+// Bytes bound the large calls: four prompts of 2048 tokens of 64 query and 8 kv
+// heads of 128 move 319 MB (of which the queries 268) in 66.5 us, 4.8 TB/s, where a
+// large copy reaches 5.1.  Small ones are a chain of dependent reads, lengths ->
+// page -> scale beside list -> rows and angles, then the block's maximum and the codes:
+// one token of 56 heads 6.7 us (without rotation and queries 5.0), 64 sequences of
+// 64 query and 8 kv heads 8.9, the accepted rows of 48 trees 6.7.
 #include "kv.hpp"
 #include "rope.hpp"
 

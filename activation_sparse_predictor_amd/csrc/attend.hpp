@@ -222,7 +222,8 @@ __device__ __forceinline__ int att_plan(const ARGS& A, int item, AttUnit& w) {
             C = fit(att_piece(wish, A.min_tiles), once);
             // Items alike in length do not divide into just any number of workgroups:
             // where one turn of pieces would leave many idle, two turns of shorter ones
-            // (each with its start and join, about eight tiles' time) may end earlier.
+            // (each with its start and join, about eight tiles' time) may end earlier (9 trees
+            // of 64 rows of 64 heads, 8 kv, on 4096 tokens: 137 us against 169).
             const float slots = (float)kAttSlots / (float)A.c.n_kv, twice = 2.f * once < slots ? 2.f * once : slots;
             if ((float)C > 1.5f * wish && C > 32) {
                 const int c = fit(att_piece(0.5f * wish, A.min_tiles), twice);

@@ -30,7 +30,10 @@ __device__ __forceinline__ void rope_cos_sin(int pos, uint64_t turns, float gain
 }
 
 // From so many units on, four heads share a thread's angles; below, the threads
-// would be too few to fill the chip.
+// would be too few to fill the chip.  By the card, shared and not, heads of 128:
+// half layout, 72 heads: 64 tokens (2^15 units) 3.6 and 3.1 us, 512 (2^18) 5.3 and
+// 6.1, 2048 13.4 and 15.4, 8192 49.7 and 54; beside an append, 64 heads: 256 tokens
+// (2^17) 6.8 and 7.0, 512 7.6 and 8.2, 8192 57 and 81.
 constexpr long long kRopeShareFrom = 1 << 18;
 
 constexpr int kRopePairs = 1;   // of pi_rope_layout; 0: half
