@@ -57,7 +57,7 @@ struct TreeArgs : AttArgs {
     const uint64_t* mask;          // n_tok x words
     int words;
     const int32_t* pos;            // n_tok; only read under a window
-    int at_once;                   // workgroups that the chip holds (target: the bound that the slots rest on)
+    int at_once;                   // prompt.hip: workgroups that the chip holds (target: the bound that the slots rest on); attend.hip: 0
 };
 constexpr int kMaxDrafted = 4;     // tiles of drafted rows (words)
 template <class ARGS> constexpr bool is_tree = std::is_same_v<ARGS, TreeArgs>;
@@ -215,24 +215,25 @@ __device__ __forceinline__ int att_plan(const ARGS& A, int item, AttUnit& w) {
         }
         return c;
     };
-    if constexpr (is_tree<ARGS>) {
-        const float once = (float)A.at_once / (float)A.c.n_kv;
-        if (b.n_seq <= kWave && items <= once) {
-            const float wish = all / once * 1.001f;
-            C = fit(att_piece(wish, A.min_tiles), once);
+    float once = room;
+    if constexpr (is_tree<ARGS>) once = A.at_once > 0 ? (float)A.at_once / (float)A.c.n_kv : room;
+    if (b.n_seq <= kWave && items <= once) {
+        // All items can run at once.
+        const float wish = all / once * 1.001f;
+        C = fit(att_piece(wish, A.min_tiles), once);
+        if constexpr (is_tree<ARGS>) {
             // Items alike in length do not divide into just any number of workgroups:
             // where one turn of pieces would leave many idle, two turns of shorter ones
             // (each with its start and join, about eight tiles' time) may end earlier (9 trees
-            // of 64 rows of 64 heads, 8 kv, on 4096 tokens: 137 us against 169).
+            // of 64 rows of 64 heads, 8 kv, on 4096 tokens: 137 us against 169).  For
+            // single rows' pieces they never did (12 trees of up to 48 rows of 8 kv heads of 256
+            // on up to 4096 tokens: 73 us, 68 in one turn).
             const float slots = (float)kAttSlots / (float)A.c.n_kv, twice = 2.f * once < slots ? 2.f * once : slots;
-            if ((float)C > 1.5f * wish && C > 32) {
+            if (A.at_once > 0 && (float)C > 1.5f * wish && C > 32) {
                 const int c = fit(att_piece(0.5f * wish, A.min_tiles), twice);
                 if (2 * (c + 8) < C + 8) C = c;
             }
         }
-    } else if (b.n_seq <= kWave && items <= room) {
-        // All items can run at once.
-        C = fit(C, room);
     }
     int before = 0, slots = 0;
     for (int s0 = 0; s0 < b.n_seq; s0 += kWave) {
