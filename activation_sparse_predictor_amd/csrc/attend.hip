@@ -32,8 +32,10 @@
 // tenth of the time.
 //
 // A chain of 8 drafted tokens behind 128 cached ones, 56 heads: 9.7 us; 4 of 4 rows of 64
-// heads, 8 kv, on 16384 tokens (134 MB) 48, where the rows as a chain in the cache take 40:
-// the wave with the drafted tile is a round behind the others.
+// heads, 8 kv, on 16384 tokens (134 MB) 41, where the rows as a chain in the cache take 39;
+// 16 of 4 rows of 64 heads of 64 up to 8000 tokens 29.5 (28.5).  The drafted rows' values come
+// as pairs of dimensions; with the cached codes read in the pairs' order too, half a
+// line an instruction, these took 48 and 34.
 #include "attend.hpp"
 #include "pi.h"
 
@@ -41,6 +43,7 @@ namespace pi {
 
 constexpr float kLift = 15.7f, kSlack = 0.25f;   // of the references, above
 constexpr int kAttRows = 16;   // query rows of a workgroup
+constexpr int kHeadRounds = 2;   // of tiles that the waves without drafted ones share among them
 constexpr int kMinTiles = 4;   // tiles a piece of a whole context has at least
 // workgroups the work is split into: those that run at once, by the registers
 constexpr int single_target(int kj, int waves) { return kj == 4 || waves == 8 ? 256 : 512; }
@@ -73,12 +76,7 @@ __device__ __forceinline__ void attend_unit(const ARGS& A, const AttUnit& w) {
             for (int j = 0; j < KJ; ++j) kc[t][j] = ld16_stream(p + t * 4 * d + (FULL ? j * 256 : ko[j]));
     };
     auto load_v = [&](const Gran& e) {
-        const uint8_t* p = gran_at(A.c.v, e) + n16 * (TREE ? 32 : 16);
-        if constexpr (TREE) {   // output tile k: every other dimension of 32, as the drafted rows' pairs come
-#pragma unroll
-            for (int k = 0; k < 4 * KJ; ++k) vc[k] = ld16_stream(p + k % 2 * 16 + (FULL || k / 2 * 32 + 2 * n16 < d ? k / 2 * 512 : -32 * n16));
-            return;
-        }
+        const uint8_t* p = gran_at(A.c.v, e) + n16 * 16;
 #pragma unroll
         for (int k = 0; k < 4 * KJ; ++k) vc[k] = ld16_stream(p + (FULL || k < dc ? k : dc - 1) * 256);
     };
@@ -156,7 +154,7 @@ __device__ __forceinline__ void attend_unit(const ARGS& A, const AttUnit& w) {
         l = fmaf(sum, unscale, l);
     };
 
-    int c0 = w.t0, c1 = w.t1, turn = 0;   // cached tiles, and the wave that has the first of them
+    int c0 = w.t0, c1 = w.t1, nd = 0;   // cached tiles; drafted ones, of waves 0 .. nd - 1
     auto look_up = [&](int seg) __attribute__((always_inline)) {
         const int tiles = c1 - seg < kSegTiles ? c1 - seg : kSegTiles;
         att_lookup(A, w, d, seg * (kTile / kGran), tiles * (kTile / kGran), threadIdx.x, kAttThreads, grans);
@@ -167,7 +165,7 @@ __device__ __forceinline__ void attend_unit(const ARGS& A, const AttUnit& w) {
         // round the waves, the drafted ones first, at most one of them a wave; its
         // rows are under way while the first granules are looked up.
         const TreeTiles tt = tree_tiles(A, w);
-        c0 = tt.from, c1 = tt.to, turn = tt.drafted & (kAttWaves - 1);
+        c0 = tt.from, c1 = tt.to, nd = tt.drafted;
         const bool has = wave < tt.drafted;
         const int n = w.q.n, tok0 = (w.t0 + wave) * kTile;
         auto row = [&](int tok) { return (size_t)(w.q.row0 + (tok < n ? tok : n - 1)); };
@@ -225,25 +223,45 @@ __device__ __forceinline__ void attend_unit(const ARGS& A, const AttUnit& w) {
                 O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pl[0], O[k], 0, 0, 0);
                 O[k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, pl[1], O[k], 0, 0, 0);
             }
+            // Tiles k and k + 1 hold the even and the odd dimensions of 32, lane group g
+            // those from 8 g on.  They go where the cached tiles' results will: tile k + t has
+            // dimensions 16 t + 4 g + r, which group 2 t + g / 2 holds.
+#pragma unroll
+            for (int k = 0; k < 4 * KJ; k += 2) {
+                const f32x4 even = O[k], odd = O[k + 1];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int from = n16 + 16 * (2 * t + (g >> 1));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float low = __shfl(r % 2 ? odd[r / 2] : even[r / 2], from, kWave);
+                        const float high = __shfl(r % 2 ? odd[2 + r / 2] : even[2 + r / 2], from, kWave);
+                        O[k + t][r] = g & 1 ? high : low;
+                    }
+                }
+            }
             if (__ballot(bad != 0u)) {
                 bad = or_lanes16(bad);
                 if (bad & bits) l = __builtin_nanf("");
             }
         }
     }
+    // A drafted tile takes a wave some two rounds of cached ones: the others share the tiles of these.
+    const int others = kAttWaves - nd, head = TREE ? kHeadRounds * others : 0;
     for (int seg = c0; seg < c1; seg += kSegTiles) {
         const int tiles = c1 - seg < kSegTiles ? c1 - seg : kSegTiles;
         if (seg != c0) __syncthreads();   // the last segment's entries are no longer read
         if (!TREE || seg != c0) look_up(seg);
-        int i = TREE ? (wave - turn) & (kAttWaves - 1) : wave;   // this wave's tile in the segment
+        int i = TREE && seg == c0 ? wave < nd ? head + wave : wave - nd : wave;   // this wave's tile in the segment
         Gran e;         // of the lane's V granule
         if (i < tiles) {
             load_k(grans[i * 4 + (n16 >> 2)]);
             e = grans[i * 4 + g];
             load_v(e);
         }
-        for (; i < tiles; i += kAttWaves) {
-            const int next = i + kAttWaves;
+        for (int next; i < tiles; i = next) {
+            next = i + kAttWaves;
+            if (TREE && seg == c0 && i < head) next = i + others < head ? i + others : head + wave;
             const float kx = e.kx, lv = e.lv;
             f32x4 S[4];
 #pragma unroll
@@ -309,15 +327,7 @@ __device__ __forceinline__ void attend_unit(const ARGS& A, const AttUnit& w) {
         const float f = exp2_fast(M - Mr);
 #pragma unroll
         for (int k = 0; k < 4 * KJ; ++k) {
-            if constexpr (TREE) {   // (tiles k and k + 1: eight neighbours)
-                if (k % 2 == 0) {
-                    float* to = &outs[(wave * ROWS + n16) * LD + k * 16 + g * 8];
-                    *reinterpret_cast<f32x4*>(to) = f32x4{O[k][0], O[k + 1][0], O[k][1], O[k + 1][1]} * f;
-                    *reinterpret_cast<f32x4*>(to + 4) = f32x4{O[k][2], O[k + 1][2], O[k][3], O[k + 1][3]} * f;
-                }
-            } else {
-                *reinterpret_cast<f32x4*>(&outs[(wave * ROWS + n16) * LD + k * 16 + g * 4]) = O[k] * f;
-            }
+            *reinterpret_cast<f32x4*>(&outs[(wave * ROWS + n16) * LD + k * 16 + g * 4]) = O[k] * f;
         }
         if (wave == 0 && g == 0) {
             float sum = 0.f;
