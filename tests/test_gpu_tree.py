@@ -270,3 +270,13 @@ def test_another_stream_and_captured_graphs():
             got = y.clone()
             torch.cuda.synchronize()
             assert torch.equal(got, R.kv_attend_tree(cache, q, k, v, batch, mask, pos=pos, window=500))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+@pytest.mark.parametrize("heads,n_kv,d,counts,ctx", [(2, 1, 64, [200, 3], [9000, 30]), (1, 1, 128, [256], [20000]), (1, 1, 256, [250, 70], [700, 5000]),
+                                                     (2, 2, 128, [129], [400]), (1, 1, 64, [256, 1], [0, 64])])
+def test_several_drafted_tiles_beside_cached_ones(fmt, heads, n_kv, d, counts, ctx):
+    """The kernel of few items: up to all waves of a workgroup have a drafted tile, the others share the cached ones meanwhile."""
+    c = case(counts, ctx, heads, n_kv, d, 32, fmt, seed=d + counts[0])
+    check(*c)
+    check(*c, window=260)
