@@ -31,7 +31,7 @@
 // half keep 22 bits where the products are free: the matrix cores are busy a
 // tenth of the time.
 //
-// A chain of 8 drafted tokens behind 128 cached ones, 56 heads: 9.7 us; 4 of 4 rows of 64
+// A chain of 8 drafted tokens behind 128 cached ones, 56 heads: 9.3 us; 4 of 4 rows of 64
 // heads, 8 kv, on 16384 tokens (134 MB) 41, where the rows as a chain in the cache take 39;
 // 16 of 4 rows of 64 heads of 64 up to 8000 tokens 29.5 (28.5).  The drafted rows' values come
 // as pairs of dimensions; with the cached codes read in the pairs' order too, half a
