@@ -536,7 +536,13 @@ static hipError_t launch_singles(ARGS A, hipStream_t s) {
 template <class ARGS>
 static hipError_t launch_attend(ARGS A, hipStream_t s) {
     const KvBatch& b = A.b;
-    if (uses_prompt(b, A.group, A.c.n_kv)) {
+    // Drafted rows, up to two items of 16 a sequence: the second reading of the keys comes from
+    // L2 and costs less than the other kernel's idle waves, however many items there are (64 heads, 8
+    // kv: 32 ragged sequences of 4 rows on up to 8192 tokens 87 us against 112, 64 on 4096 82
+    // against 114, 128 on 1024 60 against 75; 8 kv heads of 256 104 against 182; with three
+    // items, 32 of 6 rows on 8192, 121 against 110).
+    const bool few = is_tree<ARGS> && (long long)b.max_q * A.group <= 2 * kAttRows;
+    if (!few && uses_prompt(b, A.group, A.c.n_kv)) {
         // Drafted rows: where most sequences have about as many as the largest, a
         // workgroup's waves without rows cost less than a second launch that finds
         // little or nothing to do (16 ragged trees of 6 to 16: 79 us against 88).  One tree of

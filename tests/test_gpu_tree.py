@@ -280,3 +280,15 @@ def test_several_drafted_tiles_beside_cached_ones(fmt, heads, n_kv, d, counts, c
     c = case(counts, ctx, heads, n_kv, d, 32, fmt, seed=d + counts[0])
     check(*c)
     check(*c, window=260)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+@pytest.mark.parametrize("heads,n_kv,d,n", [(64, 8, 128, 4), (64, 32, 64, 16), (16, 8, 256, 16), (64, 8, 128, 5)])
+def test_many_sequences_of_two_items(fmt, heads, n_kv, d, n):
+    """More 16-row items than the kernel of few rows takes for chains, on either side of 32 rows a kv head."""
+    rng = np.random.default_rng(d)
+    counts = [n] + [int(x) for x in rng.integers(0, n + 1, 39)]
+    ctx = [int(x) for x in rng.integers(0, 300, 40)]
+    c = case(counts, ctx, heads, n_kv, d, 16, fmt, seed=n)
+    check(*c)
+    check(*c, window=100)
