@@ -9,6 +9,7 @@ W_down, b_up, b_gate, P1, b1, P2, b2) plus kind, tau and sizes.
 from __future__ import annotations
 
 import functools
+import threading
 from typing import Dict, Optional, Tuple
 
 import torch
@@ -633,7 +634,9 @@ def kv_append_rope(cache: dict, k: torch.Tensor, v: torch.Tensor, batch: dict, r
     return q_out
 
 
-_VERIFY_WS: Dict[Tuple[int, int], torch.Tensor] = {}
+# Of each host thread, by device and stream: pi_verify's second launch reads what its first left
+# in the workspace, and another thread's call on the same stream may be queued between the two.
+_VERIFY_WS = threading.local()
 _verify_bytes = functools.lru_cache(maxsize=256)(B.pi_verify_workspace_size)
 
 
@@ -670,10 +673,11 @@ def verify(batch: dict, tokens: torch.Tensor, parent: torch.Tensor, p: torch.Ten
     size = _verify_bytes(n_seq, n_tok, vocab)
     if _capturing():   # the graph's own, from its pool
         ws = torch.empty(size, dtype=_U8, device=on)
-    else:              # a stream's calls share one: it holds nothing between them
-        ws = _VERIFY_WS.get((dev, st))
+    else:              # a thread's calls on a stream share one: it holds nothing from call to call
+        kept = _VERIFY_WS.__dict__
+        ws = kept.get((dev, st))
         if ws is None or ws.numel() < size:
-            ws = _VERIFY_WS[(dev, st)] = torch.empty(size, dtype=_U8, device=on)
+            ws = kept[(dev, st)] = torch.empty(size, dtype=_U8, device=on)
     B.check(B.pi_verify(n_seq, n_tok, vocab, start, ctx, tokens, parent, p, p.stride(0) if n_tok > 1 else vocab, q,
                         0 if q is None else q.stride(0) if n_tok > 1 else vocab, u, u_next, rows, new_start, new_ctx, after, ws,
                         size, st), "pi_verify")
