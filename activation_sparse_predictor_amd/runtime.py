@@ -27,10 +27,11 @@ class Workspace:
     def get(self, nbytes: int) -> Tuple[Optional[torch.Tensor], int]:
         if nbytes == 0:
             return None, 0
-        if self.buf is None or self.buf.numel() < nbytes:
+        buf = self.buf   # (read once: another thread may replace it)
+        if buf is None or buf.numel() < nbytes:
             # zero-filled once: the library keeps epoch-tagged sync words in its header
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-        return self.buf, self.buf.numel()
+            buf = self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        return buf, buf.numel()
 
 
 _WS: Dict[Tuple[str, int], Workspace] = {}
@@ -480,7 +481,8 @@ def _attend_with(call, b, heads: int, n_kv: int, d: int, device, st: int, ws: Op
     own = _KV_WS.get(key)
     if own is None:
         own = _KV_WS[key] = Workspace(device)
-    status = call(own.buf, 0 if own.buf is None else own.buf.numel())
+    buf = own.buf   # (read once: another thread may replace it by a larger one)
+    status = call(buf, 0 if buf is None else buf.numel())
     if status == B.PI_ERR_WORKSPACE:   # too small for these sizes: nothing was launched
         status = call(*own.get(B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, n_kv, d)))
     B.check(status, name)

@@ -65,3 +65,59 @@ def test_a_threads_verify_calls_share_a_workspace(on_host, monkeypatch):
     for seqs in (20, 3, 20):
         verify(seqs)
     assert len(set(seen)) == 1
+
+
+class Growing:
+    """A kept workspace that another thread replaces by a larger one after its first reading."""
+
+    def __init__(self):
+        self.bufs = [torch.zeros(64, dtype=torch.uint8), torch.zeros(1 << 30, dtype=torch.uint8, device="meta")]
+
+    @property
+    def buf(self):
+        return self.bufs.pop(0) if len(self.bufs) > 1 else self.bufs[0]
+
+    def get(self, nbytes):
+        b = torch.zeros(nbytes, dtype=torch.uint8)
+        return b, nbytes
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_a_workspace_replaced_meanwhile_is_not_taken_for_the_larger(on_host, monkeypatch, tree):
+    """What the library is told of a workspace's size is that of the buffer it gets."""
+    seen = []
+
+    def note(a):
+        ws, size = a[-3], a[-2]
+        seen.append((0 if ws is None else ws.numel(), size))
+        return B.PI_OK if size >= 4096 else B.PI_ERR_WORKSPACE
+
+    monkeypatch.setattr(B, "pi_kv_attend", lambda *a: note(a))
+    monkeypatch.setattr(B, "pi_kv_attend_tree", lambda *a: note(a))
+    device = torch.device("cpu")
+    monkeypatch.setattr(R, "_KV_WS", {(d, 7): Growing() for d in (device.index, -1)})
+    c, b = R.kv_cache(4, 2, 64, device="cpu"), R.kv_batch([1], [5], [[0]], device="cpu")
+    q, x = torch.zeros(1, 4, 64).half(), torch.zeros(1, 2, 64).half()
+    if tree:
+        R.kv_attend_tree(c, q, x, x, b, torch.ones(1, 1, dtype=torch.int64))
+    else:
+        R.kv_attend(c, q, b)
+    assert seen and all(have == told for have, told in seen)
+
+
+def test_a_grown_workspace_is_returned_with_its_own_size():
+    class Racing(R.Workspace):
+        """Every reading of buf after the first finds a larger one."""
+        def __init__(self):
+            super().__init__("cpu")
+            self.reads = 0
+
+        def __getattribute__(self, name):
+            if name != "buf" or "reads" not in super().__getattribute__("__dict__"):
+                return super().__getattribute__(name)
+            self.reads += 1
+            return torch.zeros(256 * self.reads, dtype=torch.uint8)
+
+    w = Racing()
+    buf, size = w.get(100)
+    assert buf.numel() == size
