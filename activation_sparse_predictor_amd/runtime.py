@@ -452,8 +452,12 @@ def kv_attend(cache: dict, q: torch.Tensor, batch: dict, y: Optional[torch.Tenso
     st = _raw_stream(dev)
     scale = d ** -0.5 if scale is None else float(scale)
     window = _window(window)
-    _attend_with(lambda ws, size: B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, ws, size, st), b, heads, c.n_kv, d, q.device,
-                 st, ws, "pi_kv_attend")
+    ws, size, own = _attend_ws(ws, b, heads, c, q.device, dev, st)
+    status = B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, ws, size, st)
+    if status == B.PI_ERR_WORKSPACE and own is not None:   # too small for these sizes: nothing was launched
+        ws, size = own.get(B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, d))
+        status = B.pi_kv_attend(c, b, q, qs, heads, scale, window, y, lse, ws, size, st)
+    B.check(status, "pi_kv_attend")
     return y
 
 
@@ -461,31 +465,25 @@ def _window(window) -> int:
     return min(max(int(window), -1), 2 ** 31 - 1)   # (ctypes would drop what lies above 32 bits)
 
 
-def _attend_with(call, b, heads: int, n_kv: int, d: int, device, st: int, ws: Optional[torch.Tensor], name: str) -> None:
-    """call(workspace, bytes) on the caller's workspace or on one of this module's."""
+def _attend_ws(ws: Optional[torch.Tensor], b, heads: int, c, device, dev: int, st: int):
+    """The caller's workspace or one of this module's, its bytes, and the keeper that can grow it if it is too small."""
     if ws is not None:
-        _need(ws.device == device and ws.is_contiguous(), "ws must be contiguous and on q's device")
-        B.check(call(ws, ws.numel() * ws.element_size()), name)
-        return
+        _need(ws.get_device() == dev and ws.is_contiguous(), "ws must be contiguous and on q's device")
+        return ws, ws.numel() * ws.element_size(), None
     if _capturing():
         # A graph's workspace is its alone: what other captures or eager calls on
         # this stream do is not replayed with it, and a kept buffer may be
         # replaced by a larger one.  The capture's pool holds the memory as long
         # as the graph lives and gives it to later allocations of the capture.
-        size = B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, n_kv, d)
+        size = B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, c.d)
         ws = torch.empty(size, dtype=_U8, device=device)
         ws[:B.PI_KV_WS_ZERO_BYTES].zero_()
-        B.check(call(ws, size), name)
-        return
-    key = (device.index, st)
-    own = _KV_WS.get(key)
+        return ws, size, None
+    own = _KV_WS.get((dev, st))
     if own is None:
-        own = _KV_WS[key] = Workspace(device)
+        own = _KV_WS[(dev, st)] = Workspace(device)
     buf = own.buf   # (read once: another thread may replace it by a larger one)
-    status = call(buf, 0 if buf is None else buf.numel())
-    if status == B.PI_ERR_WORKSPACE:   # too small for these sizes: nothing was launched
-        status = call(*own.get(B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, n_kv, d)))
-    B.check(status, name)
+    return buf, 0 if buf is None else buf.numel(), own
 
 
 def kv_tree(parents, device="cuda") -> dict:
@@ -541,8 +539,13 @@ def kv_attend_tree(cache: dict, q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     st = _raw_stream(dev)
     scale = d ** -0.5 if scale is None else float(scale)
     window = _window(window)
-    _attend_with(lambda ws, size: B.pi_kv_attend_tree(c, b, q, qs, heads, k, ks, v, vs, mask, mask.shape[1], pos, scale, window, y, lse,
-                                                      ws, size, st), b, heads, c.n_kv, d, q.device, st, ws, "pi_kv_attend_tree")
+    ws, size, own = _attend_ws(ws, b, heads, c, q.device, dev, st)
+    words = mask.shape[1]
+    status = B.pi_kv_attend_tree(c, b, q, qs, heads, k, ks, v, vs, mask, words, pos, scale, window, y, lse, ws, size, st)
+    if status == B.PI_ERR_WORKSPACE and own is not None:
+        ws, size = own.get(B.pi_kv_workspace_size(b.n_seq, b.n_tok, b.max_q, heads, c.n_kv, d))
+        status = B.pi_kv_attend_tree(c, b, q, qs, heads, k, ks, v, vs, mask, words, pos, scale, window, y, lse, ws, size, st)
+    B.check(status, "pi_kv_attend_tree")
     return y
 
 
