@@ -295,6 +295,18 @@ pi_status check_draft(const pi::KvDraft& t, const pi::KvCache& c, const pi::KvBa
     return PI_OK;
 }
 
+// What a call reads or writes of an array.
+struct Span {
+    const char* name;
+    const void* at;
+    size_t bytes;
+};
+pi_status check_apart(const Span& a, const Span& b) {
+    const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+    PI_REQUIRE(a.bytes == 0 || b.bytes == 0 || x + a.bytes <= y || y + b.bytes <= x, PI_ERR_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+    return PI_OK;
+}
+
 pi_status check_verify_sizes(int n_seq, int n_tok, int vocab) {
     PI_TRY(check_kv_counts(n_seq, n_tok, 1));
     PI_REQUIRE(vocab >= 1 && vocab <= PI_VERIFY_MAX_VOCAB, PI_ERR_INVALID_ARG, "vocab=%d outside [1, %d]", vocab,
@@ -1033,7 +1045,19 @@ pi_status pi_verify(int n_seq, int n_tok, int vocab, const int32_t* q_start, con
                (long long)p_stride, vocab);
     PI_REQUIRE(!q || (q_stride >= vocab && q_stride <= far), PI_ERR_INVALID_ARG, "q_stride=%lld is below vocab=%d or out of range",
                (long long)q_stride, vocab);
-    PI_TRY(check_ws(ws, ws_bytes, pi::verify_bytes(n_seq, n_tok, vocab), "pi_verify"));
+    const size_t need = pi::verify_bytes(n_seq, n_tok, vocab);
+    PI_TRY(check_ws(ws, ws_bytes, need, "pi_verify"));
+    // A sequence's results are written while other sequences' inputs are still read.
+    const size_t seqs = (size_t)n_seq * 4, tok = (size_t)n_tok * 4;
+    const Span in[] = {{"q_start", q_start, seqs + 4}, {"ctx", ctx, seqs}, {"tokens", tokens, tok}, {"parent", parent, tok},
+                       {"p", p, ((size_t)(n_tok - 1) * p_stride + vocab) * 4}, {"q", q, q ? ((size_t)(n_tok - 1) * q_stride + vocab) * 4 : 0},
+                       {"u", u, tok}, {"u_next", u_next, seqs}};
+    const Span out[] = {{"rows", rows, tok}, {"start", start, seqs + 4}, {"new_ctx", new_ctx, seqs}, {"next", next, seqs}, {"ws", ws, need}};
+    for (const Span& o : out) {
+        for (const Span& i : in)
+            if (!(o.at == i.at && o.at == new_ctx && i.at == ctx)) PI_TRY(check_apart(o, i));   // (ctx in place: one thread reads and writes each)
+        for (const Span* other = out; other != &o; ++other) PI_TRY(check_apart(o, *other));
+    }
     ws_forget(ws);
     pi::VerifyArgs A{n_seq, n_tok, vocab, q_start, ctx, tokens, parent, p, q, p_stride, q_stride, u, u_next, rows, start, new_ctx,
                      next, 0, 0, 0};

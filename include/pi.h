@@ -746,9 +746,14 @@ pi_status pi_kv_attend_tree(const pi_kv_cache* cache, const pi_kv_batch* batch,
  * new_ctx are the batch for pi_kv_append_rope, and rows its list.  A sequence
  * without rows: none, ctx[s], next -1.
  * ws: pi_verify_workspace_size() bytes, 256-byte aligned; it need not be zeroed.
+ * Until the call's work is done it is that call's alone: calls that host threads queue
+ * on one stream at the same time need one each.
+ * The outputs and ws lie outside the inputs' spans and apart from each other, but
+ * new_ctx may be ctx itself.
  *
  * Errors: INVALID_ARG for NULL pointers, n_seq outside [1, PI_KV_MAX_SEQ], n_tok
- * outside [1, PI_KV_MAX_TOKENS], vocab outside [1, PI_VERIFY_MAX_VOCAB], strides below vocab;
+ * outside [1, PI_KV_MAX_TOKENS], vocab outside [1, PI_VERIFY_MAX_VOCAB], strides below vocab,
+ * overlaps;
  * UNSUPPORTED for misalignment (4 bytes); WORKSPACE.
  */
 #define PI_VERIFY_MAX_VOCAB (1 << 24)
