@@ -9,6 +9,7 @@
 #include <cstdio>
 #include <mutex>
 #include <numeric>
+#include <tuple>
 #include <unordered_map>
 #include <vector>
 
@@ -1014,6 +1015,11 @@ pi_status pi_kv_append_rope(const pi_kv_cache* cache, const pi_kv_batch* batch, 
         PI_TRY(check_stride(q_stride, (int64_t)n_head * c.d, "q_stride"));
         PI_TRY(check_stride(out_stride, (int64_t)n_head * c.d, "out_stride"));
         PI_TRY(check_rotated(q, q_stride, q_out, out_stride, b.n_tok, (int64_t)n_head * c.d));
+        // the queries are written beside the workgroups that read keys and values
+        for (const auto& x : {std::make_tuple("k", k, k_stride), std::make_tuple("v", v, v_stride)})
+            PI_REQUIRE(!pi::rows_meet((uintptr_t)q_out, 2 * out_stride, 2 * (int64_t)n_head * c.d, b.n_tok, (uintptr_t)std::get<1>(x),
+                                      2 * std::get<2>(x), 2 * (int64_t)c.n_kv * c.d, b.n_tok),
+                       PI_ERR_INVALID_ARG, "q_out overlaps %s", std::get<0>(x));
     }
     hipError_t e = pi::launch_kv_append_rope(
         c, b, rope ? &r : nullptr, rows, n_src, reinterpret_cast<const pi::h16*>(k), k_stride, reinterpret_cast<const pi::h16*>(v),

@@ -310,6 +310,26 @@ struct Rope {
     const uint64_t* turns;
 };
 
+// Whether any of n rows of `row` bytes, `stride` apart from a on, meets one of m rows of
+// `other`, `step` apart from b on (rows of one set do not meet each other).
+inline bool rows_meet(uintptr_t a, int64_t stride, int64_t row, int64_t n, uintptr_t b, int64_t step, int64_t other, int64_t m) {
+    const int64_t off = (int64_t)(b - a);   // below 2^61: addresses, and checked strides
+    if (off >= (n - 1) * stride + row || -off >= (m - 1) * step + other) return false;
+    auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+    if (stride == step) {   // slices of one projection's rows: row j of b lies against rows k + j and k + j + 1 of a
+        const int64_t k = floor_div(off, stride), in = off - k * stride;
+        auto some = [&](int64_t shift) { return -shift <= m - 1 && shift <= n - 1; };   // a j with both rows there
+        return (in < row && some(k)) || (in + other > stride && some(k + 1));
+    }
+    for (int64_t i = 0; i < n; ++i) {
+        const int64_t at = i * stride - off;   // of the row, from b on
+        int64_t lo = floor_div(at - other, step) + 1, hi = floor_div(at + row - 1, step);
+        lo = lo > 0 ? lo : 0, hi = hi < m - 1 ? hi : m - 1;
+        if (lo <= hi) return true;
+    }
+    return false;
+}
+
 // rope.hip
 hipError_t launch_rotate(const Rope& R, const int32_t* pos, int n_tok, const h16* x, long long x_stride, int n_head, int d,
                          h16* y, long long y_stride, hipStream_t s);

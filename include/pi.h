@@ -665,14 +665,14 @@ pi_status pi_rotate(const pi_rope* rope, const int32_t* pos, int n_tok, int n_he
  *    batch's last row (q_start[n_seq]) are not read: pi_verify's results go in as they are.
  *  - q (may be NULL): n_tok rows of n_head heads of d, q_stride apart, turned by
  *    the positions of the batch's rows, as pi_rotate does, into q_out
- *    (out_stride apart; q itself with q's stride, or memory outside its span,
- *    and not k or v).  Rows that belong to no sequence are left as they were.
- *    Needs rope, and rows NULL.
+ *    (out_stride apart; q itself with q's stride, or memory outside its span;
+ *    no row of k or v, but q, k and v may be slices of one projection).  Rows that
+ *    belong to no sequence are left as they were.  Needs rope, and rows NULL.
  * One launch.
  *
  * Errors: as pi_kv_append and pi_rotate; INVALID_ARG for n_src below 1 (or
  * below n_tok without rows) or above PI_KV_MAX_TOKENS, q without q_out or rope
- * or with rows, n_head not a multiple of n_kv.
+ * or with rows, n_head not a multiple of n_kv, a row of q_out that overlaps one of k or v.
  */
 pi_status pi_kv_append_rope(const pi_kv_cache* cache, const pi_kv_batch* batch, const pi_rope* rope,
                             const int32_t* rows, int n_src, const pi_half* k, int64_t k_stride,
