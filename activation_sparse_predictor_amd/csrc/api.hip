@@ -315,6 +315,31 @@ pi_status check_verify_sizes(int n_seq, int n_tok, int vocab) {
     return PI_OK;
 }
 
+// f / (2 pi) mod 1 in units of 2^-64, to the nearest, for f in [0, 2^20].  In integers:
+// the whole turns of a quotient in floating point take the place of its last bits.
+uint64_t turns_of(double f) {
+    constexpr uint64_t kInv[3] = {0x36D8A5664F10E410u, 0x7F09D5F47D4D3770u, 0x28BE60DB9391054Au};   // 2^192 / (2 pi) without its fraction
+    int e;
+    const uint64_t digits = (uint64_t)std::ldexp(std::frexp(f, &e), 53);   // f = digits 2^(e - 53)
+    if (digits == 0) return 0;
+    uint64_t x[5] = {0, 0, 0, 0, 0};   // digits * 2^192 / (2 pi), low by less than digits
+    unsigned __int128 carry = 0;
+    for (int i = 0; i < 3; ++i) {
+        carry += (unsigned __int128)digits * kInv[i];
+        x[i] = (uint64_t)carry;
+        carry >>= 64;
+    }
+    x[3] = (uint64_t)carry;
+    // the result starts at bit 128 - (e - 53), 160 at least: what x is low by is 2^-107 of its unit at most
+    const int at = 181 - e;
+    if (at > 256) return 0;
+    const int word = at / 64, bit = at % 64;
+    uint64_t v = word < 4 ? x[word] >> bit : 0;
+    if (bit > 0 && word < 3) v |= x[word + 1] << (64 - bit);
+    const int below = at - 1;
+    return v + (x[below / 64] >> (below % 64) & 1u);   // 2^64 is a whole turn, 0
+}
+
 // A rotary plan for heads of d, checked and turned into the kernels' own.
 pi_status check_rope(const pi_rope* r, int d, pi::Rope* out) {
     PI_REQUIRE(r != nullptr, PI_ERR_INVALID_ARG, "rope is NULL");
@@ -962,11 +987,7 @@ pi_status pi_rope_turns(const double* freqs, int n, uint64_t* turns) {
     PI_REQUIRE(n >= 1, PI_ERR_INVALID_ARG, "n=%d must be positive", n);
     for (int m = 0; m < n; ++m)
         PI_REQUIRE(freqs[m] >= 0.0 && freqs[m] <= 0x1p20, PI_ERR_INVALID_ARG, "frequency %d is %g, not in [0, 2^20]", m, freqs[m]);
-    for (int m = 0; m < n; ++m) {
-        const long double t = (long double)freqs[m] / 6.283185307179586476925286766559L, part = t - floorl(t);
-        const long double v = roundl(part * 0x1p64L);
-        turns[m] = v >= 0x1p64L ? 0 : (uint64_t)v;
-    }
+    for (int m = 0; m < n; ++m) turns[m] = turns_of(freqs[m]);
     return ok();
 }
 

@@ -4,6 +4,7 @@ pi_kv_attend_tree, pi_verify): plain numpy in float64, one row, block or token
 at a time."""
 
 import math
+from fractions import Fraction
 
 import numpy as np
 
@@ -14,6 +15,23 @@ def pairs(layout, rot):
     """The two dimensions of each pair."""
     m = np.arange(rot // 2)
     return (m, m + rot // 2) if layout == "half" else (2 * m, 2 * m + 1)
+
+
+def turns(f):
+    """f / (2 pi) mod 1 in units of 2^-64, to the nearest, from a double f: in rationals, pi from Machin's series."""
+    one = 1 << 400
+
+    def arctan_inverse(x):
+        total, term, n = 0, one // x, 1
+        while term:
+            total += term // n if n % 4 == 1 else -(term // n)
+            term //= x * x
+            n += 2
+        return total
+
+    tau = Fraction(8 * (4 * arctan_inverse(5) - arctan_inverse(239)), one)
+    units = Fraction(f) / tau * 2 ** 64
+    return math.floor(units + Fraction(1, 2)) % 2 ** 64
 
 
 def rotate(x, pos, freqs, layout="half", gain=1.0):
