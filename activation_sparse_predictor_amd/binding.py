@@ -49,11 +49,13 @@ PI_ROPE_PLAIN = 0
 PI_ROPE_LINEAR = 1
 PI_ROPE_NTK = 2
 PI_ROPE_YARN = 3
+PI_ROPE_YARN_INDEX = 5
 PI_VERIFY_MAX_VOCAB = 1 << 24
 PI_KV_MAX_TREE = 256
 
 ROPE_LAYOUTS = {"half": PI_ROPE_HALF, "pairs": PI_ROPE_PAIRS}
-ROPE_SCALINGS = {"none": PI_ROPE_PLAIN, "linear": PI_ROPE_LINEAR, "ntk": PI_ROPE_NTK, "yarn": PI_ROPE_YARN}
+ROPE_SCALINGS = {"none": PI_ROPE_PLAIN, "linear": PI_ROPE_LINEAR, "ntk": PI_ROPE_NTK, "yarn": PI_ROPE_YARN,
+                 "yarn-index": PI_ROPE_YARN_INDEX}
 KV_FMTS = {"int8": PI_KV_INT8, "fp8": PI_KV_FP8}
 KINDS = {"relu": PI_FFN_RELU, "reglu": PI_FFN_REGLU, "swiglu": PI_FFN_SWIGLU}
 ACTS = {"relu": PI_ACT_RELU, "none": PI_ACT_NONE}

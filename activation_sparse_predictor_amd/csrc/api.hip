@@ -959,26 +959,32 @@ pi_status pi_rope_frequencies(int rot, double base, int scaling, double factor, 
     PI_REQUIRE(freqs && gain, PI_ERR_INVALID_ARG, "NULL pointer argument");
     PI_REQUIRE(rot >= 2 && rot % 2 == 0, PI_ERR_INVALID_ARG, "rot=%d is not an even positive number", rot);
     PI_REQUIRE(std::isfinite(base) && base > 1.0, PI_ERR_INVALID_ARG, "base=%g must be above 1", base);
-    PI_REQUIRE(scaling >= PI_ROPE_PLAIN && scaling <= PI_ROPE_YARN, PI_ERR_INVALID_ARG, "scaling=%d unknown", scaling);
+    const bool by_index = scaling == PI_ROPE_YARN_INDEX, by_pair = by_index || scaling == PI_ROPE_YARN;
+    PI_REQUIRE((scaling >= PI_ROPE_PLAIN && scaling <= PI_ROPE_YARN) || by_index, PI_ERR_INVALID_ARG, "scaling=%d unknown", scaling);
     PI_REQUIRE(scaling == PI_ROPE_PLAIN || (std::isfinite(factor) && factor >= 1.0), PI_ERR_INVALID_ARG,
                "factor=%g must be at least 1", factor);
-    if (scaling == PI_ROPE_YARN) {
+    if (by_pair) {
         PI_REQUIRE(std::isfinite(trained) && trained >= 1.0, PI_ERR_INVALID_ARG, "trained=%g must be at least 1", trained);
         PI_REQUIRE(std::isfinite(fast) && slow >= 0.0 && slow < fast, PI_ERR_INVALID_ARG, "slow=%g and fast=%g: not 0 <= slow < fast",
                    slow, fast);
     }
     const double tau = 6.283185307179586476925287;
     if (scaling == PI_ROPE_NTK && rot > 2) base *= std::pow(factor, rot / (rot - 2.0));
+    // the numbers of the pairs between which the blend falls
+    auto turning = [&](double n) { return n > 0.0 ? rot * std::log(trained / (tau * n)) / (2.0 * std::log(base)) : (double)rot; };
+    const double from = by_index ? std::max(0.0, std::floor(turning(fast))) : 0.0;
+    const double to = by_index ? std::max(from + 0.001, std::min(rot - 1.0, std::ceil(turning(slow)))) : 1.0;
     for (int m = 0; m < rot / 2; ++m) {
         double f = std::pow(base, -2.0 * m / rot);
         if (scaling == PI_ROPE_LINEAR) f /= factor;
-        if (scaling == PI_ROPE_YARN) {
-            const double c = std::min(1.0, std::max(0.0, (trained * f / tau - slow) / (fast - slow)));
+        if (by_pair) {
+            const double own = by_index ? 1.0 - (m - from) / (to - from) : (trained * f / tau - slow) / (fast - slow);
+            const double c = std::min(1.0, std::max(0.0, own));
             f = (1.0 - c) * f / factor + c * f;
         }
         freqs[m] = f;
     }
-    *gain = scaling == PI_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    *gain = by_pair ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
     return ok();
 }
 

@@ -557,10 +557,13 @@ def rope(rot: int, base: float = 10000.0, layout: str = "half", scaling: str = "
          trained: float = 4096.0, slow: float = 1.0, fast: float = 32.0, freqs=None, gain: Optional[float] = None,
          device="cuda") -> dict:
     """A rotary plan for the first rot dimensions of a head: pi_rope_frequencies'
-    (scaling "none", "linear", "ntk" or "yarn"), or the caller's own freqs
-    (rot / 2 radians a position) and gain."""
+    (scaling "none", "linear", "ntk", "yarn", blended by each pair's turns as that
+    method's paper words it, or "yarn-index", blended by the pair's number as the
+    model code released with it does: what checkpoints stretched by that code
+    need), or the caller's own freqs (rot / 2 radians a position) and gain, for
+    a model stretched in any other way."""
     import numpy as np
-    _need(layout in B.ROPE_LAYOUTS and scaling in B.ROPE_SCALINGS, "layout is 'half' or 'pairs', scaling 'none', 'linear', 'ntk' or 'yarn'")
+    _need(layout in B.ROPE_LAYOUTS and scaling in B.ROPE_SCALINGS, "layout is 'half' or 'pairs', scaling 'none', 'linear', 'ntk', 'yarn' or 'yarn-index'")
     if freqs is None:
         freqs, own = B.pi_rope_frequencies(int(rot), float(base), B.ROPE_SCALINGS[scaling], float(factor), float(trained),
                                            float(slow), float(fast))

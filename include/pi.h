@@ -604,10 +604,18 @@ typedef enum pi_rope_scaling {
     PI_ROPE_PLAIN = 0,   /* f_m = base^(-2 m / rot) */
     PI_ROPE_LINEAR = 1,  /* f_m / factor: positions as if they were factor times closer */
     PI_ROPE_NTK = 2,     /* base times factor^(rot / (rot - 2)) (rot = 2: base): the slowest pair is stretched by factor, the fastest kept */
-    PI_ROPE_YARN = 3     /* each pair between its own and the linear frequency, by its turns n over
+    PI_ROPE_YARN = 3,    /* each pair between its own and the linear frequency, by its turns n over
                             the trained length: own from n = fast on, linear up to n = slow,
                             in between (1 - c) f / factor + c f with c = (n - slow) / (fast - slow);
                             gain = 0.1 ln(factor) + 1 */
+    PI_ROPE_YARN_INDEX = 5 /* the same, but c falls evenly with the pair's number m, from 1 at a to 0 at b:
+                            c = 1 - (m - a) / (b - a), kept in [0, 1], where with
+                            i(n) = rot ln(trained / (2 pi n)) / (2 ln base), the number of the pair that turns n times,
+                            a = max(0, floor(i(fast))), b = max(a + 0.001, min(rot - 1, ceil(i(slow)))) */
+    /* The two differ by up to a factor of 2 or more in the pairs between.  PI_ROPE_YARN is the
+       method as its paper words it; the model code released with it, and checkpoints
+       trained or tuned by that code, go by the pair's number.  A model stretched in yet
+       another way brings its own frequencies to pi_rope_turns. */
 } pi_rope_scaling;
 
 typedef struct pi_rope {    /* read by the host during the call */
@@ -619,8 +627,8 @@ typedef struct pi_rope {    /* read by the host during the call */
 
 /*
  * pi_rope_frequencies -- HOST-ONLY frequencies (host, rot / 2 doubles) and gain (host).
- * trained (tokens), slow and fast (turns, usually 1 and 32) are PI_ROPE_YARN's; the
- * others ignore them.  factor is ignored by PI_ROPE_PLAIN.
+ * trained (tokens), slow and fast (turns, usually 1 and 32) are PI_ROPE_YARN's and
+ * PI_ROPE_YARN_INDEX's; the others ignore them.  factor is ignored by PI_ROPE_PLAIN.
  * Errors: INVALID_ARG for NULL pointers, an odd or non-positive rot, base not finite or
  * not above 1, an unknown scaling, factor below 1, trained < 1, or not 0 <= slow < fast.
  *

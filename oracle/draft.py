@@ -56,6 +56,13 @@ def frequencies(rot, base=10000.0, scaling="none", factor=1.0, trained=4096.0, s
         return np.array(own), 1.0
     if scaling == "linear":
         return np.array([f / factor for f in own]), 1.0
+    if scaling == "yarn-index":
+        def pair(n):   # the (fractional) number of the pair that turns n times over the trained length: trained base^(-2 i / rot) = 2 pi n
+            return rot / 2 * math.log(trained / (2 * math.pi * n), base) if n else rot
+        a = max(0, math.floor(pair(fast)))
+        b = max(a + 0.001, min(rot - 1, math.ceil(pair(slow))))
+        blend = [f / factor + min(1.0, max(0.0, (b - m) / (b - a))) * (f - f / factor) for m, f in enumerate(own)]
+        return np.array(blend), 0.1 * math.log(factor) + 1.0
     out = []
     for f in own:
         n = trained * f / (2 * math.pi)   # turns over the trained length
