@@ -666,7 +666,8 @@ pi_status pi_rotate(const pi_rope* rope, const int32_t* pos, int n_tok, int n_he
  * finite), with three additions:
  *  - rope (may be NULL: none): keys are turned by their cache position before they are
  *    quantised.  They stay in fp32 in between: a code is what the rotation in
- *    fp32 gives, without a rounding to fp16.
+ *    fp32 gives, without a rounding to fp16.  A turned key beyond fp16's largest number
+ *    is attended to as it is; pi_kv_read gives it as infinity.
  *  - rows (device, may be NULL): row i of the batch is row rows[i] of k and v,
  *    which hold n_src rows; an entry outside [0, n_src) counts as a value that is not
  *    finite.  NULL: row i itself (n_src >= n_tok).  Entries past the
@@ -713,7 +714,8 @@ pi_status pi_kv_append_rope(const pi_kv_cache* cache, const pi_kv_batch* batch, 
  * Both together under one softmax, in pi_kv_attend's precision; a row that
  * attends to nothing gets y = 0, lse = -infinity.  Drafted tokens that a row does
  * not attend to may hold anything, NaN included; a drafted value that is not
- * finite makes the whole heads that attend to its token NaN.  max_q is at most 64 words.
+ * finite makes the whole heads that attend to its token NaN.  max_q is at most 64
+ * words.  y and lse lie outside k, v, mask, pos and the cache.
  *
  * Errors: as pi_kv_attend; INVALID_ARG for words outside [1, PI_KV_MAX_TREE /
  * 64], max_q above 64 words, k, v or mask NULL, pos NULL under a window;
