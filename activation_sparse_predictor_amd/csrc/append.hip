@@ -13,6 +13,11 @@
 // page -> scale beside list -> rows and angles, then the block's maximum and the codes:
 // one token of 56 heads 6.7 us (without rotation and queries 5.0), 64 sequences of
 // 64 query and 8 kv heads 8.9, the accepted rows of 48 trees 6.7.
+//
+// The half layout with rot not a multiple of 32 (heads of 80 turned whole) works out
+// every angle twice and reads a pair's other half in single loads: keys and values of
+// four prompts of 2048 tokens of 32 heads of 80 take 103 us, where the pairs layout
+// takes 71, heads of 96 65 and heads that are not turned 50; single tokens take the same.
 #include "kv.hpp"
 #include "rope.hpp"
 

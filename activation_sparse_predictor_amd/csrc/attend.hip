@@ -32,7 +32,9 @@
 // tenth of the time.
 //
 // A chain of 8 drafted tokens behind 128 cached ones, 56 heads: 9.3 us; 4 of 4 rows of 64
-// heads, 8 kv, on 16384 tokens (134 MB) 41, where the rows as a chain in the cache take 39;
+// heads, 8 kv, on 16384 tokens (134 MB) 40, as the rows as a chain in the cache do.  Of those
+// 10-12 are start and end (13 on 256 tokens); in between each key is read by two items of 16 rows,
+// 4.5 TB/s of keys (9 with the second reading, from L2).  With 2 rows, one item: 33 us, 6.7 TB/s.
 // 16 of 4 rows of 64 heads of 64 up to 8000 tokens 29.5 (28.5).  The drafted rows' values come
 // as pairs of dimensions; with the cached codes read in the pairs' order too, half a
 // line an instruction, these took 48 and 34.

@@ -49,8 +49,9 @@ struct AttArgs {
 // Attention of drafted tokens (pi_kv_attend_tree): every row sees the cached
 // tokens, all ctx of them or, under a window, those above its own position less
 // the window, and the drafted rows that its mask names.  The drafted rows are
-// further tiles of 64 keys, before the cached ones: their loads are under way
-// while the cached granules are looked up.
+// further tiles of 64 keys, before the cached ones.  In attend.hip their loads are
+// under way while the cached granules are looked up; prompt.hip looks up first,
+// then loads, stores and multiplies one drafted tile after the other.
 struct TreeArgs : AttArgs {
     const h16 *tk, *tv;            // drafted keys and values: n_tok rows
     long long tk_stride, tv_stride;

@@ -1,11 +1,13 @@
 // pi_rotate: rotary positions of rows that the caller keeps.
 //
-// Bytes bound it: two in and two out an element, no more than once (2048 tokens of 72
-// heads of 128, 75 MB: 13.4 us, 5.7 TB/s; 8192: 49.7 us, 6.1; a large copy
-// reaches 5.1).  The angles cost some 30 operations a pair, which is why four
-// heads share them.  The pairs layout, whose thread has 16 neighbouring
-// dimensions, takes 15.1 and 54 us there (with eight, half the angles a thread
-// reads together: 17.3 and 63).  One token of 56 heads: 2.7 us, a launch.
+// Bytes bound it: two in and two out an element, no more than once.  2048 tokens of 72
+// heads of 128, 75 MB: 13.1 us over the same buffers again, which the last-level cache
+// serves in part (a copy of as many bytes: 11.4), 17.4 through 3 GB of buffers in turn
+// (copy: 16.2).  8192 tokens: 49.5 and 54.8 us (copy 57).  The angles cost some 30
+// operations a pair, which is why four heads share them.  The pairs layout, whose
+// thread has 16 neighbouring dimensions, takes 14.8 and 19.6 us for 2048 tokens, 53.8 and
+// 56.9 for 8192 (with eight, half the angles a thread reads together: 17.3 and 63 over
+// the same buffers).  One token of 56 heads: 2.7 us, a launch.
 #include "rope.hpp"
 
 namespace pi {

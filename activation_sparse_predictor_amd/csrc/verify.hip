@@ -18,13 +18,17 @@
 // its end, a wave a slice of the vocabulary; a sequence's workgroup that is done
 // last finds the slice and the element in it.
 //
-// What bounds it: latency.  The second launch is a chain (where the walk ended, the
-// row, the sums written through, the arrival, the sums back, the slice's elements)
-// of 10.4 us for one sequence of 32000 tokens and 12.9 for 48 of 50257 (19 MB, 4 us at a
-// copy's rate); the walk takes 1.9 us where no sum is asked for, 25 us where
-// the longest of 48 trees asks for several one after the other, each one pass of a
-// workgroup over both rows (400 KB, some 4 us with eight loads of each a thread under way).
-// A third launch of one workgroup for the search took 2-5 us more.
+// What bounds it: latency, and how the work is divided.  The second launch is a chain
+// (where the walk ended, the row, the sums written through, the arrival, the sums back,
+// the slice's elements) of 10 us for one sequence of 32000 tokens and 12.8 for 48 of
+// 50257 (19 MB, 4 us at a copy's rate).  For fixed proposals (16 sequences, 128000
+// tokens: 13.3 us) its sums add to that single loads with a bit looked up for each, none
+// under way ahead, and three barriers for every four slices.  The walk takes 1.9 us
+// where no sum is asked for, 25 us where the longest of 48 trees asks for several one
+// after the other, each one pass of the sequence's one workgroup over both rows (400 KB,
+// some 4 us with eight loads of each a thread under way) while most of the chip is idle:
+// one workgroup a sequence is this kernel's choice, not the card's bound.  A third
+// launch of one workgroup for the search took 2-5 us more.
 #include "common.hpp"
 #include "internal.hpp"
 #include "pi.h"
