@@ -271,7 +271,8 @@ __global__ __launch_bounds__(kVerThreads) void k_verify_next(VerifyArgs A, Verif
             bounds(i, from, to);
             double v = 0.0;
             if (DRAWN) {
-                if (i < end) v = sum_left<DRAWN, 4>(p, q, s, from, to, lane, kWave);
+                // (no child rejected: q has no part in it, and may hold anything in a row that nothing hangs below)
+                if (i < end) v = s != 0.0 ? sum_left<true, 4>(p, q, s, from, to, lane, kWave) : sum_left<false, 4>(p, nullptr, 0.0, from, to, lane, kWave);
             } else {
                 mark_children(A, row0, n, cur, i0 * A.slice, kVerWaves * A.slice, gone, tid);
                 bool nan = false;
@@ -373,7 +374,7 @@ __global__ __launch_bounds__(kVerThreads) void k_verify_next(VerifyArgs A, Verif
         for (int j = 0; j < 4; ++j) {
             const int i = i0 + tid * 4 + j;
             v[j] = 0.0;
-            if (i < to) v[j] = left_of(p[i], DRAWN ? q[i] : 0.f, s, nan);
+            if (i < to) v[j] = left_of(p[i], DRAWN && s != 0.0 ? q[i] : 0.f, s, nan);
             if (i < to && !whole && taken(i, from)) v[j] = 0.0;
             mine += v[j];
         }

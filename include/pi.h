@@ -743,6 +743,8 @@ pi_status pi_kv_attend_tree(const pi_kv_cache* cache, const pi_kv_batch* batch,
  *   and the walk goes on from it; otherwise P becomes max(P - q, 0) over its sum
  *   and the next child is tried; when none is left,
  *   next[s] = the smallest x with P(0) + .. + P(x) > u_next[s] (P(0) + .. + P(vocab - 1)).
+ * q of a row without rejected children is not part of it, and may hold anything
+ * but for the elements of the tokens below the row.
  * Tokens and what follows them are then distributed as if drawn from p alone
  * (u, u_next: uniform in [0, 1)).  If nothing is left of P (all 0), the
  * row's own p decides; if its sum is 0, infinite or NaN, next[s] = -1.  A

@@ -99,3 +99,40 @@ def test_threads_that_share_a_stream():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -1.0])
+def test_the_draft_of_a_row_without_rejected_children_does_not_matter(value):
+    """A draft model has no distribution for rows that nothing hangs below, and what the target's row gives is its own
+    then: whatever lies in those rows of q, and in all rows once every child stays."""
+    rng = np.random.default_rng(21)
+    c = case(rng, [5, 1, 9, 16], 3001, True)
+    for s in range(4):   # rows without children
+        a, e = int(c["q_start"][s]), int(c["q_start"][s + 1])
+        below = set(c["parent"][a + 1:e].tolist())
+        for j in range(e - a):
+            if j not in below:
+                c["q"][a + j] = value
+    for _ in range(4):
+        c["u"][:] = rng.random(31, dtype=np.float32)
+        c["u_next"][:] = rng.random(4, dtype=np.float32)
+        same(c)
+    c = case(rng, [4, 7], 501, True, chain=True)
+    c["u"][:] = 0.0    # every child stays
+    c["q"][:] = np.float32(value)
+    for s, n in ((0, 4), (4, 7)):
+        for j in range(1, n):
+            c["q"][s + j - 1, c["tokens"][s + j]] = 0.25
+    want = same(c)
+    assert want[1] == [0, 4, 11] and min(want[3]) >= 0
+
+
+def test_nothing_left_beside_an_endless_draft():
+    """An infinite element of q takes its token away; where nothing is left the row's own p decides, that token's included."""
+    c = dict(q_start=np.array([0, 2], np.int32), ctx=np.array([3], np.int32), tokens=np.array([0, 5], np.int32),
+             parent=np.array([-1, 0], np.int32), p=np.zeros((2, 40), np.float32), q=np.zeros((2, 40), np.float32),
+             u=np.array([0.0, 0.5], np.float32), u_next=np.array([0.5], np.float32))
+    c["p"][0, 30] = 1.0
+    c["q"][0, 30] = np.inf
+    c["q"][0, 5] = 0.5    # the child's, of probability 0: rejected
+    assert same(c)[3] == [30]
