@@ -20,8 +20,8 @@
 //
 // What bounds it: latency, and how the work is divided.  The second launch is a chain
 // (where the walk ended, the row, the sums written through, the arrival, the sums back,
-// the slice's elements) of 10 us for one sequence of 32000 tokens and 12.8 for 48 of
-// 50257 (19 MB, 4 us at a copy's rate).  For fixed proposals (16 sequences, 128000
+// the slice's elements) of 10 us for one sequence of 32000 tokens and 11.7 for 48 of
+// 50257 (9.6 MB of p, and of q where a child was rejected).  For fixed proposals (16 sequences, 128000
 // tokens: 13.3 us) its sums add to that single loads with a bit looked up for each, none
 // under way ahead, and three barriers for every four slices.  The walk takes 1.9 us
 // where no sum is asked for, 25 us where the longest of 48 trees asks for several one
@@ -42,7 +42,7 @@ constexpr int kVerStep = 4 * kVerThreads, kVerMaxSlices = 1024, kVerMaxSlice = P
 // Workgroups of the second launch.  Each is one more arrival on its sequence's
 // counter, and arrivals on one cache line wait for each other: with a workgroup
 // a slice and the counters side by side 48 sequences of 50257 tokens (2400
-// workgroups) took 31 us, so (336) they take 12.5.
+// workgroups) took 31 us, so (336) they took 12.5, q read for all.
 constexpr int kVerBlocks = 512, kVerCtrStride = 32;
 
 struct VerifyWs {   // kept between the two kernels
